@@ -11,6 +11,9 @@ Functions (see include/fq.h for the exact definitions and the pages each one fol
     rmsnorm_rope_quant(x, w, cos, sin, eps, fp8_max, want_y)  -> (y | None, q, scale)
     qk_norm_rope_quant(qk, wq, wk, cos, sin, Hq, Hk, ...)     -> (q, scale)
     rmsnorm_bwd(x, w, grad_y, eps)                            -> (dx, dw, dw_f32)
+    fp8_matmul(a, a_scale, b, b_scale)                        -> out (block-scaled FP8 matrix product)
+    qkv_norm_rope_append(qkv, ..., slots, k_cache, ...)       -> (q, q_scale), K and V into a paged cache
+    paged_attention(q, q_scale, k_cache, ..., seq_lens)       -> (out, lse | None)
     RMSNormFunction / rmsnorm: autograd wrapper (forward and backward both in libfq)
 fp8 outputs are torch.uint8 tensors of e4m3fn codes (``.view(torch.float8_e4m3fn)`` reinterprets).
 """
@@ -21,12 +24,14 @@ import ctypes
 import torch
 
 from . import _capi
+from .serving import fp8_matmul, paged_attention, paged_attention_workspace_bytes, qkv_norm_rope_append
 
 __all__ = ["layernorm_fwd", "rmsnorm_fwd", "rmsnorm_fwd_rstd", "rmsnorm_bwd_rstd", "rmsnorm_rope", "rmsnorm_rope_quant", "rmsnorm_rope_quant_groups", "qk_norm_rope_quant", "qk_norm_rope_quant_blocks",
            "rmsnorm_bwd",
            "rmsnorm_bwd_workspace_bytes", "rmsnorm", "RMSNormFunction", "device_status", "check_bounded_wait",
            "set_strict",
-           "stream_floor", "FqError"]
+           "stream_floor", "FqError",
+           "fp8_matmul", "qkv_norm_rope_append", "paged_attention", "paged_attention_workspace_bytes"]
 
 FqError = _capi.FqError
 

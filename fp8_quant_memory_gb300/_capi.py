@@ -16,6 +16,15 @@ FQ_BF16, FQ_FP16, FQ_FP32 = 0, 1, 2
 
 _vp, _i64, _int, _f32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 
+
+class PagedCache(ctypes.Structure):
+    """fq_paged_cache: pointers, sizes and strides of a paged FP8 cache."""
+
+    _fields_ = ([(n, _vp) for n in ("k", "v", "k_scale", "v_scale")] +
+                [(n, _i64) for n in ("pages", "page_size", "page_stride", "head_stride", "token_stride",
+                                     "scale_page_stride", "scale_head_stride", "scale_token_stride")])
+
+
 # name -> (restype, argtypes), mirroring include/fq.h
 SIGNATURES = {
     "fq_last_error": (ctypes.c_char_p, []),
@@ -39,6 +48,12 @@ SIGNATURES = {
     "fq_rmsnorm_bwd_workspace_bytes": (_sz, [_i64, _i64]),
     "fq_rmsnorm_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i64, _i64, _int, _f32, _vp]),
     "fq_rmsnorm_bwd_rstd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i64, _i64, _int, _vp]),
+    "fq_fp8_matmul": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _int, _vp]),
+    "fq_qkv_norm_rope_append": (_int, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64,
+                                       _i64, _int, _int, _f32, _f32, _vp]),
+    "fq_paged_attention_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
+    "fq_paged_attention": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _i64, _i64, _i64,
+                                  _i64, _i64, _i64, _f32, _int, _vp]),
     "fq_rmsnorm_bwd_noalloc": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _f32, _vp]),
 }
 

@@ -10,6 +10,7 @@
 
 #include "fq.h"
 #include "fq_internal.h"
+#include "fq_serving.h"
 
 namespace {
 
@@ -143,6 +144,12 @@ int set_error(int code, const char* fmt, ...) {
   return rc;
 }
 
+int finish_launch(const char* fn, cudaStream_t s) { return check_launch(fn, s); }
+
+void drop_stale_error() { cudaGetLastError(); }
+
+int succeed() { return ok(); }
+
 int sm_count() {
   static int cache[128] = {0};
   int dev = 0;
@@ -161,7 +168,7 @@ extern "C" {
 
 const char* fq_last_error(void) { return g_err.c_str(); }
 
-int fq_version(void) { return 2; }
+int fq_version(void) { return 3; }
 
 int fq_device_status(unsigned int* word, int clear, cudaStream_t stream) {
   if (word == nullptr) return fail(FQ_ERR_INVALID_ARG, "fq_device_status: word is null");

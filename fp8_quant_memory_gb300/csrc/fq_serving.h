@@ -1,0 +1,78 @@
+// fq_serving.h -- host-side launch interface of the FP8 serving operators: the block-scaled matrix
+// product, the QKV prologue that appends to a paged cache, and paged attention of one new token.
+#pragma once
+
+#include "fq_internal.h"
+
+namespace fq {
+
+constexpr int kScaleBlock = 128;  // columns (and weight rows) per scale of the matrix product
+
+// out[i, j] = dtype(sum_g a_scale[i, g] * b_scale[j / 128, g] * sum_{k in block g} a[i, k] * b[j, k]).
+// Strides are in elements; `groups` = ceil(K / 128).
+struct MatmulArgs {
+  const uint8_t* a;
+  const uint8_t* b;
+  const float* a_scale;
+  const float* b_scale;
+  void* out;
+  int64_t a_stride, b_stride, a_scale_stride, b_scale_stride, out_stride;
+  int64_t M, N, K, groups;
+};
+
+// The cache as the kernels see it: row (page, head, slot) of K starts at k + page*page_stride +
+// head*head_stride + slot*token_stride (bytes: e4m3 codes), its scale likewise with the s_* strides.
+struct CacheView {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t page_stride, head_stride, token_stride;
+  int64_t s_page_stride, s_head_stride, s_token_stride;
+  int64_t pages;
+  int32_t page_size;
+  int32_t page_shift;  // log2(page_size), or -1 when it is no power of two
+};
+
+struct AppendArgs {
+  RowArgs rows;  // x = qkv, H = Hq + 2*Hk, rows = T*H, q and scale = the q outputs
+  const int64_t* slots;
+  CacheView cache;
+  int32_t Hk;
+};
+
+struct PagedArgs {
+  const uint8_t* q;
+  const float* q_scale;
+  int64_t q_stride, q_scale_stride;
+  CacheView cache;
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* lens;
+  void* out;
+  float* lse;  // nullable
+  float* partial;
+  int32_t B, Hq, Hk, D;
+  int64_t max_len;  // lengths are cut to this (the caller's bound and what the page table holds)
+  float scale_log2;  // softmax_scale * log2(e)
+};
+
+// tcgen05 kernels: 16-byte aligned operands and strides. False (nothing launched) otherwise.
+bool launch_matmul_tc(const MatmulArgs& a, int dtype, cudaStream_t s);
+void launch_matmul_scalar(const MatmulArgs& a, int dtype, cudaStream_t s);
+
+bool launch_append_vector(const AppendArgs& a, int dtype, int table_dtype, cudaStream_t s);
+void launch_append_scalar(const AppendArgs& a, int dtype, int table_dtype, cudaStream_t s);
+
+// Partial results of split sequences: what launch_attention_split needs in its workspace.
+size_t attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len);
+bool launch_attention_split(const PagedArgs& a, int dtype, cudaStream_t s);
+void launch_attention_scalar(const PagedArgs& a, int dtype, cudaStream_t s);
+
+// Launch result of an entry point (and the strict-mode check), as every entry point reports it.
+int finish_launch(const char* fn, cudaStream_t s);
+// Drops a stale error that an unrelated earlier call left behind.
+void drop_stale_error();
+int succeed();
+
+}  // namespace fq

@@ -261,6 +261,88 @@ int fq_rmsnorm_bwd_rstd(const void* x, const void* w, const void* grad_y, const 
 int fq_rmsnorm_bwd_noalloc(const void* x, const void* w, const void* grad_y, void* dx, void* dw,
                            float* dw_f32, int64_t M, int64_t N, int dtype, float eps, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------------------------------
+ * FP8 serving operators: what reads the FP8 rows that the entry points above write. The tutorial
+ * pages end at the prologue; these three carry it on: the projection in front of it, the prologue with
+ * its K and V rows placed in a paged cache, and the attention of one new token over that cache.
+ * ------------------------------------------------------------------------------------------------ */
+
+/*
+ * Block-scaled FP8 matrix product, the consumer of fq_rmsnorm_rope_quant_groups with group_size 128:
+ *   out[i, j] = dtype( sum_g a_scale[i, g] * b_scale[j / 128, g] * sum_{k in block g} a[i, k] * b[j, k] )
+ * with blocks g of 128 consecutive k (the last one shorter when 128 does not divide K), every sum in
+ * fp32 and one rounding to dtype. a: [M, K] e4m3 codes, a_scale: [M, ceil(K/128)] fp32; b: [N, K] codes
+ * (a weight stored row by output column), b_scale: [ceil(N/128), ceil(K/128)] fp32, one scale per
+ * 128 x 128 block; out: [M, N] dtype. Rows are contiguous, *_stride elements apart; the strides of what
+ * is only read may be 0. M, N >= 0 (0: no-op), K >= 1.
+ * Operands that are 16-byte aligned with strides that are multiples of 16 take the tensor cores; other
+ * layouts take a scalar kernel with the same results up to the order of the sums.
+ */
+int fq_fp8_matmul(const uint8_t* a, int64_t a_stride, const float* a_scale, int64_t a_scale_stride, const uint8_t* b,
+                  int64_t b_stride, const float* b_scale, int64_t b_scale_stride, void* out, int64_t out_stride,
+                  int64_t M, int64_t N, int64_t K, int dtype, cudaStream_t stream);
+
+/*
+ * A paged FP8 key-value cache: `pages` pages of `page_size` tokens. Token slot o of page p holds, for
+ * key head h, the K row of head_dim codes at k + p*page_stride + h*head_stride + o*token_stride and its
+ * scale at k_scale[p*scale_page_stride + h*scale_head_stride + o*scale_token_stride]; the V row likewise
+ * with v and v_scale and the same strides. Codes of a row are contiguous; strides are in elements and
+ * must keep rows apart, so any order of page, head and token is allowed. All memory is the caller's.
+ */
+typedef struct fq_paged_cache {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t pages, page_size;
+  int64_t page_stride, head_stride, token_stride;
+  int64_t scale_page_stride, scale_head_stride, scale_token_stride;
+} fq_paged_cache;
+
+/*
+ * The prologue of fq_qk_norm_rope_quant on a whole QKV row, with K and V placed in the cache:
+ *   qkv[t*token_stride + h*D + (0..D-1)], heads ordered Hq q heads, Hk k heads, Hk v heads;
+ *   q and k rows as fq_qk_norm_rope_quant (norm with wq / wk, RoPE with table row t, one scale per row);
+ *   v rows: scale = max(max_j |v_j|, 1e-4) / fp8_max, codes e4m3(clamp(v_j / scale, +-fp8_max)).
+ * q codes go to q_out [T, Hq, D], their scales to q_scale [T, Hq]; k and v codes and scales of token t go
+ * to slot slots[t] = page * page_size + offset of the cache. A slot outside [0, pages*page_size) (a
+ * negative one, say) marks padding: its q row is computed, nothing is written to the cache. Slots that
+ * no token names keep their contents. Two tokens of one call must not name the same slot (its contents
+ * would be either token's, or parts of both). T = 0 is a no-op; Hq = 0 is allowed.
+ */
+int fq_qkv_norm_rope_append(const void* qkv, int64_t token_stride, const void* wq, const void* wk, const void* cos,
+                            const void* sin, const int64_t* slots, uint8_t* q_out, float* q_scale,
+                            const fq_paged_cache* cache, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                            int64_t rope_dim, int dtype, int table_dtype, float eps, float fp8_max,
+                            cudaStream_t stream);
+
+/* Bytes of caller-provided device workspace fq_paged_attention needs on the current device: the fp32
+ * partial results of sequences that several CTAs share. 0 when no sequence can be shared. */
+size_t fq_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t max_seq_len);
+
+/*
+ * Attention of one new token per sequence over a paged FP8 cache, grouped query heads:
+ *   s_j   = softmax_scale * q_scale[b,h] * k_scale_j * sum_d q[b,h,d] * k_j[d]     j < len_b
+ *   p_j   = exp(s_j - max s) / sum exp(s - max s)
+ *   out[b,h,d] = dtype( sum_j p_j * v_scale_j * v_j[d] ),   lse[b,h] = log sum_j exp(s_j)
+ * where row j of sequence b is slot j % page_size of page page_table[b*table_stride + j / page_size] and
+ * query head h reads key head h / (Hq/Hk). fp32 throughout (the probabilities times V scales are rounded
+ * once to fp16, relative to their row's largest, for the tensor cores); one rounding to dtype.
+ * q: [B, Hq, D] codes, rows of a sequence q_stride elements apart (so the q heads of a prologue's
+ * [T, H, D] output can be passed in place), q_scale and page_table likewise (strides of what is only
+ * read may be 0: sequences that share a page table row); out: [B, Hq, D] packed; lse: [B, Hq] or null. len_b = seq_lens[b] cut to [0, min(max_seq_len, max_pages*page_size)]. An empty sequence gives
+ * out = 0 and lse = -inf. A page id outside [0, pages) is an absent page: its tokens take no part.
+ * Hq is a multiple of Hk; D <= 256 (else FQ_ERR_UNSUPPORTED). workspace: at least
+ * fq_paged_attention_workspace_bytes(B, Hq, Hk, D, max_seq_len) bytes, 16-byte aligned, no initial
+ * contents required; it must not be shared by calls that may overlap on the GPU. The result does not
+ * depend on timing: the split of the work follows from the arguments and the lengths alone.
+ */
+int fq_paged_attention(const uint8_t* q, int64_t q_stride, const float* q_scale, int64_t q_scale_stride,
+                       const fq_paged_cache* cache, const int32_t* page_table, int64_t table_stride,
+                       const int32_t* seq_lens, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                       int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t max_pages, int64_t max_seq_len,
+                       float softmax_scale, int dtype, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
