@@ -1,12 +1,10 @@
-// fq_matmul.cu -- choice of kernel for the FP8 serving operators: every layout takes the any-layout
-// kernels of fq_serving_scalar.cu.
+// fq_matmul.cu -- choice of kernel for the matrix product and the append: every layout takes the
+// any-layout kernels of fq_serving_scalar.cu.
 #include "fq_serving.h"
 
 namespace fq {
 
 bool launch_matmul_tc(const MatmulArgs&, int, cudaStream_t) { return false; }
 bool launch_append_vector(const AppendArgs&, int, int, cudaStream_t) { return false; }
-size_t attention_workspace_bytes(int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
-bool launch_attention_split(const PagedArgs&, int, cudaStream_t) { return false; }
 
 }  // namespace fq
