@@ -15,12 +15,14 @@
 // scheduler) and 16 fp16 products (8 clocks), about 230 of the ~700 clocks its 4 KB take to arrive at
 // 6.8 TB/s; tcgen05 would need the value tile transposed through shared memory and 128 rows to fill.
 //
-// Layout. Nothing is exchanged between threads on the way in. Both products contract over an index whose
-// order is free as long as both operands agree: thread (g, c) = (lane / 4, lane % 4) takes bytes 64i + 16c
-// .. +15 of key rows as the k indices that its B fragments hold, and bytes 16g .. +15 of value rows
-// 4c..4c+3, so every cp.async of 16 bytes lands in the thread's own slots of a ring in shared memory, is
-// read back by the same thread, and covers whole 64- or 128-byte runs of global memory per row. The score
-// tile's columns are numbered so that its accumulators are the weights' A fragment without a shuffle.
+// Layout. A producer warp streams units of 128 tokens, 16 per consumer warp, through a ring of stages: one
+// TMA box of the rows of a page at a time where pages are multiples of 8 tokens, else 16-byte cp.async row by
+// row. Both products contract over an index whose order is free as long as both operands agree: thread
+// (g, c) = (lane / 4, lane % 4) reads pieces 2c and 2c + 1 of key rows g and g + 8 as the k indices of its B
+// fragments, and piece g of value rows 2c, 2c + 1, 2c + 8, 2c + 9. Pieces are stored at (piece ^ row % 8), the
+// 128-byte swizzle, which puts the eight lanes of every 16-byte access phase in different banks for both
+// readings. The value product is taken transposed (columns x heads), so the score tile's accumulators are
+// the weights' B fragment without a shuffle and eight heads need DP / 4 accumulators a thread.
 //
 // Split. The work is a list of units (128 tokens of one sequence and key head, 16 per warp) in the order
 // sequence, head, tokens; CTA i of n takes units [i*U/n, (i+1)*U/n). The lengths are on the device, so each
@@ -32,40 +34,56 @@
 #include "fq_device.cuh"
 #include "fq_serving.h"
 #include "fq_sync.cuh"
+#include "fq_tensormap.h"
 
 namespace fq {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kStep = 16;                // tokens of one warp per unit
-constexpr int kUnit = kStep * kWarps;    // tokens per unit
-constexpr int kRows = 16;                // query heads per work item (rows of the score tile)
+constexpr int kWarps = 8;                     // consumer warps
+constexpr int kConsumers = kWarps * 32;
+constexpr int kThreads = kConsumers + 32;     // + one producer warp
+constexpr int kStep = 16;                     // tokens of one warp per unit
+constexpr int kHeads = 8;                     // query heads of one warp
+
+// A work item is one key head with kHeads * HG of its query heads; HG warps share each step's tokens.
+template <int HG>
+struct Item {
+  static constexpr int kSlabs = kWarps / HG;      // steps of 16 tokens per unit
+  static constexpr int kUnit = kStep * kSlabs;    // tokens per unit
+  static constexpr int kRows = kHeads * HG;       // query heads
+};
 constexpr float kLowest = -3.402823466e38f;  // below every score: a maximum before the first token
 
-// Ring depth and CTAs per SM by padded head size: two CTAs where the output accumulators (DP/2 registers a
-// thread) leave room, and as deep a ring as their shared memory holds.
+// Ring depth (for units of 128 tokens; twice that for 64) and CTAs per SM by padded head size, from what
+// shared memory holds.
 template <int DP>
 struct Shape {
   static constexpr int kCtas = DP <= 128 ? 2 : 1;
-  static constexpr int kStages = DP == 64 ? 6 : DP == 128 ? 3 : DP == 192 ? 4 : 3;
-  static constexpr int kStageBytes = 2 * kStep * DP;  // codes of one warp's step
-  static constexpr int kV16 = DP / 128;               // 16-byte pieces of a value row per lane
-  static constexpr int kV8 = (DP % 128) / 64;         // 8-byte pieces
+  static constexpr int kStages = DP == 64 ? 5 : DP == 128 ? 3 : DP == 192 ? 4 : 3;
+  // A unit's rows are stored as kA tiles of [rows][128 bytes], then kB of [rows][64], keys before values.
+  static constexpr int kA = DP / 128;
+  static constexpr int kB = (DP % 128) / 64;
 };
+
+// Where 16-byte piece `piece` of row `row` sits in a tile of 128-byte (64-byte) rows.
+__device__ __forceinline__ int spot128(int row, int piece) { return row * 128 + ((piece ^ (row & 7)) << 4); }
+__device__ __forceinline__ int spot64(int row, int piece) { return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4); }
 
 constexpr int kJoinStride = 36;  // floats per joined row of 32: float4 stores without bank conflicts
 
-template <int DP>
+template <int DP, int HG>
 struct Shared {
-  alignas(16) unsigned char codes[kWarps][Shape<DP>::kStages][Shape<DP>::kStageBytes];
-  alignas(16) float scales[kWarps][Shape<DP>::kStages][2 * kStep];  // K then V
-  uint32_t live[kWarps][Shape<DP>::kStages];                        // bit t: token t of the step counts
-  alignas(16) float join[kWarps][8][kJoinStride];
-  float stat[kWarps][kRows][3];  // m, M, l
-  int64_t scan[kWarps];
-  int64_t start_unit;
-  int32_t start_b;
+  static constexpr int kStages = Shape<DP>::kStages * HG;
+  static constexpr int kUnit = Item<HG>::kUnit;
+  alignas(1024) unsigned char codes[kStages][2][kUnit * DP];  // K then V
+  alignas(16) float scales[kStages][2][kUnit];  // K then V
+  uint32_t live[kStages][kUnit / 32];           // bit t % 32 of word t / 32: token t counts
+  alignas(16) float join[kWarps][kHeads][kJoinStride];
+  float stat[kWarps][kHeads][3];  // m, M, l
+  alignas(8) uint64_t full[kStages];
+  uint64_t empty[kStages];
+  int32_t scan[kThreads / 32];
+  int32_t start_unit, start_b;
 };
 
 // What a CTA that begins inside a head leaves for the join of that head.
@@ -76,18 +94,32 @@ struct Meta {
 struct SplitArgs {
   PagedArgs p;
   int32_t G;       // query heads per key head
-  int32_t chunks;  // work items per key head: ceil(G / 16)
+  int32_t chunks;  // work items per key head
   int32_t slots;   // 2 * the first kernel's grid
+  uint32_t page_magic;  // t / page_size = (t * page_magic) >> page_magic_shift for t < 2^31
+  int32_t page_magic_shift;
+  unsigned int* status;
+  int32_t dtype;
+  int32_t box_shift;    // TMA feed: log2 of the rows per box, which divide a page and a unit
+  int32_t bulk_scales;  // TMA feed: the scales of a box are contiguous and 16-byte aligned
   Meta* meta;      // [grid]
-  float* stats;    // [slots][16][4]: m, M, l
-  float* part;     // [slots][16][DP]
+  float* stats;    // [slots][rows of an item][4]: m, M, l
+  float* part;     // [slots][rows of an item][DP]
+};
+
+// TMA feed: maps of the keys' and values' 128-byte and 64-byte pieces of a row ({D, slot, head, page}).
+struct Maps {
+  CUtensorMap k128, v128, k64, v64;
 };
 
 __device__ __forceinline__ int32_t length_of(const PagedArgs& p, int32_t b) {
   return static_cast<int32_t>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(__ldg(p.lens + b)), p.max_len)));
 }
 
-__device__ __forceinline__ int32_t tiles_of(int32_t len) { return (len + kUnit - 1) / kUnit; }
+template <int HG>
+__device__ __forceinline__ int32_t tiles_of(int32_t len) {
+  return (len + Item<HG>::kUnit - 1) / Item<HG>::kUnit;
+}
 
 __device__ __forceinline__ float ex2(float v) {
   float r;
@@ -97,7 +129,7 @@ __device__ __forceinline__ float ex2(float v) {
 
 __device__ __forceinline__ float lg2(float v) {
   float r;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
 
@@ -108,27 +140,21 @@ __device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Copies of `bytes` (or zeros in their place) into shared memory.
+// N bytes into shared memory, or zeros (and nothing read) where `live` is false.
 template <int N>
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool live) {
+__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void* src, bool live) {
   if constexpr (N == 16)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(live ? N : 0)
                  : "memory");
-}
-
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // e4m3 codes at the same byte of two words (tokens t, t+1) -> the fp16 pair of a B fragment; exact.
@@ -157,35 +183,48 @@ __device__ __forceinline__ float quad_max(float v) {
   return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
 }
 
-// A place in the list of units: tile t of work item `item` (key head item / chunks, query heads from
-// 16 * (item % chunks)) of sequence b, which has `len` tokens.
+// A place in the list of units: a work item of sequence b (key head item / chunks, and the item % chunks-th
+// part of its query heads) with `left` tiles to go, `len` tokens in all.
+template <int HG>
 struct Place {
-  int32_t b, item, t, len;
+  int32_t b, item, len, left;
 
-  __device__ __forceinline__ void step(const SplitArgs& a) {
-    if (++t < tiles_of(len)) return;
-    t = 0;
-    if (++item < a.p.Hk * a.chunks) return;
-    item = 0;
-    len = 0;
-    while (len == 0 && ++b < a.p.B) len = length_of(a.p, b);
+  // To the next head; `left` is its number of tiles.
+  __device__ __forceinline__ void next_head(const SplitArgs& a) {
+    if (++item == a.p.Hk * a.chunks) {
+      item = 0;
+      len = 0;
+      while (len == 0 && ++b < a.p.B) len = length_of(a.p, b);
+    }
+    left = tiles_of<HG>(len);
+  }
+};
+
+// The units of `total` that each of n CTAs takes: the first `rest` take each + 1, the others `each`.
+struct Share {
+  int32_t each, rest;
+  __device__ __forceinline__ Share(int32_t total, int32_t n) : each(total / n), rest(total - total / n * n) {}
+  __device__ __forceinline__ int32_t begin(int32_t cta) const { return cta * each + min(cta, rest); }
+  __device__ __forceinline__ int32_t owner(int32_t unit) const {
+    const int32_t wide = rest * (each + 1);
+    return unit < wide ? unit / (each + 1) : rest + (unit - wide) / each;
   }
 };
 
 // The block's inclusive sum of v over its threads.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scan, int64_t* total) {
+__device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* scan, int32_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   __syncthreads();
   if (lane == 31) scan[warp] = v;
   __syncthreads();
-  int64_t before = 0, all = 0;
+  int32_t before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += scan[w];
     all += scan[w];
   }
@@ -193,55 +232,295 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scan, int64_t*
   return v + before;
 }
 
-template <typename T, int DP, bool kWide>
-__global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas) attention_split_kernel(const SplitArgs a) {
+// The producer warp, any page size and layout of scales: copies units `begin`..`begin + units - 1`, whose first is at `at`, into the ring.
+template <int DP, int HG>
+__device__ __forceinline__ void produce_rows(const SplitArgs& a, Shared<DP, HG>& sm, Place<HG> at, int32_t units) {
   using S = Shape<DP>;
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  Shared<DP>& sm = *reinterpret_cast<Shared<DP>*>(smem_raw);
+  constexpr int kUnit = Item<HG>::kUnit, kQ = kUnit / 32, kStages = Shared<DP, HG>::kStages;
   const PagedArgs& p = a.p;
   const CacheView& cache = p.cache;
+  const int lane = threadIdx.x & 31;
+  int32_t tok = (tiles_of<HG>(at.len) - at.left) * kUnit + lane;  // this lane's tokens: tok + 32*q
+  int64_t head_off = 0, head_soff = 0;
+  const int32_t* table = nullptr;
+  auto enter = [&]() {
+    const int32_t head = at.item / a.chunks;
+    head_off = head * cache.head_stride;
+    head_soff = head * cache.s_head_stride;
+    table = p.table + static_cast<int64_t>(at.b) * p.table_stride;
+  };
+  auto page_index = [&](int32_t t) {
+    return static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(t)) * a.page_magic) >> a.page_magic_shift);
+  };
+  // The pages of the next unit's tokens, loaded one unit ahead of their use; -1 behind the end.
+  int32_t page[kQ];
+  auto look_up = [&]() {
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) page[q] = tok + 32 * q < at.len ? __ldg(table + page_index(tok + 32 * q)) : -1;
+  };
+  enter();
+  look_up();
+  int stage = 0;
+  uint32_t phase = 1;  // the first round finds every stage empty
+  for (int32_t u = 0; u < units; ++u) {
+    if (u >= kStages && !mbar_wait(kWaitLimitNs, &sm.empty[stage], phase)) {
+      flag_failure(a.status);
+      break;
+    }
+    int64_t row[kQ];
+    uint32_t mask[kQ];
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+      const int32_t t = tok + 32 * q;
+      const int32_t off = t - page_index(t) * cache.page_size;
+      const bool live = static_cast<uint32_t>(page[q]) < static_cast<uint32_t>(cache.pages);
+      mask[q] = __ballot_sync(0xffffffffu, live);
+      row[q] = live ? page[q] * cache.page_stride + head_off + off * cache.token_stride : -1;
+      if (mask[q] != 0u) {
+        const int64_t srow = live ? page[q] * cache.s_page_stride + head_soff + off * cache.s_token_stride : 0;
+        cp_async_or_zero<4>(smem_addr(&sm.scales[stage][0][32 * q + lane]), cache.k_scale + srow, live);
+        cp_async_or_zero<4>(smem_addr(&sm.scales[stage][1][32 * q + lane]), cache.v_scale + srow, live);
+      }
+    }
+    if (lane == 0)
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) sm.live[stage][q] = mask[q];
+    const uint32_t kd = smem_addr(sm.codes[stage][0]), vd = smem_addr(sm.codes[stage][1]);
+#pragma unroll
+    for (int w = 0; w < Item<HG>::kSlabs; ++w) {
+      const uint32_t here = (mask[w >> 1] >> (16 * (w & 1))) & 0xffffu;
+      if (here == 0u) continue;
+      if constexpr (S::kA > 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = (lane >> 3) + 4 * j, piece = lane & 7;
+          const int64_t from = __shfl_sync(0xffffffffu, row[w >> 1], 16 * (w & 1) + r) + 16 * piece;
+          const int d = 2048 * w + spot128(r, piece);
+#pragma unroll
+          for (int i = 0; i < S::kA; ++i) {
+            const bool ok = from >= 16 * piece && 128 * i + 16 * piece < p.D;
+            cp_async_or_zero<16>(kd + 128 * kUnit * i + d, cache.k + (ok ? from + 128 * i : 0), ok);
+            cp_async_or_zero<16>(vd + 128 * kUnit * i + d, cache.v + (ok ? from + 128 * i : 0), ok);
+          }
+        }
+      }
+      if constexpr (S::kB > 0) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = (lane >> 2) + 8 * j, piece = lane & 3;
+          const int64_t from = __shfl_sync(0xffffffffu, row[w >> 1], 16 * (w & 1) + r) + 16 * piece;
+          const int d = 128 * kUnit * S::kA + 1024 * w + spot64(r, piece);
+          const bool ok = from >= 16 * piece && 128 * S::kA + 16 * piece < p.D;
+          cp_async_or_zero<16>(kd + d, cache.k + (ok ? from + 128 * S::kA : 0), ok);
+          cp_async_or_zero<16>(vd + d, cache.v + (ok ? from + 128 * S::kA : 0), ok);
+        }
+      }
+    }
+    // Each lane arrives once its copies have landed, lane 0 once more for the masks.
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(&sm.full[stage])) : "memory");
+    if (lane == 0) mbar_arrive(&sm.full[stage]);
+    if (u + 1 < units) {
+      tok += kUnit;
+      if (--at.left == 0) {
+        at.next_head(a);
+        tok = lane;
+        enter();
+      }
+      look_up();
+    }
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");  // nothing in flight when the warp ends
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z, int32_t w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// The producer warp for pages that are multiples of 8 tokens: lane k feeds the k-th box of each unit, 2^box_shift
+// tokens of one page. Rows of a box behind the sequence's end are loaded too (they are inside the cache) and
+// masked by the consumers.
+template <int DP, int HG>
+__device__ __forceinline__ void produce_boxes(const SplitArgs& a, const Maps& maps, Shared<DP, HG>& sm, Place<HG> at,
+                                              int32_t units) {
+  using S = Shape<DP>;
+  constexpr int kUnit = Item<HG>::kUnit, kQ = kUnit / 32, kStages = Shared<DP, HG>::kStages;
+  const PagedArgs& p = a.p;
+  const CacheView& cache = p.cache;
+  const int lane = threadIdx.x & 31;
+  const int rows = 1 << a.box_shift;
+  const bool mine = (lane << a.box_shift) < kUnit;
+  int32_t base = (tiles_of<HG>(at.len) - at.left) * kUnit;  // the unit's first token
+  int32_t head = 0;
+  const int32_t* table = nullptr;
+  auto enter = [&]() {
+    head = at.item / a.chunks;
+    table = p.table + static_cast<int64_t>(at.b) * p.table_stride;
+  };
+  // Page and slot of this lane's box of the unit at `base`, loaded one unit ahead; page -1 behind the end.
+  int32_t page = -1, slot = 0;
+  auto look_up = [&]() {
+    const int32_t t = base + (lane << a.box_shift);
+    const int32_t i = static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(t)) * a.page_magic) >> a.page_magic_shift);
+    slot = t - i * cache.page_size;
+    page = mine && t < at.len ? __ldg(table + i) : -1;
+  };
+  enter();
+  look_up();
+  int stage = 0;
+  uint32_t phase = 1;  // the first round finds every stage empty
+  int32_t u = 0;
+  bool ok = true;
+  for (; u < units; ++u) {
+    if (u >= kStages && !mbar_wait(kWaitLimitNs, &sm.empty[stage], phase)) {
+      ok = false;
+      break;
+    }
+    const bool live = static_cast<uint32_t>(page) < static_cast<uint32_t>(cache.pages);
+    const uint32_t boxes = __ballot_sync(0xffffffffu, live);
+    const int32_t tok = base + lane;
+    uint32_t mask = 0;
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+      const uint32_t b = __ballot_sync(0xffffffffu, ((boxes >> ((32 * q + lane) >> a.box_shift)) & 1u) != 0u && tok + 32 * q < at.len);
+      if (lane == q) mask = b;
+    }
+    if (lane < kQ) sm.live[stage][lane] = mask;
+    uint64_t* bar = &sm.full[stage];
+    if (a.bulk_scales == 0) {
+#pragma unroll
+      for (int q = 0; q < kQ; ++q) {
+        const int from = (32 * q + lane) >> a.box_shift;  // the lane whose box holds this lane's token
+        const int32_t pg = __shfl_sync(0xffffffffu, page, from), sl = __shfl_sync(0xffffffffu, slot, from);
+        const bool have = (boxes >> from) & 1u;
+        const int64_t srow = have ? pg * cache.s_page_stride + head * cache.s_head_stride +
+                                        (sl + ((32 * q + lane) & (rows - 1))) * cache.s_token_stride
+                                  : 0;
+        cp_async_or_zero<4>(smem_addr(&sm.scales[stage][0][32 * q + lane]), cache.k_scale + srow, have);
+        cp_async_or_zero<4>(smem_addr(&sm.scales[stage][1][32 * q + lane]), cache.v_scale + srow, have);
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+    }
+    __syncwarp();  // the masks are written before lane 0 arrives
+    if (lane == 0)
+      mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(boxes)) * static_cast<uint32_t>(rows) *
+                                     (2u * DP + (a.bulk_scales != 0 ? 8u : 0u)));
+    __syncwarp();
+    if (live) {
+      const int row = lane << a.box_shift;
+      const uint32_t kd = smem_addr(sm.codes[stage][0]), vd = smem_addr(sm.codes[stage][1]);
+#pragma unroll
+      for (int i = 0; i < S::kA; ++i) {
+        tma_load_4d(kd + 128 * (kUnit * i + row), &maps.k128, 128 * i, slot, head, page, bar);
+        tma_load_4d(vd + 128 * (kUnit * i + row), &maps.v128, 128 * i, slot, head, page, bar);
+      }
+      if constexpr (S::kB > 0) {
+        tma_load_4d(kd + 128 * kUnit * S::kA + 64 * row, &maps.k64, 128 * S::kA, slot, head, page, bar);
+        tma_load_4d(vd + 128 * kUnit * S::kA + 64 * row, &maps.v64, 128 * S::kA, slot, head, page, bar);
+      }
+      if (a.bulk_scales != 0) {
+        const int64_t srow = page * cache.s_page_stride + head * cache.s_head_stride + slot;
+        bulk_g2s(&sm.scales[stage][0][row], cache.k_scale + srow, 4u * rows, bar);
+        bulk_g2s(&sm.scales[stage][1][row], cache.v_scale + srow, 4u * rows, bar);
+      }
+    }
+    if (u + 1 < units) {
+      base += kUnit;
+      if (--at.left == 0) {
+        at.next_head(a);
+        base = 0;
+        enter();
+      }
+      look_up();
+    }
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  if (!ok) {
+    flag_failure(a.status);
+    // Let the copies already issued land before this CTA's shared memory goes away.
+    for (int32_t j = max(0, u - kStages); j < u; ++j)
+      if (!mbar_wait(kWaitLimitNs, &sm.full[j % kStages], static_cast<uint32_t>(j / kStages) & 1u)) break;
+  }
+}
+
+__device__ __forceinline__ void store_out(int dtype, void* out, int64_t i, float v) {
+  if (dtype == DT_BF16) Elem<__nv_bfloat16>::store1(out, i, v);
+  else Elem<__half>::store1(out, i, v);
+}
+
+__device__ __forceinline__ void consumer_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
+
+// kBoxes: fed by TMA boxes, else row by row.
+template <int DP, int HG, bool kBoxes>
+__global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas)
+    attention_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ SplitArgs a) {
+  using S = Shape<DP>;
+  using Sm = Shared<DP, HG>;
+  constexpr int kSlabs = Item<HG>::kSlabs;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  // The swizzles repeat every 1024 bytes: align the ring to 1024.
+  Sm& sm = *reinterpret_cast<Sm*>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
+  const PagedArgs& p = a.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x < Sm::kStages) {
+    mbar_init(&sm.full[threadIdx.x], kBoxes && a.bulk_scales != 0 ? 1 : 33);  // lane 0, and each lane's cp.async
+    mbar_init(&sm.empty[threadIdx.x], kWarps);
+    fence_barrier_init();
+  }
 
-  // This CTA's units [begin, end) of all U, and the place of the first.
-  const int64_t per_tile = static_cast<int64_t>(p.Hk) * a.chunks;
-  int64_t total = 0;
-  int64_t incl = 0, mine = 0;
+  // This CTA's units [begin, end) of all, and the place of the first. (block_scan's barriers also publish
+  // the mbarriers.)
+  const int32_t per_tile = p.Hk * a.chunks;
+  int32_t total = 0, incl = 0, mine = 0;
   for (int32_t b0 = 0; b0 < p.B; b0 += kThreads) {
     const int32_t b = b0 + static_cast<int32_t>(threadIdx.x);
     const int32_t len = b < p.B ? length_of(p, b) : 0;
-    mine = tiles_of(len) * per_tile;
-    int64_t sum;
+    mine = tiles_of<HG>(len) * per_tile;
+    int32_t sum;
     incl = block_scan(mine, sm.scan, &sum);
     total += sum;
     // Sequences without tokens: zeros and -inf, spread over the CTAs.
     if (b < p.B && len == 0 && b % gridDim.x == blockIdx.x) {
-      T* o = static_cast<T*>(p.out) + static_cast<int64_t>(b) * p.Hq * p.D;
+      uint16_t* o = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(b) * p.Hq * p.D;
       for (int64_t i = 0; i < static_cast<int64_t>(p.Hq) * p.D; i += 8)
         *reinterpret_cast<uint4*>(o + i) = make_uint4(0u, 0u, 0u, 0u);
       if (p.lse != nullptr)
         for (int32_t h = 0; h < p.Hq; ++h) p.lse[static_cast<int64_t>(b) * p.Hq + h] = -CUDART_INF_F;
     }
   }
-  const int64_t n = min(static_cast<int64_t>(gridDim.x), total);  // CTAs with work
-  const int64_t cta = blockIdx.x;
-  const int64_t begin = cta < n ? cta * total / n : 0, end = cta < n ? (cta + 1) * total / n : 0;
-  if (begin == end) {
+  const int32_t n = min(static_cast<int32_t>(gridDim.x), total);  // CTAs with work
+  const int32_t cta = blockIdx.x;
+  if (cta >= n) {
     if (threadIdx.x == 0 && a.meta != nullptr) a.meta[cta].b = -1;
     return;
   }
+  const Share share(total, n);
+  const int32_t begin = share.begin(cta), units = share.begin(cta + 1) - begin;
   if (p.B <= kThreads) {
     if (incl - mine <= begin && begin < incl) {
       sm.start_b = threadIdx.x;
       sm.start_unit = begin - (incl - mine);
     }
   } else {
-    int64_t carry = 0;
+    int32_t carry = 0;
     for (int32_t b0 = 0; b0 < p.B && carry <= begin; b0 += kThreads) {
       const int32_t b = b0 + static_cast<int32_t>(threadIdx.x);
-      mine = b < p.B ? tiles_of(length_of(p, b)) * per_tile : 0;
-      int64_t sum;
+      mine = b < p.B ? tiles_of<HG>(length_of(p, b)) * per_tile : 0;
+      int32_t sum;
       incl = block_scan(mine, sm.scan, &sum) + carry;
       if (incl - mine <= begin && begin < incl) {
         sm.start_b = b;
@@ -251,298 +530,244 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas) attention_split_ke
     }
   }
   __syncthreads();
-  Place use;
+  Place<HG> use;
   use.b = sm.start_b;
   use.len = length_of(p, use.b);
-  {
-    const int32_t nt = tiles_of(use.len);
-    use.item = static_cast<int32_t>(sm.start_unit / nt);
-    use.t = static_cast<int32_t>(sm.start_unit - static_cast<int64_t>(use.item) * nt);
-    if (threadIdx.x == 0 && a.meta != nullptr) {
-      // The head this CTA begins inside is joined by the second CTA that has a part of it.
-      const int64_t first = begin - use.t;                       // the head's first unit
-      const int64_t i0 = ((first + 1) * n - 1) / total;          // the CTA that has it
-      const int64_t i1 = ((first + nt) * n - 1) / total;         // the CTA that has its last unit
-      Meta m;
-      m.b = use.t > 0 && i0 == cta - 1 ? use.b : -1;
-      m.item = use.item;
-      m.last = static_cast<int32_t>(i1);
-      m.slot = i0 * total / n == first ? 0 : 1;
-      a.meta[cta] = m;
-    }
+  const int32_t nt = tiles_of<HG>(use.len);
+  use.item = sm.start_unit / nt;
+  const int32_t t = sm.start_unit - use.item * nt;
+  use.left = nt - t;
+  if (warp == kWarps) {
+    if constexpr (kBoxes) produce_boxes<DP, HG>(a, maps, sm, use, units);
+    else produce_rows<DP, HG>(a, sm, use, units);
+    return;
   }
-  const int64_t units = end - begin;
-
-  // ------------------------------------------------------------------------------- way in
-  Place next = use;
-  int64_t issued = 0;
-  // The page of this lane's token of the next unit to be issued, loaded one unit ahead.
-  auto page_of = [&](const Place& at) {
-    const int32_t tok = at.t * kUnit + warp * kStep + (lane & 15);
-    if (tok >= at.len) return -1;
-    const int32_t i = cache.page_shift >= 0 ? tok >> cache.page_shift : tok / cache.page_size;
-    return __ldg(p.table + static_cast<int64_t>(at.b) * p.table_stride + i);
-  };
-  int32_t page = page_of(next);
-  auto issue = [&](int stage) {
-    if (issued < units) {
-      const int32_t tok = next.t * kUnit + warp * kStep + (lane & 15);
-      const int32_t off = cache.page_shift >= 0 ? tok & (cache.page_size - 1) : tok % cache.page_size;
-      const int32_t head = next.item / a.chunks;
-      const bool live = page >= 0 && page < cache.pages;
-      const int64_t row = live ? page * cache.page_stride + head * cache.head_stride + off * cache.token_stride : -1;
-      const int64_t srow = page * cache.s_page_stride + head * cache.s_head_stride + off * cache.s_token_stride;
-      const uint32_t mask = __ballot_sync(0xffffffffu, live) & 0xffffu;
-      if (lane == 0) sm.live[warp][stage] = mask;
-      if (mask != 0u) {
-        const uint32_t dst = smem_addr(sm.codes[warp][stage]);
-        const float* sbase = lane < 16 ? cache.k_scale : cache.v_scale;
-        cp_async<4>(smem_addr(&sm.scales[warp][stage][lane]), live ? sbase + srow : sbase, live);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int64_t r = __shfl_sync(0xffffffffu, row, 4 * (g >> 1) + (g & 1) + 2 * u);
-#pragma unroll
-          for (int i = 0; i < DP / 64; ++i) {
-            const bool ok = r >= 0 && 64 * i + 16 * c < p.D;
-            cp_async<16>(dst + ((u * (DP / 64) + i) * 32 + lane) * 16, cache.k + (ok ? r + 64 * i + 16 * c : 0), ok);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int64_t r = __shfl_sync(0xffffffffu, row, 4 * c + e);
-#pragma unroll
-          for (int i = 0; i < S::kV16; ++i) {
-            const bool ok = r >= 0 && 128 * i + 16 * g < p.D;
-            cp_async<16>(dst + kStep * DP + (i * 4 + e) * 512 + lane * 16, cache.v + (ok ? r + 128 * i + 16 * g : 0), ok);
-          }
-          if constexpr (S::kV8 > 0) {
-            constexpr int d0 = 128 * S::kV16;
-            const bool ok = r >= 0 && d0 + 8 * g < p.D;
-            cp_async<8>(dst + kStep * DP + S::kV16 * 2048 + e * 256 + lane * 8, cache.v + (ok ? r + d0 + 8 * g : 0), ok);
-          }
-        }
-      }
-      next.step(a);
-      if (++issued < units) page = page_of(next);
-    }
-    cp_commit();
-  };
-#pragma unroll
-  for (int s = 0; s < S::kStages - 1; ++s) issue(s);
+  if (threadIdx.x == 0 && a.meta != nullptr) {
+    // The head this CTA begins inside is joined by the second CTA that has a part of it.
+    const int32_t first = begin - t;  // the head's first unit
+    const int32_t i0 = share.owner(first);
+    Meta m;
+    m.b = t > 0 && i0 == cta - 1 ? use.b : -1;
+    m.item = use.item;
+    m.last = share.owner(first + nt - 1);
+    m.slot = share.begin(i0) == first ? 0 : 1;
+    a.meta[cta] = m;
+  }
 
   // --------------------------------------------------------------------------- the heads
-  constexpr int kN = DP / 8;  // output tiles of 8 columns
-  uint4 qa[DP / 64], qb[kWide ? DP / 64 : 1];
-  float qf[2], m[2], mo[2], l[2];
+  const int slab = warp % kSlabs, group = warp / kSlabs;  // this warp's tokens of a unit and heads of an item
+  uint4 q[DP / 64];
+  float qf = 0.f, m = kLowest, mo = kLowest, l = 0.f;  // of head g, the same in the four threads of its row
+  // Output tiles of 16 columns x 8 heads: o[n][2h + e] is column 16g + .. + h of head 2c + e.
+  constexpr int kN = DP / 16;
   float o[kN][4];
   bool first_segment = true;
-  bool fresh = true;
-  int32_t t0 = use.t;
-  int stage = 0, fill = S::kStages - 1;
+  bool fresh = true, from_start = false;
+  int32_t rows = 0, head0 = 0;  // query heads of the item, and the first of them
+  int stage = 0;
+  uint32_t phase = 0;
+  bool arrived = true;  // false once a wait gave up: the rest runs through without waiting
 
-  for (int64_t u = 0; u < units; ++u) {
-    const int32_t rows = min(kRows, a.G - kRows * (use.item % a.chunks));
-    const int32_t head0 = use.item / a.chunks * a.G + kRows * (use.item % a.chunks);  // first query head
+  for (int32_t u = 0; u < units; ++u) {
     if (fresh) {
       fresh = false;
-      t0 = use.t;
-      const uint8_t* q = p.q + static_cast<int64_t>(use.b) * p.q_stride + static_cast<int64_t>(head0) * p.D;
-      const float* qs = p.q_scale + static_cast<int64_t>(use.b) * p.q_scale_stride + head0;
+      from_start = use.left == tiles_of<HG>(use.len);
+      const int32_t head = use.item / a.chunks, chunk = use.item - head * a.chunks;
+      rows = min(Item<HG>::kRows, a.G - Item<HG>::kRows * chunk);
+      head0 = head * a.G + Item<HG>::kRows * chunk;
+      const int32_t h = kHeads * group + g;
+      const uint8_t* src = p.q + static_cast<int64_t>(use.b) * p.q_stride + static_cast<int64_t>(head0 + h) * p.D;
 #pragma unroll
       for (int i = 0; i < DP / 64; ++i) {
-        const int d = 64 * i + 16 * c;
-        qa[i] = g < rows && d < p.D ? __ldg(reinterpret_cast<const uint4*>(q + g * p.D + d)) : make_uint4(0u, 0u, 0u, 0u);
-        if constexpr (kWide)
-          qb[i] = g + 8 < rows && d < p.D ? __ldg(reinterpret_cast<const uint4*>(q + (g + 8) * p.D + d))
-                                          : make_uint4(0u, 0u, 0u, 0u);
+        const int d = i < 2 * S::kA ? 128 * (i >> 1) + 16 * (2 * c + (i & 1)) : 128 * S::kA + 16 * c;
+        q[i] = h < rows && d < p.D ? __ldg(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0u, 0u, 0u, 0u);
       }
-      qf[0] = g < rows ? __ldg(qs + g) * p.scale_log2 : 0.f;
-      qf[1] = kWide && g + 8 < rows ? __ldg(qs + g + 8) * p.scale_log2 : 0.f;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        m[r] = mo[r] = kLowest;
-        l[r] = 0.f;
-      }
+      qf = h < rows ? __ldg(p.q_scale + static_cast<int64_t>(use.b) * p.q_scale_stride + head0 + h) * p.scale_log2 : 0.f;
+      m = mo = kLowest;
+      l = 0.f;
 #pragma unroll
       for (int i = 0; i < kN; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     }
-    cp_wait<S::kStages - 2>();
-    __syncwarp();  // the scales and the mask come from other lanes
-    issue(fill);
-    if (++fill == S::kStages) fill = 0;
-
-    const uint32_t live = sm.live[warp][stage];
+    if (arrived && !mbar_wait(kWaitLimitNs, &sm.full[stage], phase)) {
+      flag_failure(a.status);
+      arrived = false;
+    }
+    const uint32_t live = (sm.live[stage][slab >> 1] >> (16 * (slab & 1))) & 0xffffu;
     if (live != 0u) {
-      const unsigned char* st = sm.codes[warp][stage];
-      float s[2][4] = {};
+      const unsigned char* kt = sm.codes[stage][0];
+      float s[2][4] = {};  // rows 8..15 of the score tile stay empty
 #pragma unroll
       for (int i = 0; i < DP / 64; ++i) {
-        const uint4 k0 = *reinterpret_cast<const uint4*>(st + (i * 32 + lane) * 16);
-        const uint4 k1 = *reinterpret_cast<const uint4*>(st + ((DP / 64 + i) * 32 + lane) * 16);
-        const uint4 b8 = kWide ? qb[kWide ? i : 0] : make_uint4(0u, 0u, 0u, 0u);
-        mma_e4m3(s[0], qa[i].x, b8.x, qa[i].y, b8.y, k0.x, k0.y);
-        mma_e4m3(s[1], qa[i].x, b8.x, qa[i].y, b8.y, k1.x, k1.y);
-        mma_e4m3(s[0], qa[i].z, b8.z, qa[i].w, b8.w, k0.z, k0.w);
-        mma_e4m3(s[1], qa[i].z, b8.z, qa[i].w, b8.w, k1.z, k1.w);
+        const int at = i < 2 * S::kA ? 128 * Sm::kUnit * (i >> 1) + 2048 * slab + spot128(g, 2 * c + (i & 1))
+                                     : 128 * Sm::kUnit * S::kA + 1024 * slab + spot64(g, c);
+        const uint4 k0 = *reinterpret_cast<const uint4*>(kt + at);
+        const uint4 k1 = *reinterpret_cast<const uint4*>(kt + at + (i < 2 * S::kA ? 1024 : 512));  // row g + 8
+        mma_e4m3(s[0], q[i].x, 0u, q[i].y, 0u, k0.x, k0.y);
+        mma_e4m3(s[1], q[i].x, 0u, q[i].y, 0u, k1.x, k1.y);
+        mma_e4m3(s[0], q[i].z, 0u, q[i].w, 0u, k0.z, k0.w);
+        mma_e4m3(s[1], q[i].z, 0u, q[i].w, 0u, k1.z, k1.w);
       }
-      const float4 ks4 = *reinterpret_cast<const float4*>(&sm.scales[warp][stage][4 * c]);
-      const float4 vs4 = *reinterpret_cast<const float4*>(&sm.scales[warp][stage][kStep + 4 * c]);
-      const float ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w};
-      const float lv[4] = {lg2(vs4.x), lg2(vs4.y), lg2(vs4.z), lg2(vs4.w)};
-      constexpr int kR = kWide ? 2 : 1;
-      uint32_t pa[4] = {0u, 0u, 0u, 0u};
-      float keep[2] = {1.f, 1.f};
+      // Score 2u + e of a thread is token 2c + e + 8u.
+      const float* sk = &sm.scales[stage][0][kStep * slab + 2 * c];
+      const float* sv = &sm.scales[stage][1][kStep * slab + 2 * c];
+      const float2 ka = *reinterpret_cast<const float2*>(sk), kb = *reinterpret_cast<const float2*>(sk + 8);
+      const float2 va = *reinterpret_cast<const float2*>(sv), vb = *reinterpret_cast<const float2*>(sv + 8);
+      float x[4] = {s[0][0] * (qf * ka.x), s[0][1] * (qf * ka.y), s[1][0] * (qf * kb.x), s[1][1] * (qf * kb.y)};
+      float w[4] = {x[0] + lg2(va.x), x[1] + lg2(va.y), x[2] + lg2(vb.x), x[3] + lg2(vb.y)};
+      if (live != 0xffffu) {
 #pragma unroll
-      for (int r = 0; r < kR; ++r) {
-        float x[4], w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float v = s[e >> 1][2 * r + (e & 1)] * (qf[r] * ks[e]);
-          x[e] = (live >> (4 * c + e)) & 1u ? v : -CUDART_INF_F;
-          w[e] = x[e] + lv[e];
-          if (!((live >> (4 * c + e)) & 1u)) w[e] = -CUDART_INF_F;
-        }
-        const float mn = quad_max(fmaxf(fmaxf(m[r], fmaxf(x[0], x[1])), fmaxf(x[2], x[3])));
-        const float on = quad_max(fmaxf(fmaxf(mo[r], fmaxf(w[0], w[1])), fmaxf(w[2], w[3])));
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum += ex2(x[e] - mn);
-        l[r] = fmaf(l[r], ex2(m[r] - mn), sum);
-        keep[r] = ex2(mo[r] - on);
-        m[r] = mn;
-        mo[r] = on;
-        pa[r] = pack_f16(ex2(w[0] - on), ex2(w[1] - on));
-        pa[2 + r] = pack_f16(ex2(w[2] - on), ex2(w[3] - on));
+        for (int e = 0; e < 4; ++e)
+          if (!((live >> (2 * c + (e & 1) + 8 * (e >> 1))) & 1u)) x[e] = w[e] = -CUDART_INF_F;
       }
-      if (__any_sync(0xffffffffu, keep[0] != 1.f || keep[1] != 1.f)) {
+      const float mn = quad_max(fmaxf(fmaxf(m, fmaxf(x[0], x[1])), fmaxf(x[2], x[3])));
+      const float on = quad_max(fmaxf(fmaxf(mo, fmaxf(w[0], w[1])), fmaxf(w[2], w[3])));
+      l = fmaf(l, ex2(m - mn), (ex2(x[0] - mn) + ex2(x[1] - mn)) + (ex2(x[2] - mn) + ex2(x[3] - mn)));
+      const float keep = ex2(mo - on);
+      m = mn;
+      mo = on;
+      const uint32_t p0 = pack_f16(ex2(w[0] - on), ex2(w[1] - on)), p1 = pack_f16(ex2(w[2] - on), ex2(w[3] - on));
+      if (__any_sync(0xffffffffu, keep != 1.f)) {
+        const float k0 = __shfl_sync(0xffffffffu, keep, 8 * c), k1 = __shfl_sync(0xffffffffu, keep, 8 * c + 4);
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-          o[i][0] *= keep[0];
-          o[i][1] *= keep[0];
-          o[i][2] *= keep[1];
-          o[i][3] *= keep[1];
+          o[i][0] *= k0;
+          o[i][1] *= k1;
+          o[i][2] *= k0;
+          o[i][3] *= k1;
         }
       }
-      const unsigned char* vt = st + kStep * DP;
+      const unsigned char* vt = sm.codes[stage][1];
 #pragma unroll
-      for (int i = 0; i < S::kV16; ++i) {
+      for (int i = 0; i < S::kA; ++i) {
         uint4 v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const uint4*>(vt + (i * 4 + e) * 512 + lane * 16);
+        for (int e = 0; e < 4; ++e)
+          v[e] = *reinterpret_cast<const uint4*>(vt + 128 * Sm::kUnit * i + 2048 * slab +
+                                                 spot128(2 * c + (e & 1) + 8 * (e >> 1), g));
+        if (live != 0xffffu) {  // codes of tokens that do not count may be NaN: 0 * NaN must not reach the sum
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!((live >> (2 * c + (e & 1) + 8 * (e >> 1))) & 1u)) v[e] = make_uint4(0u, 0u, 0u, 0u);
+        }
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          uint32_t b0[4], b1[4];
-          pair_f16(word(v[0], k), word(v[1], k), b0);
-          pair_f16(word(v[2], k), word(v[3], k), b1);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mma_f16(o[i * 16 + 4 * k + j], pa, b0[j], b1[j]);
+          uint32_t lo[4], hi[4];
+          pair_f16(word(v[0], k), word(v[1], k), lo);
+          pair_f16(word(v[2], k), word(v[3], k), hi);
+          mma_f16(o[8 * i + 2 * k], lo[0], lo[1], hi[0], hi[1], p0, p1);
+          mma_f16(o[8 * i + 2 * k + 1], lo[2], lo[3], hi[2], hi[3], p0, p1);
         }
       }
-      if constexpr (S::kV8 > 0) {
+      if constexpr (S::kB > 0) {
         uint2 v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const uint2*>(vt + S::kV16 * 2048 + e * 256 + lane * 8);
+        for (int e = 0; e < 4; ++e)
+          v[e] = *reinterpret_cast<const uint2*>(vt + 128 * Sm::kUnit * S::kA + 1024 * slab +
+                                                 spot64(2 * c + (e & 1) + 8 * (e >> 1), g >> 1) + 8 * (g & 1));
+        if (live != 0xffffu) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!((live >> (2 * c + (e & 1) + 8 * (e >> 1))) & 1u)) v[e] = make_uint2(0u, 0u);
+        }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          uint32_t b0[4], b1[4];
-          pair_f16(k == 0 ? v[0].x : v[0].y, k == 0 ? v[1].x : v[1].y, b0);
-          pair_f16(k == 0 ? v[2].x : v[2].y, k == 0 ? v[3].x : v[3].y, b1);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mma_f16(o[S::kV16 * 16 + 4 * k + j], pa, b0[j], b1[j]);
+          uint32_t lo[4], hi[4];
+          pair_f16(k == 0 ? v[0].x : v[0].y, k == 0 ? v[1].x : v[1].y, lo);
+          pair_f16(k == 0 ? v[2].x : v[2].y, k == 0 ? v[3].x : v[3].y, hi);
+          mma_f16(o[8 * S::kA + 2 * k], lo[0], lo[1], hi[0], hi[1], p0, p1);
+          mma_f16(o[8 * S::kA + 2 * k + 1], lo[2], lo[3], hi[2], hi[3], p0, p1);
         }
       }
     }
-    if (++stage == S::kStages) stage = 0;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.empty[stage]);
+    if (++stage == Sm::kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
 
     // ------------------------------------------------------------------- the end of a head
-    const int32_t nt = tiles_of(use.len);
-    const bool done = use.t + 1 == nt;
+    const bool done = --use.left == 0;
     if (done || u + 1 == units) {
-      const bool whole = done && t0 == 0;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-        l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-        if (c == 0) {
-          sm.stat[warp][g + 8 * r][0] = m[r];
-          sm.stat[warp][g + 8 * r][1] = mo[r];
-          sm.stat[warp][g + 8 * r][2] = l[r];
-        }
+      const bool whole = done && from_start;
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (c == 0) {
+        sm.stat[warp][g][0] = m;
+        sm.stat[warp][g][1] = mo;
+        sm.stat[warp][g][2] = l;
       }
-      __syncthreads();
-      float f[2];
+      consumer_barrier();
+      float f[2];  // brings heads 2c and 2c + 1 to the largest M of the warps that share them
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+      for (int e = 0; e < 2; ++e) {
         float top = kLowest;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm.stat[w][g + 8 * r][1]);
-        f[r] = ex2(mo[r] - top);
+        for (int w = 0; w < kSlabs; ++w) top = fmaxf(top, sm.stat[group * kSlabs + w][2 * c + e][1]);
+        f[e] = ex2(sm.stat[warp][2 * c + e][1] - top);
       }
-      const int64_t slot = 2 * cta + (first_segment ? 0 : 1);
+      // Thread (warp, lane) finishes head 8r + warp of the item, column `lane` of each piece of 32.
+      const int64_t slot = 2 * static_cast<int64_t>(cta) + (first_segment ? 0 : 1);
       first_segment = false;
+      float norm[HG];
 #pragma unroll
-      for (int r = 0; r < (kWide ? 2 : 1); ++r) {
-        // Thread (warp, lane) finishes row 8*r + warp, column `lane` of each piece of 32.
-        const int row = 8 * r + warp;
+      for (int r = 0; r < HG; ++r) {
         float top = kLowest, topo = kLowest, sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          top = fmaxf(top, sm.stat[w][row][0]);
-          topo = fmaxf(topo, sm.stat[w][row][1]);
+        for (int w = 0; w < kSlabs; ++w) {
+          top = fmaxf(top, sm.stat[r * kSlabs + w][warp][0]);
+          topo = fmaxf(topo, sm.stat[r * kSlabs + w][warp][1]);
         }
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum = fmaf(sm.stat[w][row][2], ex2(sm.stat[w][row][0] - top), sum);
-        const float norm = sum == 0.f ? 0.f : ex2(topo - top) / sum;
-        const bool live_row = row < rows;
-        const int64_t orow = static_cast<int64_t>(use.b) * p.Hq + head0 + row;
-        if (live_row && lane == 0) {
-          if (whole) {
-            if (p.lse != nullptr) p.lse[orow] = sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * 0.693147180559945309f;
-          } else {
-            float* st = a.stats + (slot * kRows + row) * 4;
-            st[0] = top;
-            st[1] = topo;
-            st[2] = sum;
-          }
+        for (int w = 0; w < kSlabs; ++w)
+          sum = fmaf(sm.stat[r * kSlabs + w][warp][2], ex2(sm.stat[r * kSlabs + w][warp][0] - top), sum);
+        norm[r] = sum == 0.f ? 0.f : ex2(topo - top) / sum;
+        const int row = kHeads * r + warp;
+        if (row < rows && lane == 0) {
+          if (!whole)
+            *reinterpret_cast<float4*>(a.stats + (slot * Item<HG>::kRows + row) * 4) = make_float4(top, topo, sum, 0.f);
+          else if (p.lse != nullptr)
+            p.lse[static_cast<int64_t>(use.b) * p.Hq + head0 + row] =
+                sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * 0.693147180559945309f;
         }
-        auto piece = [&](int n0, int d) {  // output tiles n0..n0+3; d: the column this thread finishes
+      }
+      auto piece = [&](int n0, int d) {  // output tiles n0, n0 + 1; d: the column this thread finishes
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-            *reinterpret_cast<float4*>(&sm.join[warp][g][8 * c + 4 * h]) =
-                make_float4(o[n0][2 * r + h] * f[r], o[n0 + 1][2 * r + h] * f[r], o[n0 + 2][2 * r + h] * f[r],
-                            o[n0 + 3][2 * r + h] * f[r]);
-          __syncthreads();
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float4*>(&sm.join[warp][2 * c + e][4 * g]) =
+              make_float4(o[n0][e] * f[e], o[n0][2 + e] * f[e], o[n0 + 1][e] * f[e], o[n0 + 1][2 + e] * f[e]);
+        consumer_barrier();
+#pragma unroll
+        for (int r = 0; r < HG; ++r) {
           float v = 0.f;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) v += sm.join[w][warp][lane];
-          if (live_row && d < p.D) {
-            if (whole) Elem<T>::store1(p.out, orow * p.D + d, v * norm);
-            else a.part[(slot * kRows + row) * DP + d] = v;
+          for (int w = 0; w < kSlabs; ++w) v += sm.join[r * kSlabs + w][warp][lane];
+          const int row = kHeads * r + warp;
+          if (row < rows && d < p.D) {
+            if (whole) store_out(a.dtype, p.out, (static_cast<int64_t>(use.b) * p.Hq + head0 + row) * p.D + d, v * norm[r]);
+            else a.part[(slot * Item<HG>::kRows + row) * DP + d] = v;
           }
-          __syncthreads();
-        };
-        // Column `lane` of a piece is (c, h, j) = (lane / 8, lane / 4 % 2, lane % 4).
+        }
+        consumer_barrier();
+      };
 #pragma unroll
-        for (int i = 0; i < S::kV16; ++i)
+      for (int i = 0; i < S::kA; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            piece(i * 16 + 4 * k, 128 * i + 16 * (2 * (lane >> 3) + ((lane >> 2) & 1)) + 4 * k + (lane & 3));
-        if constexpr (S::kV8 > 0)
+        for (int k = 0; k < 4; ++k) piece(8 * i + 2 * k, 128 * i + 16 * (lane >> 2) + 4 * k + (lane & 3));
+      if constexpr (S::kB > 0)
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            piece(S::kV16 * 16 + 4 * k, 128 * S::kV16 + 8 * (2 * (lane >> 3) + ((lane >> 2) & 1)) + 4 * k + (lane & 3));
-      }
+        for (int k = 0; k < 2; ++k) piece(8 * S::kA + 2 * k, 128 * S::kA + 8 * (lane >> 2) + 4 * k + (lane & 3));
       fresh = true;
+      if (u + 1 < units) use.next_head(a);
     }
-    use.step(a);
   }
-  cp_wait<0>();
 }
 
 // Joins the partial results of one head: CTA (k, row) takes the head that CTA k of the first kernel began
 // inside. The warps share the parts, each in a fixed order.
-template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads) attention_join_kernel(const SplitArgs a) {
+template <int DP, int HG>
+__global__ void __launch_bounds__(kConsumers) attention_join_kernel(const __grid_constant__ SplitArgs a) {
+  constexpr int kRows = Item<HG>::kRows;
   constexpr int kV = DP / 64;  // float2 per lane
   __shared__ float2 sum[kWarps][DP / 2];
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -589,11 +814,13 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const SplitArg
   __syncthreads();
   const float norm = l == 0.f ? 0.f : ex2(topo - top) / l;
   const int64_t orow = static_cast<int64_t>(me.b) * p.Hq + me.item / a.chunks * a.G + kRows * (me.item % a.chunks) + row;
-  for (int d = threadIdx.x; 2 * d < p.D; d += kThreads) {
+  for (int d = threadIdx.x; 2 * d < p.D; d += kConsumers) {
     float2 r = make_float2(0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) r = add2(r, sum[w][d]);
-    static_cast<uint32_t*>(p.out)[(orow * p.D) / 2 + d] = Elem<T>::pack(make_float2(r.x * norm, r.y * norm));
+    const float2 y = make_float2(r.x * norm, r.y * norm);
+    static_cast<uint32_t*>(p.out)[(orow * p.D) / 2 + d] =
+        a.dtype == DT_BF16 ? Elem<__nv_bfloat16>::pack(y) : Elem<__half>::pack(y);
   }
   if (p.lse != nullptr && threadIdx.x == 0)
     p.lse[orow] = l == 0.f ? -CUDART_INF_F : (top + log2f(l)) * 0.693147180559945309f;
@@ -603,50 +830,91 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const SplitArg
 int padded(int64_t D) { return D <= 64 ? 64 : D <= 128 ? 128 : D <= 192 ? 192 : 256; }
 
 struct Plan {
-  int64_t grid, items_per_seq;
+  int64_t grid, units, chunks;  // units: at most
+  int hg;                       // warps that share a step's tokens
   bool join;
 };
 
 Plan plan_of(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
   Plan q;
-  const int64_t G = Hq / Hk, tiles = (max_len + kUnit - 1) / kUnit;
-  q.items_per_seq = Hk * ((G + kRows - 1) / kRows);
+  const int64_t G = Hq / Hk;
+  q.hg = G > kHeads ? 2 : 1;
+  const int64_t unit = kStep * kWarps / q.hg, rows = kHeads * q.hg;
+  const int64_t tiles = (max_len + unit - 1) / unit;
+  q.chunks = (G + rows - 1) / rows;
   const int64_t resident = static_cast<int64_t>(sm_count()) * (padded(D) <= 128 ? 2 : 1);
-  const __int128 units = static_cast<__int128>(B) * q.items_per_seq * tiles;
+  const __int128 units = static_cast<__int128>(B) * Hk * q.chunks * tiles;
+  q.units = units < 0x7fffffffLL ? static_cast<int64_t>(units) : 0x7fffffffLL;
   q.grid = units < resident ? static_cast<int64_t>(units) : resident;
   if (q.grid < 1) q.grid = 1;
   q.join = tiles > 1 && q.grid > 1;
   return q;
 }
 
-template <typename T, int DP, bool kWide>
-bool launch_dp(const SplitArgs& a, const Plan& plan, cudaStream_t s) {
-  auto kern = attention_split_kernel<T, DP, kWide>;
-  constexpr size_t smem = sizeof(Shared<DP>);
+template <int DP, int HG, bool kBoxes>
+bool launch_fed(const SplitArgs& a, const Maps& maps, const Plan& plan, cudaStream_t s) {
+  auto kern = attention_split_kernel<DP, HG, kBoxes>;
+  constexpr size_t smem = sizeof(Shared<DP, HG>) + 1024;
   static_assert(smem <= 227 * 1024 && (smem + 1024) * Shape<DP>::kCtas <= 228 * 1024, "the ring fits the SM");
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem)) return false;
-  kern<<<static_cast<unsigned>(plan.grid), kThreads, smem, s>>>(a);
+  kern<<<static_cast<unsigned>(plan.grid), kThreads, smem, s>>>(maps, a);
   if (!plan.join) return true;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(plan.grid - 1), a.G < kRows ? a.G : kRows);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.grid - 1), a.G < Item<HG>::kRows ? a.G : Item<HG>::kRows);
+  cfg.blockDim = dim3(kConsumers);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, attention_join_kernel<T, DP>, a);  // a failure is reported by the caller's check
+  cudaLaunchKernelEx(&cfg, attention_join_kernel<DP, HG>, a);  // a failure is reported by the caller's check
   return true;
 }
 
-template <typename T, bool kWide>
-bool launch_t(const SplitArgs& a, const Plan& plan, cudaStream_t s) {
+// Maps of the cache for the TMA feed; false where its layout has none (the rows are then copied one by one).
+template <int DP>
+bool cache_maps(const PagedArgs& p, int box_rows, Maps* m) {
+  const CacheView& c = p.cache;
+  const uint64_t dims[4] = {static_cast<uint64_t>(p.D), static_cast<uint64_t>(c.page_size), static_cast<uint64_t>(p.Hk),
+                            static_cast<uint64_t>(c.pages)};
+  // the stride of a dimension of one element is never used, but has to be a valid one
+  auto stride = [](int64_t extent, int64_t s) { return static_cast<uint64_t>(extent > 1 ? s : 256); };
+  const uint64_t strides[3] = {stride(c.page_size, c.token_stride), stride(p.Hk, c.head_stride), stride(c.pages, c.page_stride)};
+  for (uint64_t s : strides)
+    if (s >= (1ull << 40)) return false;
+  const uint32_t wide[4] = {128, static_cast<uint32_t>(box_rows), 1, 1}, narrow[4] = {64, static_cast<uint32_t>(box_rows), 1, 1};
+  bool ok = true;
+  if constexpr (Shape<DP>::kA > 0)
+    ok = ok && byte_tensor_map(&m->k128, 4, c.k, dims, strides, wide, CU_TENSOR_MAP_SWIZZLE_128B) &&
+         byte_tensor_map(&m->v128, 4, c.v, dims, strides, wide, CU_TENSOR_MAP_SWIZZLE_128B);
+  if constexpr (Shape<DP>::kB > 0)
+    ok = ok && byte_tensor_map(&m->k64, 4, c.k, dims, strides, narrow, CU_TENSOR_MAP_SWIZZLE_64B) &&
+         byte_tensor_map(&m->v64, 4, c.v, dims, strides, narrow, CU_TENSOR_MAP_SWIZZLE_64B);
+  return ok;
+}
+
+template <int DP, int HG>
+bool launch_dp(SplitArgs a, const Plan& plan, cudaStream_t s) {
+  const CacheView& c = a.p.cache;
+  Maps maps{};
+  // Rows per box: the largest power of two that divides a page, at most a unit.
+  a.box_shift = 0;
+  while (a.box_shift < 7 && (2 << a.box_shift) <= Item<HG>::kUnit && c.page_size % (2 << a.box_shift) == 0) ++a.box_shift;
+  if (a.box_shift < 3 || !cache_maps<DP>(a.p, 1 << a.box_shift, &maps)) return launch_fed<DP, HG, false>(a, maps, plan, s);
+  auto quad = [](int64_t extent, int64_t s) { return extent <= 1 || s % 4 == 0; };
+  a.bulk_scales = c.s_token_stride == 1 && quad(a.p.Hk, c.s_head_stride) && quad(c.pages, c.s_page_stride) &&
+                  (reinterpret_cast<uintptr_t>(c.k_scale) | reinterpret_cast<uintptr_t>(c.v_scale)) % 16 == 0;
+  return launch_fed<DP, HG, true>(a, maps, plan, s);
+}
+
+template <int HG>
+bool launch_hg(const SplitArgs& a, const Plan& plan, cudaStream_t s) {
   switch (padded(a.p.D)) {
-    case 64: return launch_dp<T, 64, kWide>(a, plan, s);
-    case 128: return launch_dp<T, 128, kWide>(a, plan, s);
-    case 192: return launch_dp<T, 192, kWide>(a, plan, s);
-    default: return launch_dp<T, 256, kWide>(a, plan, s);
+    case 64: return launch_dp<64, HG>(a, plan, s);
+    case 128: return launch_dp<128, HG>(a, plan, s);
+    case 192: return launch_dp<192, HG>(a, plan, s);
+    default: return launch_dp<256, HG>(a, plan, s);
   }
 }
 
@@ -655,25 +923,29 @@ bool launch_t(const SplitArgs& a, const Plan& plan, cudaStream_t s) {
 size_t attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
   const Plan plan = plan_of(B, Hq, Hk, D, max_len);
   if (!plan.join) return 0;
-  return static_cast<size_t>(plan.grid) * (sizeof(Meta) + 2 * kRows * (4 + padded(D)) * sizeof(float));
+  return static_cast<size_t>(plan.grid) * (sizeof(Meta) + 2 * kHeads * plan.hg * (4 + padded(D)) * sizeof(float));
 }
 
 bool launch_attention_split(const PagedArgs& p, int dtype, cudaStream_t s) {
   const Plan plan = plan_of(p.B, p.Hq, p.Hk, p.D, p.max_len);
-  if (plan.items_per_seq > 0x7fffffffLL) return false;
+  if (plan.units > 0x7fffffffLL - 0x10000) return false;  // units are counted in 32 bits
   SplitArgs a{};
   a.p = p;
   a.G = p.Hq / p.Hk;
-  a.chunks = (a.G + kRows - 1) / kRows;
+  a.chunks = static_cast<int32_t>(plan.chunks);
   a.slots = static_cast<int32_t>(2 * plan.grid);
+  a.status = device_status_ptr();
+  int lg = 0;
+  while ((1LL << lg) < p.cache.page_size) ++lg;
+  a.page_magic_shift = 31 + lg;
+  a.page_magic = static_cast<uint32_t>(((1ull << a.page_magic_shift) + p.cache.page_size - 1) / p.cache.page_size);
   if (plan.join) {
     a.meta = reinterpret_cast<Meta*>(p.partial);
     a.stats = reinterpret_cast<float*>(a.meta + plan.grid);
-    a.part = a.stats + static_cast<int64_t>(a.slots) * kRows * 4;
+    a.part = a.stats + static_cast<int64_t>(a.slots) * kHeads * plan.hg * 4;
   }
-  const bool wide = a.G > 8;
-  if (dtype == DT_BF16) return wide ? launch_t<__nv_bfloat16, true>(a, plan, s) : launch_t<__nv_bfloat16, false>(a, plan, s);
-  return wide ? launch_t<__half, true>(a, plan, s) : launch_t<__half, false>(a, plan, s);
+  a.dtype = dtype;
+  return plan.hg == 2 ? launch_hg<2>(a, plan, s) : launch_hg<1>(a, plan, s);
 }
 
 }  // namespace fq
