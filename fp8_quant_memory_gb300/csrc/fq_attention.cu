@@ -41,26 +41,29 @@ namespace {
 
 constexpr int kWarps = 8;                     // consumer warps
 constexpr int kConsumers = kWarps * 32;
-constexpr int kThreads = kConsumers + 32;     // + one producer warp
+constexpr int kProducers = 2;                 // producer warps
+constexpr int kThreads = kConsumers + 32 * kProducers;
 constexpr int kStep = 16;                     // tokens of one warp per unit
 constexpr int kHeads = 8;                     // query heads of one warp
 
-// A work item is one key head with kHeads * HG of its query heads; HG warps share each step's tokens.
-template <int HG>
+// A work item is one key head with kHeads * HG of its query heads. The consumer warps are slabs (16 tokens of
+// a unit each) x HG groups of heads x CG groups of 128 output columns; the column groups of a slab and head
+// group all take its score product, which is the smaller one, so that a thread never holds more than
+// 32 output accumulators and two CTAs fit an SM at every head size.
+template <int DP, int HG>
 struct Item {
-  static constexpr int kSlabs = kWarps / HG;      // steps of 16 tokens per unit
+  static constexpr int CG = DP > 128 ? 2 : 1;
+  static constexpr int kSlabs = kWarps / (HG * CG);
   static constexpr int kUnit = kStep * kSlabs;    // tokens per unit
   static constexpr int kRows = kHeads * HG;       // query heads
+  // Ring depth: what two CTAs per SM leave room for (98 KB of codes; 80 KB at head size 64, whose scales weigh more).
+  static constexpr int kStages = (DP == 64 ? 80 : 98) * 1024 / (2 * kUnit * DP);
 };
 constexpr float kLowest = -3.402823466e38f;  // below every score: a maximum before the first token
 
-// Ring depth (for units of 128 tokens; twice that for 64) and CTAs per SM by padded head size, from what
-// shared memory holds.
+// A unit's rows are stored as kA tiles of [rows][128 bytes], then kB of [rows][64], keys before values.
 template <int DP>
 struct Shape {
-  static constexpr int kCtas = DP <= 128 ? 2 : 1;
-  static constexpr int kStages = DP == 64 ? 5 : DP == 128 ? 3 : DP == 192 ? 4 : 3;
-  // A unit's rows are stored as kA tiles of [rows][128 bytes], then kB of [rows][64], keys before values.
   static constexpr int kA = DP / 128;
   static constexpr int kB = (DP % 128) / 64;
 };
@@ -73,11 +76,11 @@ constexpr int kJoinStride = 36;  // floats per joined row of 32: float4 stores w
 
 template <int DP, int HG>
 struct Shared {
-  static constexpr int kStages = Shape<DP>::kStages * HG;
-  static constexpr int kUnit = Item<HG>::kUnit;
+  static constexpr int kStages = Item<DP, HG>::kStages;
+  static constexpr int kUnit = Item<DP, HG>::kUnit;
   alignas(1024) unsigned char codes[kStages][2][kUnit * DP];  // K then V
   alignas(16) float scales[kStages][2][kUnit];  // K then V
-  uint32_t live[kStages][kUnit / 32];           // bit t % 32 of word t / 32: token t counts
+  uint16_t live[kStages][Item<DP, HG>::kSlabs];  // bit t of a slab's word: its token t counts
   alignas(16) float join[kWarps][kHeads][kJoinStride];
   float stat[kWarps][kHeads][3];  // m, M, l
   alignas(8) uint64_t full[kStages];
@@ -113,12 +116,12 @@ struct Maps {
 };
 
 __device__ __forceinline__ int32_t length_of(const PagedArgs& p, int32_t b) {
-  return static_cast<int32_t>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(__ldg(p.lens + b)), p.max_len)));
+  return max(0, min(__ldg(p.lens + b), p.max_len));
 }
 
-template <int HG>
+template <int DP, int HG>
 __device__ __forceinline__ int32_t tiles_of(int32_t len) {
-  return (len + Item<HG>::kUnit - 1) / Item<HG>::kUnit;
+  return (len + Item<DP, HG>::kUnit - 1) / Item<DP, HG>::kUnit;
 }
 
 __device__ __forceinline__ float ex2(float v) {
@@ -147,14 +150,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// N bytes into shared memory, or zeros (and nothing read) where `live` is false.
-template <int N>
-__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void* src, bool live) {
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(live ? N : 0)
-                 : "memory");
+// 16 bytes into shared memory, or zeros (and nothing read) where `live` is false; 4 bytes.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // e4m3 codes at the same byte of two words (tokens t, t+1) -> the fp16 pair of a B fragment; exact.
@@ -185,7 +187,7 @@ __device__ __forceinline__ float quad_max(float v) {
 
 // A place in the list of units: a work item of sequence b (key head item / chunks, and the item % chunks-th
 // part of its query heads) with `left` tiles to go, `len` tokens in all.
-template <int HG>
+template <int DP, int HG>
 struct Place {
   int32_t b, item, len, left;
 
@@ -196,7 +198,7 @@ struct Place {
       len = 0;
       while (len == 0 && ++b < a.p.B) len = length_of(a.p, b);
     }
-    left = tiles_of<HG>(len);
+    left = tiles_of<DP, HG>(len);
   }
 };
 
@@ -232,15 +234,20 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* scan, int32_t*
   return v + before;
 }
 
-// The producer warp, any page size and layout of scales: copies units `begin`..`begin + units - 1`, whose first is at `at`, into the ring.
+// A producer warp, any page size and layout of scales: copies its share (tokens kTok * half ..) of the units
+// from the one at `at` into the ring, 16 bytes a lane: lane (row, piece) copies the same piece of the key and of
+// the value row.
 template <int DP, int HG>
-__device__ __forceinline__ void produce_rows(const SplitArgs& a, Shared<DP, HG>& sm, Place<HG> at, int32_t units) {
+__device__ __forceinline__ void produce_rows(const SplitArgs& a, Shared<DP, HG>& sm, Place<DP, HG> at, int32_t units,
+                                             int half) {
   using S = Shape<DP>;
-  constexpr int kUnit = Item<HG>::kUnit, kQ = kUnit / 32, kStages = Shared<DP, HG>::kStages;
+  constexpr int kUnit = Item<DP, HG>::kUnit, kStages = Shared<DP, HG>::kStages;
+  constexpr int kTok = kUnit / kProducers;         // tokens of a unit that this warp copies
+  constexpr int kQ = (kTok + 31) / 32;             // words of 32 tokens, the last one may be half
   const PagedArgs& p = a.p;
   const CacheView& cache = p.cache;
   const int lane = threadIdx.x & 31;
-  int32_t tok = (tiles_of<HG>(at.len) - at.left) * kUnit + lane;  // this lane's tokens: tok + 32*q
+  int32_t tok = (tiles_of<DP, HG>(at.len) - at.left) * kUnit + kTok * half + lane;  // this lane's tokens: tok + 32*q
   int64_t head_off = 0, head_soff = 0;
   const int32_t* table = nullptr;
   auto enter = [&]() {
@@ -256,7 +263,8 @@ __device__ __forceinline__ void produce_rows(const SplitArgs& a, Shared<DP, HG>&
   int32_t page[kQ];
   auto look_up = [&]() {
 #pragma unroll
-    for (int q = 0; q < kQ; ++q) page[q] = tok + 32 * q < at.len ? __ldg(table + page_index(tok + 32 * q)) : -1;
+    for (int q = 0; q < kQ; ++q)
+      page[q] = tok + 32 * q < at.len && lane + 32 * q < kTok ? __ldg(table + page_index(tok + 32 * q)) : -1;
   };
   enter();
   look_up();
@@ -276,31 +284,33 @@ __device__ __forceinline__ void produce_rows(const SplitArgs& a, Shared<DP, HG>&
       const bool live = static_cast<uint32_t>(page[q]) < static_cast<uint32_t>(cache.pages);
       mask[q] = __ballot_sync(0xffffffffu, live);
       row[q] = live ? page[q] * cache.page_stride + head_off + off * cache.token_stride : -1;
-      if (mask[q] != 0u) {
-        const int64_t srow = live ? page[q] * cache.s_page_stride + head_soff + off * cache.s_token_stride : 0;
-        cp_async_or_zero<4>(smem_addr(&sm.scales[stage][0][32 * q + lane]), cache.k_scale + srow, live);
-        cp_async_or_zero<4>(smem_addr(&sm.scales[stage][1][32 * q + lane]), cache.v_scale + srow, live);
+      if (live) {
+        const int64_t srow = page[q] * cache.s_page_stride + head_soff + off * cache.s_token_stride;
+        cp_async4(smem_addr(&sm.scales[stage][0][kTok * half + 32 * q + lane]), cache.k_scale + srow);
+        cp_async4(smem_addr(&sm.scales[stage][1][kTok * half + 32 * q + lane]), cache.v_scale + srow);
       }
     }
     if (lane == 0)
 #pragma unroll
-      for (int q = 0; q < kQ; ++q) sm.live[stage][q] = mask[q];
+      for (int w = 0; w < kTok / kStep; ++w)
+        sm.live[stage][kTok / kStep * half + w] = static_cast<uint16_t>(mask[w >> 1] >> (16 * (w & 1)));
     const uint32_t kd = smem_addr(sm.codes[stage][0]), vd = smem_addr(sm.codes[stage][1]);
 #pragma unroll
-    for (int w = 0; w < Item<HG>::kSlabs; ++w) {
+    for (int w = 0; w < kTok / kStep; ++w) {
       const uint32_t here = (mask[w >> 1] >> (16 * (w & 1))) & 0xffffu;
       if (here == 0u) continue;
+      const int slab = kTok / kStep * half + w;
       if constexpr (S::kA > 0) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int r = (lane >> 3) + 4 * j, piece = lane & 7;
           const int64_t from = __shfl_sync(0xffffffffu, row[w >> 1], 16 * (w & 1) + r) + 16 * piece;
-          const int d = 2048 * w + spot128(r, piece);
+          const int d = 2048 * slab + spot128(r, piece);
 #pragma unroll
           for (int i = 0; i < S::kA; ++i) {
             const bool ok = from >= 16 * piece && 128 * i + 16 * piece < p.D;
-            cp_async_or_zero<16>(kd + 128 * kUnit * i + d, cache.k + (ok ? from + 128 * i : 0), ok);
-            cp_async_or_zero<16>(vd + 128 * kUnit * i + d, cache.v + (ok ? from + 128 * i : 0), ok);
+            cp_async16_or_zero(kd + 128 * kUnit * i + d, cache.k + (ok ? from + 128 * i : 0), ok);
+            cp_async16_or_zero(vd + 128 * kUnit * i + d, cache.v + (ok ? from + 128 * i : 0), ok);
           }
         }
       }
@@ -309,10 +319,10 @@ __device__ __forceinline__ void produce_rows(const SplitArgs& a, Shared<DP, HG>&
         for (int j = 0; j < 2; ++j) {
           const int r = (lane >> 2) + 8 * j, piece = lane & 3;
           const int64_t from = __shfl_sync(0xffffffffu, row[w >> 1], 16 * (w & 1) + r) + 16 * piece;
-          const int d = 128 * kUnit * S::kA + 1024 * w + spot64(r, piece);
+          const int d = 128 * kUnit * S::kA + 1024 * slab + spot64(r, piece);
           const bool ok = from >= 16 * piece && 128 * S::kA + 16 * piece < p.D;
-          cp_async_or_zero<16>(kd + d, cache.k + (ok ? from + 128 * S::kA : 0), ok);
-          cp_async_or_zero<16>(vd + d, cache.v + (ok ? from + 128 * S::kA : 0), ok);
+          cp_async16_or_zero(kd + d, cache.k + (ok ? from + 128 * S::kA : 0), ok);
+          cp_async16_or_zero(vd + d, cache.v + (ok ? from + 128 * S::kA : 0), ok);
         }
       }
     }
@@ -323,7 +333,7 @@ __device__ __forceinline__ void produce_rows(const SplitArgs& a, Shared<DP, HG>&
       tok += kUnit;
       if (--at.left == 0) {
         at.next_head(a);
-        tok = lane;
+        tok = kTok * half + lane;
         enter();
       }
       look_up();
@@ -349,16 +359,16 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
 // tokens of one page. Rows of a box behind the sequence's end are loaded too (they are inside the cache) and
 // masked by the consumers.
 template <int DP, int HG>
-__device__ __forceinline__ void produce_boxes(const SplitArgs& a, const Maps& maps, Shared<DP, HG>& sm, Place<HG> at,
+__device__ __forceinline__ void produce_boxes(const SplitArgs& a, const Maps& maps, Shared<DP, HG>& sm, Place<DP, HG> at,
                                               int32_t units) {
   using S = Shape<DP>;
-  constexpr int kUnit = Item<HG>::kUnit, kQ = kUnit / 32, kStages = Shared<DP, HG>::kStages;
+  constexpr int kUnit = Item<DP, HG>::kUnit, kQ = kUnit / 32, kStages = Shared<DP, HG>::kStages;
   const PagedArgs& p = a.p;
   const CacheView& cache = p.cache;
   const int lane = threadIdx.x & 31;
   const int rows = 1 << a.box_shift;
   const bool mine = (lane << a.box_shift) < kUnit;
-  int32_t base = (tiles_of<HG>(at.len) - at.left) * kUnit;  // the unit's first token
+  int32_t base = (tiles_of<DP, HG>(at.len) - at.left) * kUnit;  // the unit's first token
   int32_t head = 0;
   const int32_t* table = nullptr;
   auto enter = [&]() {
@@ -386,14 +396,16 @@ __device__ __forceinline__ void produce_boxes(const SplitArgs& a, const Maps& ma
     }
     const bool live = static_cast<uint32_t>(page) < static_cast<uint32_t>(cache.pages);
     const uint32_t boxes = __ballot_sync(0xffffffffu, live);
-    const int32_t tok = base + lane;
-    uint32_t mask = 0;
+    // Lane w makes the mask of slab w: the tokens whose box is live, up to the sequence's end.
+    if (lane < Item<DP, HG>::kSlabs) {
+      uint32_t mask = 0;
 #pragma unroll
-    for (int q = 0; q < kQ; ++q) {
-      const uint32_t b = __ballot_sync(0xffffffffu, ((boxes >> ((32 * q + lane) >> a.box_shift)) & 1u) != 0u && tok + 32 * q < at.len);
-      if (lane == q) mask = b;
+      for (int h = 0; h < 2; ++h)  // boxes are at least 8 rows
+        if ((boxes >> ((kStep * lane + 8 * h) >> a.box_shift)) & 1u) mask |= 0xffu << (8 * h);
+      const int32_t last = at.len - base - kStep * lane;
+      if (last < kStep) mask &= last > 0 ? (1u << last) - 1u : 0u;
+      sm.live[stage][lane] = static_cast<uint16_t>(mask);
     }
-    if (lane < kQ) sm.live[stage][lane] = mask;
     uint64_t* bar = &sm.full[stage];
     if (a.bulk_scales == 0) {
 #pragma unroll
@@ -404,8 +416,10 @@ __device__ __forceinline__ void produce_boxes(const SplitArgs& a, const Maps& ma
         const int64_t srow = have ? pg * cache.s_page_stride + head * cache.s_head_stride +
                                         (sl + ((32 * q + lane) & (rows - 1))) * cache.s_token_stride
                                   : 0;
-        cp_async_or_zero<4>(smem_addr(&sm.scales[stage][0][32 * q + lane]), cache.k_scale + srow, have);
-        cp_async_or_zero<4>(smem_addr(&sm.scales[stage][1][32 * q + lane]), cache.v_scale + srow, have);
+        if (have) {
+          cp_async4(smem_addr(&sm.scales[stage][0][32 * q + lane]), cache.k_scale + srow);
+          cp_async4(smem_addr(&sm.scales[stage][1][32 * q + lane]), cache.v_scale + srow);
+        }
       }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
     }
@@ -464,11 +478,11 @@ __device__ __forceinline__ void consumer_barrier() { asm volatile("bar.sync 1, %
 
 // kBoxes: fed by TMA boxes, else row by row.
 template <int DP, int HG, bool kBoxes>
-__global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas)
+__global__ void __launch_bounds__(kThreads, 2)
     attention_split_kernel(const __grid_constant__ Maps maps, const __grid_constant__ SplitArgs a) {
   using S = Shape<DP>;
   using Sm = Shared<DP, HG>;
-  constexpr int kSlabs = Item<HG>::kSlabs;
+  constexpr int kSlabs = Item<DP, HG>::kSlabs;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   // The swizzles repeat every 1024 bytes: align the ring to 1024.
   Sm& sm = *reinterpret_cast<Sm*>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
@@ -476,8 +490,27 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (kBoxes && threadIdx.x == kConsumers) {
+    if (S::kA > 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k128)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v128)) : "memory");
+    }
+    if (S::kB > 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k64)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v64)) : "memory");
+    }
+  }
+  // Bring the page table to the L2 cache while the lengths are on their way: one line per thread of the grid,
+  // as far as that goes.
+  if (p.max_len > 0) {
+    const uint32_t width = static_cast<uint32_t>((p.max_len - 1) / p.cache.page_size) + 1u;
+    const uint32_t i = (blockIdx.x * kThreads + threadIdx.x) * 32u, b = i / width;  // 32 entries per 128-byte line
+    if (b < static_cast<uint32_t>(p.B))
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + b * p.table_stride + (i - b * width)));
+  }
   if (threadIdx.x < Sm::kStages) {
-    mbar_init(&sm.full[threadIdx.x], kBoxes && a.bulk_scales != 0 ? 1 : 33);  // lane 0, and each lane's cp.async
+    // full: lane 0 of a producer for its masks and boxes, and each lane's own copies where there are any
+    mbar_init(&sm.full[threadIdx.x], kBoxes ? (a.bulk_scales != 0 ? 1 : 33) : 33 * kProducers);
     mbar_init(&sm.empty[threadIdx.x], kWarps);
     fence_barrier_init();
   }
@@ -489,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas)
   for (int32_t b0 = 0; b0 < p.B; b0 += kThreads) {
     const int32_t b = b0 + static_cast<int32_t>(threadIdx.x);
     const int32_t len = b < p.B ? length_of(p, b) : 0;
-    mine = tiles_of<HG>(len) * per_tile;
+    mine = tiles_of<DP, HG>(len) * per_tile;
     int32_t sum;
     incl = block_scan(mine, sm.scan, &sum);
     total += sum;
@@ -519,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas)
     int32_t carry = 0;
     for (int32_t b0 = 0; b0 < p.B && carry <= begin; b0 += kThreads) {
       const int32_t b = b0 + static_cast<int32_t>(threadIdx.x);
-      mine = b < p.B ? tiles_of<HG>(length_of(p, b)) * per_tile : 0;
+      mine = b < p.B ? tiles_of<DP, HG>(length_of(p, b)) * per_tile : 0;
       int32_t sum;
       incl = block_scan(mine, sm.scan, &sum) + carry;
       if (incl - mine <= begin && begin < incl) {
@@ -530,16 +563,16 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas)
     }
   }
   __syncthreads();
-  Place<HG> use;
+  Place<DP, HG> use;
   use.b = sm.start_b;
   use.len = length_of(p, use.b);
-  const int32_t nt = tiles_of<HG>(use.len);
+  const int32_t nt = tiles_of<DP, HG>(use.len);
   use.item = sm.start_unit / nt;
   const int32_t t = sm.start_unit - use.item * nt;
   use.left = nt - t;
-  if (warp == kWarps) {
-    if constexpr (kBoxes) produce_boxes<DP, HG>(a, maps, sm, use, units);
-    else produce_rows<DP, HG>(a, sm, use, units);
+  if (warp >= kWarps) {
+    if constexpr (!kBoxes) produce_rows<DP, HG>(a, sm, use, units, warp - kWarps);
+    else if (warp == kWarps) produce_boxes<DP, HG>(a, maps, sm, use, units);
     return;
   }
   if (threadIdx.x == 0 && a.meta != nullptr) {
@@ -555,11 +588,13 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas)
   }
 
   // --------------------------------------------------------------------------- the heads
-  const int slab = warp % kSlabs, group = warp / kSlabs;  // this warp's tokens of a unit and heads of an item
+  // This warp's tokens of a unit, columns and heads of an item.
+  constexpr int CG = Item<DP, HG>::CG;
+  const int slab = warp % kSlabs, cols = CG == 1 ? 0 : warp / kSlabs % CG, group = warp / (kSlabs * CG);
   uint4 q[DP / 64];
   float qf = 0.f, m = kLowest, mo = kLowest, l = 0.f;  // of head g, the same in the four threads of its row
   // Output tiles of 16 columns x 8 heads: o[n][2h + e] is column 16g + .. + h of head 2c + e.
-  constexpr int kN = DP / 16;
+  constexpr int kN = DP == 64 ? 4 : 8;
   float o[kN][4];
   bool first_segment = true;
   bool fresh = true, from_start = false;
@@ -571,10 +606,10 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas)
   for (int32_t u = 0; u < units; ++u) {
     if (fresh) {
       fresh = false;
-      from_start = use.left == tiles_of<HG>(use.len);
+      from_start = use.left == tiles_of<DP, HG>(use.len);
       const int32_t head = use.item / a.chunks, chunk = use.item - head * a.chunks;
-      rows = min(Item<HG>::kRows, a.G - Item<HG>::kRows * chunk);
-      head0 = head * a.G + Item<HG>::kRows * chunk;
+      rows = min(Item<DP, HG>::kRows, a.G - Item<DP, HG>::kRows * chunk);
+      head0 = head * a.G + Item<DP, HG>::kRows * chunk;
       const int32_t h = kHeads * group + g;
       const uint8_t* src = p.q + static_cast<int64_t>(use.b) * p.q_stride + static_cast<int64_t>(head0 + h) * p.D;
 #pragma unroll
@@ -592,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas)
       flag_failure(a.status);
       arrived = false;
     }
-    const uint32_t live = (sm.live[stage][slab >> 1] >> (16 * (slab & 1))) & 0xffffu;
+    const uint32_t live = sm.live[stage][slab];
     if (live != 0u) {
       const unsigned char* kt = sm.codes[stage][0];
       float s[2][4] = {};  // rows 8..15 of the score tile stay empty
@@ -637,12 +672,11 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas)
         }
       }
       const unsigned char* vt = sm.codes[stage][1];
-#pragma unroll
-      for (int i = 0; i < S::kA; ++i) {
+      if (S::kA > 0 && (S::kA == CG || cols == 0)) {
         uint4 v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          v[e] = *reinterpret_cast<const uint4*>(vt + 128 * Sm::kUnit * i + 2048 * slab +
+          v[e] = *reinterpret_cast<const uint4*>(vt + 128 * Sm::kUnit * cols + 2048 * slab +
                                                  spot128(2 * c + (e & 1) + 8 * (e >> 1), g));
         if (live != 0xffffu) {  // codes of tokens that do not count may be NaN: 0 * NaN must not reach the sum
 #pragma unroll
@@ -650,15 +684,14 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas)
             if (!((live >> (2 * c + (e & 1) + 8 * (e >> 1))) & 1u)) v[e] = make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kN / 2; ++k) {
           uint32_t lo[4], hi[4];
           pair_f16(word(v[0], k), word(v[1], k), lo);
           pair_f16(word(v[2], k), word(v[3], k), hi);
-          mma_f16(o[8 * i + 2 * k], lo[0], lo[1], hi[0], hi[1], p0, p1);
-          mma_f16(o[8 * i + 2 * k + 1], lo[2], lo[3], hi[2], hi[3], p0, p1);
+          mma_f16(o[2 * k], lo[0], lo[1], hi[0], hi[1], p0, p1);
+          mma_f16(o[2 * k + 1], lo[2], lo[3], hi[2], hi[3], p0, p1);
         }
-      }
-      if constexpr (S::kB > 0) {
+      } else if constexpr (S::kB > 0) {
         uint2 v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -674,8 +707,8 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas)
           uint32_t lo[4], hi[4];
           pair_f16(k == 0 ? v[0].x : v[0].y, k == 0 ? v[1].x : v[1].y, lo);
           pair_f16(k == 0 ? v[2].x : v[2].y, k == 0 ? v[3].x : v[3].y, hi);
-          mma_f16(o[8 * S::kA + 2 * k], lo[0], lo[1], hi[0], hi[1], p0, p1);
-          mma_f16(o[8 * S::kA + 2 * k + 1], lo[2], lo[3], hi[2], hi[3], p0, p1);
+          mma_f16(o[2 * k], lo[0], lo[1], hi[0], hi[1], p0, p1);
+          mma_f16(o[2 * k + 1], lo[2], lo[3], hi[2], hi[3], p0, p1);
         }
       }
     }
@@ -703,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas)
       for (int e = 0; e < 2; ++e) {
         float top = kLowest;
 #pragma unroll
-        for (int w = 0; w < kSlabs; ++w) top = fmaxf(top, sm.stat[group * kSlabs + w][2 * c + e][1]);
+        for (int w = 0; w < kSlabs; ++w) top = fmaxf(top, sm.stat[group * (CG * kSlabs) + w][2 * c + e][1]);
         f[e] = ex2(sm.stat[warp][2 * c + e][1] - top);
       }
       // Thread (warp, lane) finishes head 8r + warp of the item, column `lane` of each piece of 32.
@@ -715,48 +748,50 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas)
         float top = kLowest, topo = kLowest, sum = 0.f;
 #pragma unroll
         for (int w = 0; w < kSlabs; ++w) {
-          top = fmaxf(top, sm.stat[r * kSlabs + w][warp][0]);
-          topo = fmaxf(topo, sm.stat[r * kSlabs + w][warp][1]);
+          top = fmaxf(top, sm.stat[r * (CG * kSlabs) + w][warp][0]);
+          topo = fmaxf(topo, sm.stat[r * (CG * kSlabs) + w][warp][1]);
         }
 #pragma unroll
         for (int w = 0; w < kSlabs; ++w)
-          sum = fmaf(sm.stat[r * kSlabs + w][warp][2], ex2(sm.stat[r * kSlabs + w][warp][0] - top), sum);
+          sum = fmaf(sm.stat[r * (CG * kSlabs) + w][warp][2], ex2(sm.stat[r * (CG * kSlabs) + w][warp][0] - top), sum);
         norm[r] = sum == 0.f ? 0.f : ex2(topo - top) / sum;
         const int row = kHeads * r + warp;
         if (row < rows && lane == 0) {
           if (!whole)
-            *reinterpret_cast<float4*>(a.stats + (slot * Item<HG>::kRows + row) * 4) = make_float4(top, topo, sum, 0.f);
+            *reinterpret_cast<float4*>(a.stats + (slot * Item<DP, HG>::kRows + row) * 4) = make_float4(top, topo, sum, 0.f);
           else if (p.lse != nullptr)
             p.lse[static_cast<int64_t>(use.b) * p.Hq + head0 + row] =
                 sum == 0.f ? -CUDART_INF_F : (top + log2f(sum)) * 0.693147180559945309f;
         }
       }
-      auto piece = [&](int n0, int d) {  // output tiles n0, n0 + 1; d: the column this thread finishes
+      // Piece k: each thread's columns 4k..4k+3 of its two heads.
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          *reinterpret_cast<float4*>(&sm.join[warp][2 * c + e][4 * g]) =
-              make_float4(o[n0][e] * f[e], o[n0][2 + e] * f[e], o[n0 + 1][e] * f[e], o[n0 + 1][2 + e] * f[e]);
-        consumer_barrier();
+      for (int k = 0; k < kN / 2; ++k) {
+        const bool narrow = S::kA < CG && (S::kA == 0 || cols > 0);  // 8 columns a thread, not 16
+        if (!narrow || k < 2) {
 #pragma unroll
-        for (int r = 0; r < HG; ++r) {
-          float v = 0.f;
-#pragma unroll
-          for (int w = 0; w < kSlabs; ++w) v += sm.join[r * kSlabs + w][warp][lane];
-          const int row = kHeads * r + warp;
-          if (row < rows && d < p.D) {
-            if (whole) store_out(a.dtype, p.out, (static_cast<int64_t>(use.b) * p.Hq + head0 + row) * p.D + d, v * norm[r]);
-            else a.part[(slot * Item<HG>::kRows + row) * DP + d] = v;
-          }
+          for (int e = 0; e < 2; ++e)
+            *reinterpret_cast<float4*>(&sm.join[warp][2 * c + e][4 * g]) =
+                make_float4(o[2 * k][e] * f[e], o[2 * k][2 + e] * f[e], o[2 * k + 1][e] * f[e], o[2 * k + 1][2 + e] * f[e]);
         }
         consumer_barrier();
-      };
 #pragma unroll
-      for (int i = 0; i < S::kA; ++i)
+        for (int r = 0; r < HG; ++r)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) piece(8 * i + 2 * k, 128 * i + 16 * (lane >> 2) + 4 * k + (lane & 3));
-      if constexpr (S::kB > 0)
+          for (int y = 0; y < CG; ++y) {
+            const bool slim = y >= S::kA;
+            if (slim && k >= 2) continue;
+            float v = 0.f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) piece(8 * S::kA + 2 * k, 128 * S::kA + 8 * (lane >> 2) + 4 * k + (lane & 3));
+            for (int w = 0; w < kSlabs; ++w) v += sm.join[(r * CG + y) * kSlabs + w][warp][lane];
+            const int row = kHeads * r + warp, d = 128 * y + (slim ? 8 : 16) * (lane >> 2) + 4 * k + (lane & 3);
+            if (row < rows && d < p.D) {
+              if (whole) store_out(a.dtype, p.out, (static_cast<int64_t>(use.b) * p.Hq + head0 + row) * p.D + d, v * norm[r]);
+              else a.part[(slot * Item<DP, HG>::kRows + row) * DP + d] = v;
+            }
+          }
+        consumer_barrier();
+      }
       fresh = true;
       if (u + 1 < units) use.next_head(a);
     }
@@ -767,9 +802,10 @@ __global__ void __launch_bounds__(kThreads, Shape<DP>::kCtas)
 // inside. The warps share the parts, each in a fixed order.
 template <int DP, int HG>
 __global__ void __launch_bounds__(kConsumers) attention_join_kernel(const __grid_constant__ SplitArgs a) {
-  constexpr int kRows = Item<HG>::kRows;
+  constexpr int kRows = Item<DP, HG>::kRows;
   constexpr int kV = DP / 64;  // float2 per lane
   __shared__ float2 sum[kWarps][DP / 2];
+  __shared__ float4 stat[kWarps];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t k = blockIdx.x + 1;
   const Meta me = a.meta[k];
@@ -781,49 +817,70 @@ __global__ void __launch_bounds__(kConsumers) attention_join_kernel(const __grid
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int parts = static_cast<int>(me.last - k + 2);
   auto slot_of = [&](int i) { return i == 0 ? 2 * (k - 1) + me.slot : 2 * (k - 1 + i); };
-  float top = kLowest, topo = kLowest;
-  for (int i = lane; i < parts; i += 32) {
-    const float4 st = *reinterpret_cast<const float4*>(a.stats + (slot_of(i) * kRows + row) * 4);
-    top = fmaxf(top, st.x);
-    topo = fmaxf(topo, st.y);
-  }
-  top = group_max<32>(top);
-  topo = group_max<32>(topo);
-  float l = 0.f;
-  for (int i = lane; i < parts; i += 32) {
-    const float4 st = *reinterpret_cast<const float4*>(a.stats + (slot_of(i) * kRows + row) * 4);
-    l = fmaf(st.z, ex2(st.x - top), l);
-  }
-  l = group_sum<32>(l);
+  // Each warp's own running maxima, so that statistics and values are on their way at the same time.
+  float top = kLowest, topo = kLowest, l = 0.f;
   float2 v[kV];
 #pragma unroll
-  for (int i = 0; i < kV; ++i) v[i] = make_float2(0.f, 0.f);
-#pragma unroll 4
-  for (int i = warp; i < parts; i += kWarps) {
-    const int64_t at = slot_of(i) * kRows + row;
-    const float f = ex2(a.stats[at * 4 + 1] - topo);
+  for (int j = 0; j < kV; ++j) v[j] = make_float2(0.f, 0.f);
+  constexpr int kAhead = 4;
+  for (int i0 = warp; i0 < parts; i0 += kWarps * kAhead) {
+    float4 st[kAhead];
+    float2 x[kAhead][kV];
 #pragma unroll
-    for (int j = 0; j < kV; ++j) {
-      const int d = 2 * (lane + 32 * j);
-      const float2 x = d < p.D ? *reinterpret_cast<const float2*>(a.part + at * DP + d) : make_float2(0.f, 0.f);
-      v[j] = fma2(x, splat2(f), v[j]);
+    for (int e = 0; e < kAhead; ++e) {
+      const bool have = i0 + kWarps * e < parts;
+      const int64_t at = slot_of(have ? i0 + kWarps * e : i0) * kRows + row;
+      st[e] = have ? *reinterpret_cast<const float4*>(a.stats + at * 4) : make_float4(kLowest, kLowest, 0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < kV; ++j) {
+        const int d = 2 * (lane + 32 * j);
+        x[e][j] = have && d < p.D ? *reinterpret_cast<const float2*>(a.part + at * DP + d) : make_float2(0.f, 0.f);
+      }
     }
+    float mn = top, on = topo;
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      mn = fmaxf(mn, st[e].x);
+      on = fmaxf(on, st[e].y);
+    }
+    l *= ex2(top - mn);
+    const float keep = ex2(topo - on);
+#pragma unroll
+    for (int j = 0; j < kV; ++j) v[j] = mul2(v[j], splat2(keep));
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e) {
+      l = fmaf(st[e].z, ex2(st[e].x - mn), l);
+      const float f = ex2(st[e].y - on);
+#pragma unroll
+      for (int j = 0; j < kV; ++j) v[j] = fma2(x[e][j], splat2(f), v[j]);
+    }
+    top = mn;
+    topo = on;
   }
+  if (lane == 0) stat[warp] = make_float4(top, topo, l, 0.f);
 #pragma unroll
   for (int j = 0; j < kV; ++j) sum[warp][lane + 32 * j] = v[j];
   __syncthreads();
-  const float norm = l == 0.f ? 0.f : ex2(topo - top) / l;
+  float mj = kLowest, oj = kLowest, lj = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    mj = fmaxf(mj, stat[w].x);
+    oj = fmaxf(oj, stat[w].y);
+  }
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) lj = fmaf(stat[w].z, ex2(stat[w].x - mj), lj);
+  const float norm = lj == 0.f ? 0.f : ex2(oj - mj) / lj;
   const int64_t orow = static_cast<int64_t>(me.b) * p.Hq + me.item / a.chunks * a.G + kRows * (me.item % a.chunks) + row;
   for (int d = threadIdx.x; 2 * d < p.D; d += kConsumers) {
-    float2 r = make_float2(0.f, 0.f);
+    float2 y = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) r = add2(r, sum[w][d]);
-    const float2 y = make_float2(r.x * norm, r.y * norm);
+    for (int w = 0; w < kWarps; ++w) y = fma2(sum[w][d], splat2(ex2(stat[w].y - oj)), y);
+    y = mul2(y, splat2(norm));
     static_cast<uint32_t*>(p.out)[(orow * p.D) / 2 + d] =
         a.dtype == DT_BF16 ? Elem<__nv_bfloat16>::pack(y) : Elem<__half>::pack(y);
   }
   if (p.lse != nullptr && threadIdx.x == 0)
-    p.lse[orow] = l == 0.f ? -CUDART_INF_F : (top + log2f(l)) * 0.693147180559945309f;
+    p.lse[orow] = lj == 0.f ? -CUDART_INF_F : (mj + log2f(lj)) * 0.693147180559945309f;
 }
 
 // ---------------------------------------------------------------------------------- host side
@@ -839,10 +896,10 @@ Plan plan_of(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len) {
   Plan q;
   const int64_t G = Hq / Hk;
   q.hg = G > kHeads ? 2 : 1;
-  const int64_t unit = kStep * kWarps / q.hg, rows = kHeads * q.hg;
+  const int64_t unit = kStep * kWarps / (q.hg * (padded(D) > 128 ? 2 : 1)), rows = kHeads * q.hg;
   const int64_t tiles = (max_len + unit - 1) / unit;
   q.chunks = (G + rows - 1) / rows;
-  const int64_t resident = static_cast<int64_t>(sm_count()) * (padded(D) <= 128 ? 2 : 1);
+  const int64_t resident = static_cast<int64_t>(sm_count()) * 2;  // two CTAs per SM
   const __int128 units = static_cast<__int128>(B) * Hk * q.chunks * tiles;
   q.units = units < 0x7fffffffLL ? static_cast<int64_t>(units) : 0x7fffffffLL;
   q.grid = units < resident ? static_cast<int64_t>(units) : resident;
@@ -855,12 +912,12 @@ template <int DP, int HG, bool kBoxes>
 bool launch_fed(const SplitArgs& a, const Maps& maps, const Plan& plan, cudaStream_t s) {
   auto kern = attention_split_kernel<DP, HG, kBoxes>;
   constexpr size_t smem = sizeof(Shared<DP, HG>) + 1024;
-  static_assert(smem <= 227 * 1024 && (smem + 1024) * Shape<DP>::kCtas <= 228 * 1024, "the ring fits the SM");
+  static_assert(smem <= 227 * 1024 && (smem + 1024) * 2 <= 228 * 1024, "the ring fits the SM");
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem)) return false;
   kern<<<static_cast<unsigned>(plan.grid), kThreads, smem, s>>>(maps, a);
   if (!plan.join) return true;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(plan.grid - 1), a.G < Item<HG>::kRows ? a.G : Item<HG>::kRows);
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.grid - 1), a.G < Item<DP, HG>::kRows ? a.G : Item<DP, HG>::kRows);
   cfg.blockDim = dim3(kConsumers);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -900,8 +957,9 @@ bool launch_dp(SplitArgs a, const Plan& plan, cudaStream_t s) {
   Maps maps{};
   // Rows per box: the largest power of two that divides a page, at most a unit.
   a.box_shift = 0;
-  while (a.box_shift < 7 && (2 << a.box_shift) <= Item<HG>::kUnit && c.page_size % (2 << a.box_shift) == 0) ++a.box_shift;
-  if (a.box_shift < 3 || !cache_maps<DP>(a.p, 1 << a.box_shift, &maps)) return launch_fed<DP, HG, false>(a, maps, plan, s);
+  while ((2 << a.box_shift) <= Item<DP, HG>::kUnit && c.page_size % (2 << a.box_shift) == 0) ++a.box_shift;
+  // Small boxes cost the TMA unit as much as large ones (about 30 clocks each): below 1 KB rows are copied one by one.
+  if (a.box_shift < 3 || (DP << a.box_shift) < 1024 || !cache_maps<DP>(a.p, 1 << a.box_shift, &maps)) return launch_fed<DP, HG, false>(a, maps, plan, s);
   auto quad = [](int64_t extent, int64_t s) { return extent <= 1 || s % 4 == 0; };
   a.bulk_scales = c.s_token_stride == 1 && quad(a.p.Hk, c.s_head_stride) && quad(c.pages, c.s_page_stride) &&
                   (reinterpret_cast<uintptr_t>(c.k_scale) | reinterpret_cast<uintptr_t>(c.v_scale)) % 16 == 0;

@@ -53,7 +53,7 @@ struct PagedArgs {
   float* lse;  // nullable
   float* partial;
   int32_t B, Hq, Hk, D;
-  int64_t max_len;  // lengths are cut to this (the caller's bound and what the page table holds)
+  int32_t max_len;  // lengths are cut to this (the caller's bound and what the page table holds)
   float scale_log2;  // softmax_scale * log2(e)
 };
 

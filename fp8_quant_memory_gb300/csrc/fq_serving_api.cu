@@ -242,7 +242,7 @@ int fq_paged_attention(const uint8_t* q, int64_t q_stride, const float* q_scale,
   p.Hq = static_cast<int32_t>(Hq);
   p.Hk = static_cast<int32_t>(Hk);
   p.D = static_cast<int32_t>(D);
-  p.max_len = max_len;
+  p.max_len = static_cast<int32_t>(max_len);
   p.scale_log2 = softmax_scale * 1.44269504088896341f;
   const bool vec = D % 16 == 0 && aligned(q, 16) && (B == 1 || q_stride % 16 == 0) && cache_vec16(p.cache, Hk) &&
                    aligned(out, 16);

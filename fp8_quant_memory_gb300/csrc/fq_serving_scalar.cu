@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) attention_scalar_kernel(const PagedA
   const int32_t h = static_cast<int32_t>(row - b * a.Hq);
   const int32_t hk = h / (a.Hq / a.Hk);
   const CacheView& c = a.cache;
-  const int64_t len = max(static_cast<int64_t>(0), min(static_cast<int64_t>(a.lens[b]), a.max_len));
+  const int64_t len = max(static_cast<int64_t>(0), static_cast<int64_t>(min(a.lens[b], a.max_len)));
   const float qs = a.q_scale[b * a.q_scale_stride + h] * a.scale_log2;
   float q[kMaxD / 32], o[kMaxD / 32];
 #pragma unroll
