@@ -1,10 +1,322 @@
-// fq_matmul.cu -- choice of kernel for the matrix product and the append: every layout takes the
-// any-layout kernels of fq_serving_scalar.cu.
+// fq_matmul.cu -- the block-scaled FP8 matrix product on the 5th-generation tensor cores.
+//
+// Mathematics: out[i, j] = sum over blocks g of 128 k of sa[i, g] sb[j/128, g] P_g[i, j], P_g = sum of a[i, k]
+// b[j, k] over the block. A block is one 128-byte swizzled row of a tile, four tcgen05.mma of 32 k; its product
+// P_g is complete in tensor memory, so the epilogue warps read it once per block and add it, scaled, to fp32
+// accumulators in registers: one FMA per output and block, against 128 products on the tensor cores.
+//
+// What bounds it. Per SM and clock the tensor cores take 8192 e4m3 products; a 128 x 256 block of 128 k is 512
+// clocks. The epilogue of the same block is 128 clocks of FMA pairs and 128 of tensor-memory reads per warp, two
+// warps per scheduler, under the products of the next block (two accumulator buffers). With few rows the weights'
+// bytes bound it: HBM.
+//
+// Two kernels:
+//   wide   (many rows): CTA pairs, tiles of 256 rows x NT columns, rows of `a` on the tensor-memory lanes, so a
+//          thread owns an output row and its scale of `a` is one register; persistent, outputs staged in shared
+//          memory and stored by TMA.
+//   narrow (few rows): weight rows on the lanes, NT rows of `a` as columns, so that the weights stream through
+//          the large operand whatever the number of rows; the k range is split over the CTAs of a cluster, which
+//          add their partial sums through distributed shared memory in rank order (no workspace, no atomics, the
+//          same bits every time).
+//
+// Waits are bounded (fq_sync.cuh): a role that gives up flags the device status word and leaves its loop, the
+// others follow when their own waits run out, and tensor memory is freed either way.
+#include "fq_device.cuh"
 #include "fq_serving.h"
+#include "fq_tcgen05.cuh"
+#include "fq_tensormap.h"
 
 namespace fq {
+namespace {
 
-bool launch_matmul_tc(const MatmulArgs&, int, cudaStream_t) { return false; }
+constexpr int kBK = 128;  // k per stage: one scale block, one swizzled row
+
+struct MmArgs {
+  const float* sa;
+  const float* sb;
+  int64_t sa_stride, sb_stride;
+  void* out;
+  int64_t out_stride;
+  unsigned int* status;
+  int32_t M, N, nkb;
+  int32_t tiles_m, tiles_n;
+  int32_t dtype;
+  int32_t tma_store;  // wide: out has a tensor map
+};
+
+__device__ __forceinline__ void store_out(int dtype, void* out, int64_t i, float v) {
+  if (dtype == DT_BF16) Elem<__nv_bfloat16>::store1(out, i, v);
+  else Elem<__half>::store1(out, i, v);
+}
+
+// ================================================================================= narrow
+constexpr int kNarrowThreads = 192;  // four epilogue warps, producer, products
+
+template <int NT>
+struct Narrow {
+  static constexpr int kCtas = NT <= 64 ? 2 : 1;  // per SM: 128 accumulators a thread leave room for one
+  static constexpr int kStageBytes = (128 + NT) * kBK;
+  static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : 6;
+  static constexpr int kBufs = NT == 128 ? 2 : 4;
+  static constexpr uint32_t kCols = NT * kBufs < 32 ? 32 : NT * kBufs;  // 64, 128, 256, 256
+};
+
+template <int NT>
+struct NarrowShared {
+  alignas(1024) unsigned char ring[Narrow<NT>::kStages][Narrow<NT>::kStageBytes];  // weights, then rows of a
+  alignas(16) float scale[4][2][NT];                                              // per epilogue warp, two blocks
+  alignas(8) uint64_t full[Narrow<NT>::kStages];
+  uint64_t empty[Narrow<NT>::kStages];
+  uint64_t done[Narrow<NT>::kBufs];   // a block's products are in tensor memory
+  uint64_t free_[Narrow<NT>::kBufs];  // and have been read
+  uint32_t tmem;
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kNarrowThreads, Narrow<NT>::kCtas)
+    matmul_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
+                                                                      const __grid_constant__ CUtensorMap amap,
+                                                                      const __grid_constant__ MmArgs p) {
+  using C = Narrow<NT>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  // The swizzle repeats every 1024 bytes: align the ring to 1024.
+  NarrowShared<NT>& sm = *reinterpret_cast<NarrowShared<NT>*>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = gridDim.x, rank = blockIdx.x;  // the cluster is the whole x axis
+  const int n0 = blockIdx.y * 128, t0 = blockIdx.z * NT;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.nkb) * rank / split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (rank + 1) / split);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int b = 0; b < C::kBufs; ++b) {
+      mbar_init(&sm.done[b], 1);
+      mbar_init(&sm.free_[b], 4);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 5) tmem_alloc<1>(&sm.tmem, C::kCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  if (warp == 4) {
+    // ------------------------------------------------------------------------ producer
+    if (lane == 0) {
+      int s = 0;
+      uint32_t phase = 1;
+      int k = kb0;
+      for (; k < kb1; ++k) {
+        if (k - kb0 >= C::kStages && !mbar_wait(kWaitLimitNs, &sm.empty[s], phase)) break;
+        mbar_arrive_expect_tx(&sm.full[s], C::kStageBytes);
+        tma_load_2d(sm.ring[s], &wmap, k * kBK, n0, &sm.full[s]);
+        tma_load_2d(sm.ring[s] + 128 * kBK, &amap, k * kBK, t0, &sm.full[s]);
+        if (++s == C::kStages) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+      if (k < kb1) {
+        flag_failure(p.status);
+        // Let the copies already issued land before this CTA's shared memory goes away.
+        for (int j = max(0, k - kb0 - C::kStages); j < k - kb0; ++j)
+          if (!mbar_wait(kWaitLimitNs, &sm.full[j % C::kStages], static_cast<uint32_t>(j / C::kStages) & 1u)) break;
+      }
+    }
+  } else if (warp == 5) {
+    // ------------------------------------------------------------------------ products
+    if (lane == 0) {
+      constexpr uint32_t idesc = e4m3_idesc(128, NT);
+      int s = 0, b = 0;
+      uint32_t phase = 0, bphase = 1;
+      bool ok = true;
+      for (int k = kb0; k < kb1 && ok; ++k) {
+        ok = (k - kb0 < C::kBufs || mbar_wait(kWaitLimitNs, &sm.free_[b], bphase)) &&
+             mbar_wait(kWaitLimitNs, &sm.full[s], phase);
+        if (!ok) {
+          flag_failure(p.status);
+          break;
+        }
+        tc_fence_after();
+        const uint64_t wd = tile_desc(smem_addr(sm.ring[s])), ad = tile_desc(smem_addr(sm.ring[s] + 128 * kBK));
+#pragma unroll
+        for (int i = 0; i < kBK / 32; ++i) mma_e4m3_tile<1>(tmem + b * NT, wd + 2 * i, ad + 2 * i, idesc, i > 0);
+        mma_commit<1>(&sm.empty[s]);
+        mma_commit<1>(&sm.done[b]);
+        if (++s == C::kStages) {
+          s = 0;
+          phase ^= 1u;
+        }
+        if (++b == C::kBufs) {
+          b = 0;
+          bphase ^= 1u;
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------------ epilogue
+    // Thread (warp, lane) owns weight row n0 + 32*warp + lane; acc[j] is row t0 + j of a.
+    float2 acc[NT / 2];
+#pragma unroll
+    for (int j = 0; j < NT / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const float* sb = p.sb + static_cast<int64_t>(blockIdx.y) * p.sb_stride;
+    constexpr int kL = (NT + 31) / 32;  // scales of a that a lane brings per block
+    float next[kL];
+    auto fetch = [&](int k) {
+      const float b = __ldg(sb + k);
+#pragma unroll
+      for (int i = 0; i < kL; ++i) {
+        const int j = lane + 32 * i;
+        next[i] = j < NT && t0 + j < p.M ? __ldg(p.sa + static_cast<int64_t>(t0 + j) * p.sa_stride + k) * b : 0.f;
+      }
+    };
+    if (kb0 < kb1) fetch(kb0);
+    int b = 0;
+    uint32_t phase = 0;
+    for (int k = kb0; k < kb1; ++k) {
+      float* sc = sm.scale[warp][k & 1];
+#pragma unroll
+      for (int i = 0; i < kL; ++i)
+        if (lane + 32 * i < NT) sc[lane + 32 * i] = next[i];
+      __syncwarp();  // the other buffer's readers have passed the last block's barrier
+      if (k + 1 < kb1) fetch(k + 1);
+      // one verdict for the whole warp: the loads below are collective
+      if (!__all_sync(0xffffffffu, mbar_wait(kWaitLimitNs, &sm.done[b], phase))) {
+        flag_failure(p.status);
+        break;
+      }
+      tc_fence_after();
+      uint32_t d[NT < 32 ? 16 : 32];
+#pragma unroll
+      for (int c = 0; c < (NT + 31) / 32; ++c) {
+        if constexpr (NT < 32) tmem_ld16(lanes + b * NT, d);
+        else tmem_ld32(lanes + b * NT + 32 * c, d);
+        tmem_wait_ld();
+        if (c == (NT + 31) / 32 - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.free_[b]);
+        }
+#pragma unroll
+        for (int j = 0; j < (NT < 32 ? 16 : 32); j += 4) {
+          const float4 s4 = *reinterpret_cast<const float4*>(sc + 32 * c + j);
+          float2& lo = acc[16 * c + j / 2];
+          float2& hi = acc[16 * c + j / 2 + 1];
+          lo = fma2(make_float2(__uint_as_float(d[j]), __uint_as_float(d[j + 1])), make_float2(s4.x, s4.y), lo);
+          hi = fma2(make_float2(__uint_as_float(d[j + 2]), __uint_as_float(d[j + 3])), make_float2(s4.z, s4.w), hi);
+        }
+      }
+      if (++b == C::kBufs) {
+        b = 0;
+        phase ^= 1u;
+      }
+    }
+    const int row = 32 * warp + lane;
+    if (split == 1) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        if (t0 + j < p.M && n0 + row < p.N)
+          store_out(p.dtype, p.out, static_cast<int64_t>(t0 + j) * p.out_stride + n0 + row, j & 1 ? acc[j / 2].y : acc[j / 2].x);
+    } else {
+      // The ring is free: every stage's products have been read. [NT][128] fp32 partial sums.
+      float* part = reinterpret_cast<float*>(sm.ring);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) part[j * 128 + row] = j & 1 ? acc[j / 2].y : acc[j / 2].x;
+    }
+  }
+  if (split > 1) {
+    __syncwarp();
+    cluster_barrier();
+    if (warp < 4) {
+      const int row = 32 * warp + lane;
+      const float* part = reinterpret_cast<const float*>(sm.ring);
+      const int live = min(NT, p.M - t0);
+      for (int j = rank; j < live; j += split) {
+        float v = 0.f;
+        for (int r = 0; r < split; ++r) {
+          float x;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(in_cta(part + j * 128 + row, r)));
+          v += x;
+        }
+        if (n0 + row < p.N) store_out(p.dtype, p.out, static_cast<int64_t>(t0 + j) * p.out_stride + n0 + row, v);
+      }
+    }
+    __syncwarp();
+    cluster_barrier();  // nobody leaves while its partial sums are read
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) tmem_free<1>(tmem, C::kCols);
+}
+
+template <int NT>
+bool launch_narrow(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
+  CUtensorMap wmap, amap;
+  const uint64_t wd[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.N)}, ws[1] = {static_cast<uint64_t>(a.b_stride)};
+  const uint64_t ad[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.M)}, as[1] = {static_cast<uint64_t>(a.a_stride)};
+  const uint32_t wb[2] = {kBK, 128}, ab[2] = {kBK, NT};
+  if (!byte_tensor_map(&wmap, 2, a.b, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !byte_tensor_map(&amap, 2, a.a, ad, as, ab, CU_TENSOR_MAP_SWIZZLE_128B))
+    return false;
+  p.tiles_n = static_cast<int32_t>((a.N + 127) / 128);
+  p.tiles_m = static_cast<int32_t>((a.M + NT - 1) / NT);
+  if (p.tiles_n > 65535 || p.tiles_m > 65535) return false;
+  // Split k as far as that fills the SMs, at most a cluster of 8, at least one block each.
+  const int64_t tiles = static_cast<int64_t>(p.tiles_n) * p.tiles_m;
+  int64_t split = Narrow<NT>::kCtas * static_cast<int64_t>(sm_count()) / tiles;
+  if (split > 8) split = 8;
+  if (split > p.nkb) split = p.nkb;
+  if (split < 1) split = 1;
+  auto kern = matmul_narrow_kernel<NT>;
+  constexpr size_t smem = sizeof(NarrowShared<NT>) + 1024;
+  static_assert((smem + 1024) * Narrow<NT>::kCtas <= 228 * 1024, "the CTAs fit the SM");
+  static_assert(NT * 128 * 4 <= Narrow<NT>::kStages * Narrow<NT>::kStageBytes, "the partial sums fit the ring");
+  if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem)) return false;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(split), static_cast<unsigned>(p.tiles_n), static_cast<unsigned>(p.tiles_m));
+  cfg.blockDim = dim3(kNarrowThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kern, wmap, amap, p);  // a failure is reported by the caller's check
+  return true;
+}
+
+}  // namespace
+
+bool launch_matmul_tc(const MatmulArgs& a, int dtype, cudaStream_t s) {
+  MmArgs p{};
+  p.sa = a.a_scale;
+  p.sb = a.b_scale;
+  p.sa_stride = a.a_scale_stride;
+  p.sb_stride = a.b_scale_stride;
+  p.out = a.out;
+  p.out_stride = a.out_stride;
+  p.status = device_status_ptr();
+  p.M = static_cast<int32_t>(a.M);
+  p.N = static_cast<int32_t>(a.N);
+  p.nkb = static_cast<int32_t>(a.groups);
+  p.dtype = dtype;
+  MatmulArgs b = a;
+  // a single row's stride is never used, but has to be a valid one
+  if (b.M == 1) b.a_stride = (b.K + 15) / 16 * 16;
+  if (b.N == 1) b.b_stride = (b.K + 15) / 16 * 16;
+  if (a.M <= 16) return launch_narrow<16>(b, p, s);
+  if (a.M <= 32) return launch_narrow<32>(b, p, s);
+  if (a.M <= 64) return launch_narrow<64>(b, p, s);
+  return launch_narrow<128>(b, p, s);
+}
+
 bool launch_append_vector(const AppendArgs&, int, int, cudaStream_t) { return false; }
 
 }  // namespace fq
