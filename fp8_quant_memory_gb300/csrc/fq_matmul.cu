@@ -44,6 +44,10 @@ struct MmArgs {
   int32_t tma_store;  // wide: out has a tensor map
 };
 
+__device__ __forceinline__ uint32_t pack_out(int dtype, float2 v) {
+  return dtype == DT_BF16 ? Elem<__nv_bfloat16>::pack(v) : Elem<__half>::pack(v);
+}
+
 __device__ __forceinline__ void store_out(int dtype, void* out, int64_t i, float v) {
   if (dtype == DT_BF16) Elem<__nv_bfloat16>::store1(out, i, v);
   else Elem<__half>::store1(out, i, v);
@@ -292,6 +296,264 @@ bool launch_narrow(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
   return true;
 }
 
+// =================================================================================== wide
+// Warpgroup 0: producer (warp 0), products (warp 1), two idle warps; warpgroups 1 and 2: epilogue. The epilogue's
+// registers come from warpgroup 0: 384 x 168 at launch = 128 x 40 + 256 x 232.
+constexpr int kWideThreads = 384;
+constexpr int kIdleRegs = 40, kEpiRegs = 232;
+
+template <int NT>
+struct Wide {
+  static constexpr int kStageBytes = (128 + NT / 2) * kBK;  // one CTA's half of the pair's operands
+  static constexpr int kStages = 192 * 1024 / kStageBytes < 8 ? 192 * 1024 / kStageBytes : 8;
+  static constexpr int kHalf = NT / 2;                      // columns per epilogue warp
+  static constexpr int kChunks = kHalf / 32;
+  static_assert(kHalf % 64 == 0, "a warp's columns are whole boxes of 64");
+};
+
+template <int NT>
+struct WideShared {
+  alignas(1024) unsigned char ring[Wide<NT>::kStages][Wide<NT>::kStageBytes];  // rows of a, then columns' weights
+  alignas(1024) unsigned char out[8][32 * 128];                                // per epilogue warp: 32 rows x 64 columns
+  alignas(8) uint64_t full[Wide<NT>::kStages];   // leader: both CTAs' operands have landed
+  uint64_t empty[Wide<NT>::kStages];             // both: the products have read them
+  uint64_t done[2];                              // both: a block's products are in tensor memory
+  uint64_t free_[2];                             // leader: all sixteen epilogue warps have read them
+  uint32_t tmem;
+};
+
+struct Tile {
+  int m, n;
+};
+
+// The t-th tile, eight tile rows at a time: CTA pairs that run together share operand rows in L2.
+__device__ __forceinline__ Tile tile_at(const MmArgs& p, int t) {
+  constexpr int kRowsAtATime = 8;
+  const int per = kRowsAtATime * p.tiles_n, group = t / per, in = t - group * per;
+  const int rows = min(kRowsAtATime, p.tiles_m - group * kRowsAtATime);
+  const int n = in / rows;
+  return {group * kRowsAtATime + in - n * rows, n};
+}
+
+template <int NT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
+    matmul_wide_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
+                       const __grid_constant__ CUtensorMap omap, const __grid_constant__ MmArgs p) {
+  using C = Wide<NT>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  // The swizzle repeats every 1024 bytes: align to 1024 (the same offset in both CTAs).
+  WideShared<NT>& sm = *reinterpret_cast<WideShared<NT>*>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pairs = gridDim.x / 2, first = blockIdx.x / 2, tiles = p.tiles_m * p.tiles_n;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&sm.done[b], 1);
+      mbar_init(&sm.free_[b], 16);
+    }
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc<2>(&sm.tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_barrier();  // the peer's barriers exist before anything arrives on them
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIdleRegs));
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------------------- producer
+      int s = 0;
+      uint32_t phase = 1;
+      int64_t k = 0;  // stages issued
+      bool ok = true;
+      for (int t = first; t < tiles && ok; t += pairs) {
+        const Tile at = tile_at(p, t);
+        const int arow = at.m * 256 + 128 * static_cast<int>(rank), wrow = at.n * NT + (NT / 2) * static_cast<int>(rank);
+        for (int kb = 0; kb < p.nkb; ++kb, ++k) {
+          if (k >= C::kStages && !mbar_wait(kWaitLimitNs, &sm.empty[s], phase)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * C::kStageBytes);
+          const uint32_t bar = in_cta(&sm.full[s], 0);
+          tma_load_2d_pair(sm.ring[s], &amap, kb * kBK, arow, bar);
+          tma_load_2d_pair(sm.ring[s] + 128 * kBK, &wmap, kb * kBK, wrow, bar);
+          if (++s == C::kStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {
+        flag_failure(p.status);
+        // Let the copies already issued land before this CTA's shared memory goes away: the leader sees both
+        // CTAs' on its barriers; the cluster barrier at the end keeps the peer.
+        if (rank == 0)
+          for (int64_t j = max(static_cast<int64_t>(0), k - C::kStages); j < k; ++j)
+            if (!mbar_wait(kWaitLimitNs, &sm.full[j % C::kStages], static_cast<uint32_t>(j / C::kStages) & 1u)) break;
+      }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ---------------------------------------------------------------------- products
+      constexpr uint32_t idesc = e4m3_idesc(256, NT);
+      int s = 0, b = 0;
+      uint32_t phase = 0, bphase = 1;
+      bool ok = true;
+      int64_t k = 0;
+      for (int t = first; t < tiles && ok; t += pairs) {
+        for (int kb = 0; kb < p.nkb; ++kb, ++k) {
+          ok = (k < 2 || mbar_wait(kWaitLimitNs, &sm.free_[b], bphase)) && mbar_wait(kWaitLimitNs, &sm.full[s], phase);
+          if (!ok) {
+            flag_failure(p.status);
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = tile_desc(smem_addr(sm.ring[s])), wd = tile_desc(smem_addr(sm.ring[s] + 128 * kBK));
+#pragma unroll
+          for (int i = 0; i < kBK / 32; ++i) mma_e4m3_tile<2>(tmem + b * 256, ad + 2 * i, wd + 2 * i, idesc, i > 0);
+          mma_commit<2>(&sm.empty[s]);
+          mma_commit<2>(&sm.done[b]);
+          if (++s == C::kStages) {
+            s = 0;
+            phase ^= 1u;
+          }
+          b ^= 1;
+          if (b == 0) bphase ^= 1u;
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------------ epilogue
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
+    const int quarter = warp & 3, half = (warp - 4) >> 2;  // lanes 32*quarter.., columns kHalf*half..
+    const uint32_t from = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + C::kHalf * half;
+    unsigned char* stage = sm.out[warp - 4];
+    const uint32_t free0 = in_cta(&sm.free_[0], 0), free1 = in_cta(&sm.free_[1], 0);
+    int b = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = first; t < tiles && ok; t += pairs) {
+      const Tile at = tile_at(p, t);
+      const int row0 = at.m * 256 + 128 * static_cast<int>(rank) + 32 * quarter, col0 = at.n * NT + C::kHalf * half;
+      const float* sa = p.sa + static_cast<int64_t>(min(row0 + lane, p.M - 1)) * p.sa_stride;
+      // The scale block of each 64 columns (a tile's columns start at a multiple of 64).
+      const float* sb[(C::kHalf + 63) / 64];
+#pragma unroll
+      for (int c = 0; c < (C::kHalf + 63) / 64; ++c)
+        sb[c] = p.sb + static_cast<int64_t>(min(col0 + 64 * c, p.N - 1) / kScaleBlock) * p.sb_stride;
+      float2 acc[C::kHalf / 2];
+#pragma unroll
+      for (int j = 0; j < C::kHalf / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+      float a_next = __ldg(sa), b_next[(C::kHalf + 63) / 64];
+#pragma unroll
+      for (int c = 0; c < (C::kHalf + 63) / 64; ++c) b_next[c] = __ldg(sb[c]);
+      for (int kb = 0; kb < p.nkb; ++kb) {
+        float sc[(C::kHalf + 63) / 64];
+#pragma unroll
+        for (int c = 0; c < (C::kHalf + 63) / 64; ++c) sc[c] = a_next * b_next[c];
+        if (kb + 1 < p.nkb) {
+          a_next = __ldg(sa + kb + 1);
+#pragma unroll
+          for (int c = 0; c < (C::kHalf + 63) / 64; ++c) b_next[c] = __ldg(sb[c] + kb + 1);
+        }
+        // one verdict for the whole warp: the loads below are collective
+        if (!__all_sync(0xffffffffu, mbar_wait(kWaitLimitNs, &sm.done[b], phase))) {
+          flag_failure(p.status);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        uint32_t d[2][32];
+        tmem_ld32(from + b * 256, d[0]);
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c) {
+          tmem_wait_ld();
+          if (c + 1 < C::kChunks) {
+            tmem_ld32(from + b * 256 + 32 * (c + 1), d[(c + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(b == 0 ? free0 : free1);
+          }
+          const float2 s2 = splat2(sc[c / 2]);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float2& x = acc[16 * c + j / 2];
+            x = fma2(make_float2(__uint_as_float(d[c & 1][j]), __uint_as_float(d[c & 1][j + 1])), s2, x);
+          }
+        }
+        b ^= 1;
+        if (b == 0) phase ^= 1u;
+      }
+      if (!ok) break;
+      if (p.tma_store) {
+        // 64 columns at a time: swizzled rows of 128 bytes, one box per warp.
+#pragma unroll
+        for (int c = 0; c < (C::kHalf + 63) / 64; ++c) {
+          if (lane == 0) bulk_wait_read();  // the last box has left the staging rows
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            if (64 * c + 8 * e < C::kHalf) {
+              const float2* v = &acc[32 * c + 4 * e];
+              *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                  make_uint4(pack_out(p.dtype, v[0]), pack_out(p.dtype, v[1]), pack_out(p.dtype, v[2]), pack_out(p.dtype, v[3]));
+            }
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            if (row0 < p.M && col0 + 64 * c < p.N) tma_store_2d(&omap, 2 * (col0 + 64 * c), row0, stage);
+            bulk_commit();
+          }
+        }
+      } else if (row0 + lane < p.M) {
+        const int64_t at0 = static_cast<int64_t>(row0 + lane) * p.out_stride + col0;
+#pragma unroll
+        for (int j = 0; j < C::kHalf; ++j)
+          if (col0 + j < p.N) store_out(p.dtype, p.out, at0 + j, j & 1 ? acc[j / 2].y : acc[j / 2].x);
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  __syncwarp();
+  cluster_barrier();  // no CTA leaves while its peer's products, arrivals or copies refer to it
+  tc_fence_after();
+  if (warp == 1) tmem_free<2>(tmem, 512);
+}
+
+template <int NT>
+bool launch_wide(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
+  CUtensorMap amap, wmap, omap{};
+  const uint64_t ad[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.M)}, as[1] = {static_cast<uint64_t>(a.a_stride)};
+  const uint64_t wd[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.N)}, ws[1] = {static_cast<uint64_t>(a.b_stride)};
+  const uint32_t ab[2] = {kBK, 128}, wb[2] = {kBK, NT / 2};
+  if (!byte_tensor_map(&amap, 2, a.a, ad, as, ab, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !byte_tensor_map(&wmap, 2, a.b, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B))
+    return false;
+  // Output boxes as bytes: 64 columns = 128 bytes; rows that are not whole 16-byte pieces are stored directly.
+  const uint64_t od[2] = {static_cast<uint64_t>(a.N) * 2, static_cast<uint64_t>(a.M)}, os[1] = {static_cast<uint64_t>(a.out_stride) * 2};
+  const uint32_t ob[2] = {128, 32};
+  p.tma_store = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && os[0] % 16 == 0 &&
+                byte_tensor_map(&omap, 2, a.out, od, os, ob, CU_TENSOR_MAP_SWIZZLE_128B);
+  p.tiles_m = static_cast<int32_t>((a.M + 255) / 256);
+  p.tiles_n = static_cast<int32_t>((a.N + NT - 1) / NT);
+  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+  if (tiles > 0x3fffffff) return false;
+  const int64_t pairs = sm_count() / 2;
+  auto kern = matmul_wide_kernel<NT>;
+  constexpr size_t smem = sizeof(WideShared<NT>) + 1024;
+  static_assert(smem <= 227 * 1024, "the ring and the staging rows fit the SM");
+  if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem)) return false;
+  kern<<<static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), kWideThreads, smem, s>>>(amap, wmap, omap, p);
+  return true;
+}
+
 }  // namespace
 
 bool launch_matmul_tc(const MatmulArgs& a, int dtype, cudaStream_t s) {
@@ -311,6 +573,7 @@ bool launch_matmul_tc(const MatmulArgs& a, int dtype, cudaStream_t s) {
   // a single row's stride is never used, but has to be a valid one
   if (b.M == 1) b.a_stride = (b.K + 15) / 16 * 16;
   if (b.N == 1) b.b_stride = (b.K + 15) / 16 * 16;
+  if (a.M > 256) return launch_wide<256>(b, p, s);
   if (a.M <= 16) return launch_narrow<16>(b, p, s);
   if (a.M <= 32) return launch_narrow<32>(b, p, s);
   if (a.M <= 64) return launch_narrow<64>(b, p, s);
