@@ -11,7 +11,7 @@
 // bytes bound it: HBM.
 //
 // Two kernels:
-//   wide   (many rows): CTA pairs, tiles of 256 rows x NT columns, rows of `a` on the tensor-memory lanes, so a
+//   wide   (many rows): CTA pairs, tiles of 256 x 256 outputs, rows of `a` on the tensor-memory lanes, so a
 //          thread owns an output row and its scale of `a` is one register; persistent, outputs staged in shared
 //          memory and stored by TMA.
 //   narrow (few rows): weight rows on the lanes, NT rows of `a` as columns, so that the weights stream through
@@ -41,7 +41,9 @@ struct MmArgs {
   int32_t M, N, nkb;
   int32_t tiles_m, tiles_n;
   int32_t dtype;
-  int32_t tma_store;  // wide: out has a tensor map
+  // wide: whole tiles, column ranges that each of the others is cut into, pieces of work in all; whether out has
+  // a tensor map
+  int32_t whole, parts, pieces, tma_store;
 };
 
 __device__ __forceinline__ uint32_t pack_out(int dtype, float2 v) {
@@ -56,18 +58,23 @@ __device__ __forceinline__ void store_out(int dtype, void* out, int64_t i, float
 // ================================================================================= narrow
 constexpr int kNarrowThreads = 192;  // four epilogue warps, producer, products
 
+// One CTA per SM with as deep a ring as fits: a few CTAs then keep HBM busy (90 KB in flight on each of 48 SMs
+// moved 2 TB/s), and no cluster larger than a pair is needed to occupy the GPU (clusters of 4 to 8 CTAs started
+// in several rounds: 1 x 6144 x 4096 took 13.5 us split six ways and 8.4 us split in two).
+constexpr int kMaxSplit = 4;
+
 template <int NT>
 struct Narrow {
-  static constexpr int kCtas = NT <= 64 ? 2 : 1;  // per SM: 128 accumulators a thread leave room for one
   static constexpr int kStageBytes = (128 + NT) * kBK;
-  static constexpr int kStages = NT <= 32 ? 5 : NT == 64 ? 4 : 6;
-  static constexpr int kBufs = NT == 128 ? 2 : 4;
-  static constexpr uint32_t kCols = NT * kBufs < 32 ? 32 : NT * kBufs;  // 64, 128, 256, 256
+  static constexpr int kStages = NT == 16 ? 11 : NT == 32 ? 10 : NT == 64 ? 8 : 5;
+  static constexpr int kBufs = 4;
+  static constexpr uint32_t kCols = NT * kBufs;  // 64 to 512
 };
 
 template <int NT>
 struct NarrowShared {
   alignas(1024) unsigned char ring[Narrow<NT>::kStages][Narrow<NT>::kStageBytes];  // weights, then rows of a
+  float part[NT / 4 * 3][128];                                                    // partial sums from the cluster's others
   alignas(16) float scale[4][2][NT];                                              // per epilogue warp, two blocks
   alignas(8) uint64_t full[Narrow<NT>::kStages];
   uint64_t empty[Narrow<NT>::kStages];
@@ -76,8 +83,8 @@ struct NarrowShared {
   uint32_t tmem;
 };
 
-template <int NT>
-__global__ void __launch_bounds__(kNarrowThreads, Narrow<NT>::kCtas)
+template <int NT, int SPLIT>
+__global__ void __launch_bounds__(kNarrowThreads, 1)
     matmul_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
                                                                       const __grid_constant__ CUtensorMap amap,
                                                                       const __grid_constant__ MmArgs p) {
@@ -86,10 +93,10 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<NT>::kCtas)
   // The swizzle repeats every 1024 bytes: align the ring to 1024.
   NarrowShared<NT>& sm = *reinterpret_cast<NarrowShared<NT>*>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = gridDim.x, rank = blockIdx.x;  // the cluster is the whole x axis
+  const int rank = blockIdx.x;  // the cluster is the whole x axis
   const int n0 = blockIdx.y * 128, t0 = blockIdx.z * NT;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(p.nkb) * rank / split);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (rank + 1) / split);
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.nkb) * rank / SPLIT);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.nkb) * (rank + 1) / SPLIT);
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&sm.full[s], 1);
@@ -104,6 +111,7 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<NT>::kCtas)
   if (warp == 5) tmem_alloc<1>(&sm.tmem, C::kCols);
   tc_fence_before();
   __syncthreads();
+  if (SPLIT > 1) cluster_arrive();  // waited for before the first access to another CTA: it runs by then
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
 
@@ -219,38 +227,45 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<NT>::kCtas)
         phase ^= 1u;
       }
     }
+    // Each CTA of the cluster finishes NT / SPLIT of the columns: the others push their partial sums of these into
+    // its shared memory, and it adds them in rank order.
     const int row = 32 * warp + lane;
-    if (split == 1) {
+    auto value = [&](int j) { return j & 1 ? acc[j / 2].y : acc[j / 2].x; };
+    if constexpr (SPLIT == 1) {
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        if (t0 + j < p.M && n0 + row < p.N)
-          store_out(p.dtype, p.out, static_cast<int64_t>(t0 + j) * p.out_stride + n0 + row, j & 1 ? acc[j / 2].y : acc[j / 2].x);
+        if (t0 + j < p.M && n0 + row < p.N) store_out(p.dtype, p.out, static_cast<int64_t>(t0 + j) * p.out_stride + n0 + row, value(j));
     } else {
-      // The ring is free: every stage's products have been read. [NT][128] fp32 partial sums.
-      float* part = reinterpret_cast<float*>(sm.ring);
+      constexpr int kOwn = NT / SPLIT;
+      cluster_wait();
 #pragma unroll
-      for (int j = 0; j < NT; ++j) part[j * 128 + row] = j & 1 ? acc[j / 2].y : acc[j / 2].x;
+      for (int r = 0; r < SPLIT; ++r)
+        if (r != rank) {
+          // the part of rank q lies at (q < r ? q : q - 1) of rank r's
+          const uint32_t to = in_cta(&sm.part[kOwn * (rank < r ? rank : rank - 1)][row], r);
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j)
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + j * 512), "f"(value(kOwn * r + j)) : "memory");
+        }
+      cluster_barrier();
+#pragma unroll
+      for (int r = 0; r < SPLIT; ++r)
+        if (r == rank) {
+#pragma unroll
+          for (int j = 0; j < kOwn; ++j) {
+            float v = 0.f;
+#pragma unroll
+            for (int q = 0; q < SPLIT; ++q) v += q == r ? value(kOwn * r + j) : sm.part[kOwn * (q < r ? q : q - 1) + j][row];
+            const int col = t0 + kOwn * r + j;
+            if (col < p.M && n0 + row < p.N) store_out(p.dtype, p.out, static_cast<int64_t>(col) * p.out_stride + n0 + row, v);
+          }
+        }
     }
   }
-  if (split > 1) {
+  if (SPLIT > 1 && warp >= 4) {
     __syncwarp();
+    cluster_wait();
     cluster_barrier();
-    if (warp < 4) {
-      const int row = 32 * warp + lane;
-      const float* part = reinterpret_cast<const float*>(sm.ring);
-      const int live = min(NT, p.M - t0);
-      for (int j = rank; j < live; j += split) {
-        float v = 0.f;
-        for (int r = 0; r < split; ++r) {
-          float x;
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(in_cta(part + j * 128 + row, r)));
-          v += x;
-        }
-        if (n0 + row < p.N) store_out(p.dtype, p.out, static_cast<int64_t>(t0 + j) * p.out_stride + n0 + row, v);
-      }
-    }
-    __syncwarp();
-    cluster_barrier();  // nobody leaves while its partial sums are read
   }
   tc_fence_before();
   __syncthreads();
@@ -269,16 +284,13 @@ bool launch_narrow(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
   p.tiles_n = static_cast<int32_t>((a.N + 127) / 128);
   p.tiles_m = static_cast<int32_t>((a.M + NT - 1) / NT);
   if (p.tiles_n > 65535 || p.tiles_m > 65535) return false;
-  // Split k as far as that fills the SMs, at most a cluster of 8, at least one block each.
+  // Split k while that occupies SMs that would be idle.
   const int64_t tiles = static_cast<int64_t>(p.tiles_n) * p.tiles_m;
-  int64_t split = Narrow<NT>::kCtas * static_cast<int64_t>(sm_count()) / tiles;
-  if (split > 8) split = 8;
-  if (split > p.nkb) split = p.nkb;
-  if (split < 1) split = 1;
-  auto kern = matmul_narrow_kernel<NT>;
+  int split = 1;
+  while (split < kMaxSplit && 2 * split * tiles <= sm_count() && 2 * split <= p.nkb) split *= 2;
+  auto kern = split == 1 ? matmul_narrow_kernel<NT, 1> : split == 2 ? matmul_narrow_kernel<NT, 2> : matmul_narrow_kernel<NT, 4>;
   constexpr size_t smem = sizeof(NarrowShared<NT>) + 1024;
-  static_assert((smem + 1024) * Narrow<NT>::kCtas <= 228 * 1024, "the CTAs fit the SM");
-  static_assert(NT * 128 * 4 <= Narrow<NT>::kStages * Narrow<NT>::kStageBytes, "the partial sums fit the ring");
+  static_assert(smem <= 227 * 1024, "the ring fits the SM");
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem)) return false;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(split), static_cast<unsigned>(p.tiles_n), static_cast<unsigned>(p.tiles_m));
@@ -302,52 +314,129 @@ bool launch_narrow(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
 constexpr int kWideThreads = 384;
 constexpr int kIdleRegs = 40, kEpiRegs = 232;
 
-template <int NT>
-struct Wide {
-  static constexpr int kStageBytes = (128 + NT / 2) * kBK;  // one CTA's half of the pair's operands
-  static constexpr int kStages = 192 * 1024 / kStageBytes < 8 ? 192 * 1024 / kStageBytes : 8;
-  static constexpr int kHalf = NT / 2;                      // columns per epilogue warp
-  static constexpr int kChunks = kHalf / 32;
-  static_assert(kHalf % 64 == 0, "a warp's columns are whole boxes of 64");
-};
+constexpr int kTileM = 256, kTileN = 256;  // outputs of a CTA pair
+constexpr int kWideStageBytes = 256 * kBK; // one CTA's half of the pair's operands
+constexpr int kWideStages = 6;
 
-template <int NT>
 struct WideShared {
-  alignas(1024) unsigned char ring[Wide<NT>::kStages][Wide<NT>::kStageBytes];  // rows of a, then columns' weights
-  alignas(1024) unsigned char out[8][32 * 128];                                // per epilogue warp: 32 rows x 64 columns
-  alignas(8) uint64_t full[Wide<NT>::kStages];   // leader: both CTAs' operands have landed
-  uint64_t empty[Wide<NT>::kStages];             // both: the products have read them
-  uint64_t done[2];                              // both: a block's products are in tensor memory
-  uint64_t free_[2];                             // leader: all sixteen epilogue warps have read them
+  alignas(1024) unsigned char ring[kWideStages][kWideStageBytes];  // 128 rows of a, then 128 weight rows
+  alignas(1024) unsigned char out[8][32 * 128];                    // per epilogue warp: 32 rows x 64 columns
+  alignas(8) uint64_t full[kWideStages];  // leader: both CTAs' operands have landed
+  uint64_t empty[kWideStages];            // both: the products have read them
+  uint64_t done[2];                       // both: a block's products are in tensor memory
+  uint64_t free_[2];                      // leader: all sixteen epilogue warps have read them
   uint32_t tmem;
 };
 
+// Columns n0.. of tile row m, `width` of them (256, 128 or 64).
 struct Tile {
-  int m, n;
+  int m, n0, width;
 };
 
-// The t-th tile, eight tile rows at a time: CTA pairs that run together share operand rows in L2.
+// The t-th piece of work: whole tiles, eight tile rows at a time so that CTA pairs that run together share operand
+// rows in L2; then the tiles that do not fill a last round, cut into `parts` column ranges. (Narrow products take
+// as long as wide ones per instruction, which is why only the last round is cut.)
 __device__ __forceinline__ Tile tile_at(const MmArgs& p, int t) {
   constexpr int kRowsAtATime = 8;
+  int sub = 0, width = kTileN;
+  if (t >= p.whole) {
+    const int extra = t - p.whole;
+    t = p.whole + extra / p.parts;
+    sub = extra - extra / p.parts * p.parts;
+    width = kTileN / p.parts;
+  }
   const int per = kRowsAtATime * p.tiles_n, group = t / per, in = t - group * per;
   const int rows = min(kRowsAtATime, p.tiles_m - group * kRowsAtATime);
   const int n = in / rows;
-  return {group * kRowsAtATime + in - n * rows, n};
+  return {group * kRowsAtATime + in - n * rows, n * kTileN + sub * width, width};
 }
 
-template <int NT>
+// A warp's part of a piece: 32 rows x 32*kChunks columns over every block of k; `b` and `phase` are the next
+// accumulator buffer and its parity. False if a wait gave up.
+template <int kChunks>
+__device__ __forceinline__ bool wide_accumulate(const MmArgs& p, WideShared& sm, const float* sa, const float* sb, uint32_t from,
+                                                uint32_t free0, uint32_t free1, int& b, uint32_t& phase,
+                                                float2 (&acc)[16 * kChunks]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < 16 * kChunks; ++j) acc[j] = make_float2(0.f, 0.f);
+  float a_next = __ldg(sa), b_next = __ldg(sb);
+  for (int kb = 0; kb < p.nkb; ++kb) {
+    const float2 s2 = splat2(a_next * b_next);
+    if (kb + 1 < p.nkb) {
+      a_next = __ldg(sa + kb + 1);
+      b_next = __ldg(sb + kb + 1);
+    }
+    // one verdict for the whole warp: the loads below are collective
+    if (!__all_sync(0xffffffffu, mbar_wait(kWaitLimitNs, &sm.done[b], phase))) return false;
+    tc_fence_after();
+    uint32_t d[2][32];
+    tmem_ld32(from + 256 * b, d[0]);
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+      tmem_wait_ld();
+      if (c + 1 < kChunks) {
+        tmem_ld32(from + 256 * b + 32 * (c + 1), d[(c + 1) & 1]);
+      } else {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(b == 0 ? free0 : free1);
+      }
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        float2& x = acc[16 * c + j / 2];
+        x = fma2(make_float2(__uint_as_float(d[c & 1][j]), __uint_as_float(d[c & 1][j + 1])), s2, x);
+      }
+    }
+    b ^= 1;
+    if (b == 0) phase ^= 1u;
+  }
+  return true;
+}
+
+// The warp's outputs from (row0, col0): by boxes of 64 columns (swizzled rows of 128 bytes), or one by one where
+// the output has no tensor map.
+template <int kChunks>
+__device__ __forceinline__ void wide_store(const MmArgs& p, const CUtensorMap* omap, unsigned char* stage, int row0, int col0,
+                                           const float2 (&acc)[16 * kChunks]) {
+  const int lane = threadIdx.x & 31;
+  if (p.tma_store) {
+#pragma unroll
+    for (int c = 0; c < kChunks / 2; ++c) {
+      if (lane == 0) bulk_wait_read();  // the last box has left the staging rows
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2* v = &acc[32 * c + 4 * e];
+        *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+            make_uint4(pack_out(p.dtype, v[0]), pack_out(p.dtype, v[1]), pack_out(p.dtype, v[2]), pack_out(p.dtype, v[3]));
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) {
+        if (row0 < p.M && col0 + 64 * c < p.N) tma_store_2d(omap, 2 * (col0 + 64 * c), row0, stage);
+        bulk_commit();
+      }
+    }
+  } else if (row0 + lane < p.M) {
+    const int64_t at = static_cast<int64_t>(row0 + lane) * p.out_stride + col0;
+#pragma unroll
+    for (int j = 0; j < 32 * kChunks; ++j)
+      if (col0 + j < p.N) store_out(p.dtype, p.out, at + j, j & 1 ? acc[j / 2].y : acc[j / 2].x);
+  }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
     matmul_wide_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
                        const __grid_constant__ CUtensorMap omap, const __grid_constant__ MmArgs p) {
-  using C = Wide<NT>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   // The swizzle repeats every 1024 bytes: align to 1024 (the same offset in both CTAs).
-  WideShared<NT>& sm = *reinterpret_cast<WideShared<NT>*>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
+  WideShared& sm = *reinterpret_cast<WideShared*>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const int pairs = gridDim.x / 2, first = blockIdx.x / 2, tiles = p.tiles_m * p.tiles_n;
+  const int pairs = gridDim.x / 2, first = blockIdx.x / 2;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < kWideStages; ++s) {
       mbar_init(&sm.full[s], 1);
       mbar_init(&sm.empty[s], 1);
     }
@@ -372,19 +461,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       uint32_t phase = 1;
       int64_t k = 0;  // stages issued
       bool ok = true;
-      for (int t = first; t < tiles && ok; t += pairs) {
+      for (int t = first; t < p.pieces && ok; t += pairs) {
         const Tile at = tile_at(p, t);
-        const int arow = at.m * 256 + 128 * static_cast<int>(rank), wrow = at.n * NT + (NT / 2) * static_cast<int>(rank);
+        const int arow = at.m * kTileM + 128 * static_cast<int>(rank);
+        const int wrow = at.n0 + at.width / 2 * static_cast<int>(rank);  // of a narrow piece the box's first rows count
         for (int kb = 0; kb < p.nkb; ++kb, ++k) {
-          if (k >= C::kStages && !mbar_wait(kWaitLimitNs, &sm.empty[s], phase)) {
+          if (k >= kWideStages && !mbar_wait(kWaitLimitNs, &sm.empty[s], phase)) {
             ok = false;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * C::kStageBytes);
+          if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 2 * kWideStageBytes);
           const uint32_t bar = in_cta(&sm.full[s], 0);
           tma_load_2d_pair(sm.ring[s], &amap, kb * kBK, arow, bar);
           tma_load_2d_pair(sm.ring[s] + 128 * kBK, &wmap, kb * kBK, wrow, bar);
-          if (++s == C::kStages) {
+          if (++s == kWideStages) {
             s = 0;
             phase ^= 1u;
           }
@@ -395,17 +485,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
         // Let the copies already issued land before this CTA's shared memory goes away: the leader sees both
         // CTAs' on its barriers; the cluster barrier at the end keeps the peer.
         if (rank == 0)
-          for (int64_t j = max(static_cast<int64_t>(0), k - C::kStages); j < k; ++j)
-            if (!mbar_wait(kWaitLimitNs, &sm.full[j % C::kStages], static_cast<uint32_t>(j / C::kStages) & 1u)) break;
+          for (int64_t j = max(static_cast<int64_t>(0), k - kWideStages); j < k; ++j)
+            if (!mbar_wait(kWaitLimitNs, &sm.full[j % kWideStages], static_cast<uint32_t>(j / kWideStages) & 1u)) break;
       }
     } else if (warp == 1 && lane == 0 && rank == 0) {
       // ---------------------------------------------------------------------- products
-      constexpr uint32_t idesc = e4m3_idesc(256, NT);
       int s = 0, b = 0;
       uint32_t phase = 0, bphase = 1;
       bool ok = true;
       int64_t k = 0;
-      for (int t = first; t < tiles && ok; t += pairs) {
+      for (int t = first; t < p.pieces && ok; t += pairs) {
+        const int width = tile_at(p, t).width;
+        const uint32_t idesc = width == 256 ? e4m3_idesc(256, 256) : width == 128 ? e4m3_idesc(256, 128) : e4m3_idesc(256, 64);
         for (int kb = 0; kb < p.nkb; ++kb, ++k) {
           ok = (k < 2 || mbar_wait(kWaitLimitNs, &sm.free_[b], bphase)) && mbar_wait(kWaitLimitNs, &sm.full[s], phase);
           if (!ok) {
@@ -418,7 +509,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
           for (int i = 0; i < kBK / 32; ++i) mma_e4m3_tile<2>(tmem + b * 256, ad + 2 * i, wd + 2 * i, idesc, i > 0);
           mma_commit<2>(&sm.empty[s]);
           mma_commit<2>(&sm.done[b]);
-          if (++s == C::kStages) {
+          if (++s == kWideStages) {
             s = 0;
             phase ^= 1u;
           }
@@ -430,94 +521,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
   } else {
     // ------------------------------------------------------------------------ epilogue
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
-    const int quarter = warp & 3, half = (warp - 4) >> 2;  // lanes 32*quarter.., columns kHalf*half..
-    const uint32_t from = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + C::kHalf * half;
+    const int quarter = warp & 3, half = (warp - 4) >> 2;  // lanes 32*quarter.., which half of the columns
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     unsigned char* stage = sm.out[warp - 4];
     const uint32_t free0 = in_cta(&sm.free_[0], 0), free1 = in_cta(&sm.free_[1], 0);
     int b = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int t = first; t < tiles && ok; t += pairs) {
+    for (int t = first; t < p.pieces && ok; t += pairs) {
       const Tile at = tile_at(p, t);
-      const int row0 = at.m * 256 + 128 * static_cast<int>(rank) + 32 * quarter, col0 = at.n * NT + C::kHalf * half;
+      // 128 or 64 columns of a warp; a piece of 64 leaves the second half without any, but its barriers are kept.
+      const bool both = at.width == 256, none = at.width == 64 && half == 1;
+      const int row0 = at.m * kTileM + 128 * static_cast<int>(rank) + 32 * quarter, col0 = at.n0 + (both ? 128 : 64) * half;
+      const uint32_t from = lanes + (both ? 128 : 64) * half;
       const float* sa = p.sa + static_cast<int64_t>(min(row0 + lane, p.M - 1)) * p.sa_stride;
-      // The scale block of each 64 columns (a tile's columns start at a multiple of 64).
-      const float* sb[(C::kHalf + 63) / 64];
-#pragma unroll
-      for (int c = 0; c < (C::kHalf + 63) / 64; ++c)
-        sb[c] = p.sb + static_cast<int64_t>(min(col0 + 64 * c, p.N - 1) / kScaleBlock) * p.sb_stride;
-      float2 acc[C::kHalf / 2];
-#pragma unroll
-      for (int j = 0; j < C::kHalf / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-      float a_next = __ldg(sa), b_next[(C::kHalf + 63) / 64];
-#pragma unroll
-      for (int c = 0; c < (C::kHalf + 63) / 64; ++c) b_next[c] = __ldg(sb[c]);
-      for (int kb = 0; kb < p.nkb; ++kb) {
-        float sc[(C::kHalf + 63) / 64];
-#pragma unroll
-        for (int c = 0; c < (C::kHalf + 63) / 64; ++c) sc[c] = a_next * b_next[c];
-        if (kb + 1 < p.nkb) {
-          a_next = __ldg(sa + kb + 1);
-#pragma unroll
-          for (int c = 0; c < (C::kHalf + 63) / 64; ++c) b_next[c] = __ldg(sb[c] + kb + 1);
-        }
-        // one verdict for the whole warp: the loads below are collective
-        if (!__all_sync(0xffffffffu, mbar_wait(kWaitLimitNs, &sm.done[b], phase))) {
-          flag_failure(p.status);
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        uint32_t d[2][32];
-        tmem_ld32(from + b * 256, d[0]);
-#pragma unroll
-        for (int c = 0; c < C::kChunks; ++c) {
-          tmem_wait_ld();
-          if (c + 1 < C::kChunks) {
-            tmem_ld32(from + b * 256 + 32 * (c + 1), d[(c + 1) & 1]);
-          } else {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(b == 0 ? free0 : free1);
-          }
-          const float2 s2 = splat2(sc[c / 2]);
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            float2& x = acc[16 * c + j / 2];
-            x = fma2(make_float2(__uint_as_float(d[c & 1][j]), __uint_as_float(d[c & 1][j + 1])), s2, x);
-          }
-        }
-        b ^= 1;
-        if (b == 0) phase ^= 1u;
+      // The columns start at a multiple of their number, so they lie in one scale block.
+      const float* sb = p.sb + static_cast<int64_t>(min(col0, p.N - 1) / kScaleBlock) * p.sb_stride;
+      if (both) {
+        float2 acc[64];
+        ok = wide_accumulate<4>(p, sm, sa, sb, from, free0, free1, b, phase, acc);
+        if (ok) wide_store<4>(p, &omap, stage, row0, col0, acc);
+      } else {
+        // Of a piece of 64 columns the second half has none: it reads what is there and keeps the barriers going.
+        float2 acc[32];
+        ok = wide_accumulate<2>(p, sm, sa, sb, from, free0, free1, b, phase, acc);
+        if (ok && !none) wide_store<2>(p, &omap, stage, row0, col0, acc);
       }
-      if (!ok) break;
-      if (p.tma_store) {
-        // 64 columns at a time: swizzled rows of 128 bytes, one box per warp.
-#pragma unroll
-        for (int c = 0; c < (C::kHalf + 63) / 64; ++c) {
-          if (lane == 0) bulk_wait_read();  // the last box has left the staging rows
-          __syncwarp();
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (64 * c + 8 * e < C::kHalf) {
-              const float2* v = &acc[32 * c + 4 * e];
-              *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
-                  make_uint4(pack_out(p.dtype, v[0]), pack_out(p.dtype, v[1]), pack_out(p.dtype, v[2]), pack_out(p.dtype, v[3]));
-            }
-          }
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) {
-            if (row0 < p.M && col0 + 64 * c < p.N) tma_store_2d(&omap, 2 * (col0 + 64 * c), row0, stage);
-            bulk_commit();
-          }
-        }
-      } else if (row0 + lane < p.M) {
-        const int64_t at0 = static_cast<int64_t>(row0 + lane) * p.out_stride + col0;
-#pragma unroll
-        for (int j = 0; j < C::kHalf; ++j)
-          if (col0 + j < p.N) store_out(p.dtype, p.out, at0 + j, j & 1 ? acc[j / 2].y : acc[j / 2].x);
-      }
+      if (!ok) flag_failure(p.status);
     }
     if (lane == 0) bulk_wait_all();
   }
@@ -527,12 +557,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
   if (warp == 1) tmem_free<2>(tmem, 512);
 }
 
-template <int NT>
 bool launch_wide(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
   CUtensorMap amap, wmap, omap{};
   const uint64_t ad[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.M)}, as[1] = {static_cast<uint64_t>(a.a_stride)};
   const uint64_t wd[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.N)}, ws[1] = {static_cast<uint64_t>(a.b_stride)};
-  const uint32_t ab[2] = {kBK, 128}, wb[2] = {kBK, NT / 2};
+  const uint32_t ab[2] = {kBK, 128}, wb[2] = {kBK, 128};
   if (!byte_tensor_map(&amap, 2, a.a, ad, as, ab, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !byte_tensor_map(&wmap, 2, a.b, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B))
     return false;
@@ -541,16 +570,24 @@ bool launch_wide(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
   const uint32_t ob[2] = {128, 32};
   p.tma_store = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && os[0] % 16 == 0 &&
                 byte_tensor_map(&omap, 2, a.out, od, os, ob, CU_TENSOR_MAP_SWIZZLE_128B);
-  p.tiles_m = static_cast<int32_t>((a.M + 255) / 256);
-  p.tiles_n = static_cast<int32_t>((a.N + NT - 1) / NT);
+  p.tiles_m = static_cast<int32_t>((a.M + kTileM - 1) / kTileM);
+  p.tiles_n = static_cast<int32_t>((a.N + kTileN - 1) / kTileN);
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
-  if (tiles > 0x3fffffff) return false;
-  const int64_t pairs = sm_count() / 2;
-  auto kern = matmul_wide_kernel<NT>;
-  constexpr size_t smem = sizeof(WideShared<NT>) + 1024;
+  if (tiles > 0x0fffffff) return false;
+  // Whole rounds of the CTA pairs first; the rest cut in two or four where that ends sooner.
+  const int64_t pairs = sm_count() / 2, rest = tiles % pairs;
+  p.whole = static_cast<int32_t>(tiles - rest);
+  p.parts = 1;
+  for (int parts = 2; parts <= 4; parts *= 2) {
+    const int64_t now = (rest * p.parts + pairs - 1) / pairs * parts, then = (rest * parts + pairs - 1) / pairs * p.parts;
+    if (then < now) p.parts = parts;
+  }
+  p.pieces = static_cast<int32_t>(p.whole + rest * p.parts);
+  constexpr size_t smem = sizeof(WideShared) + 1024;
   static_assert(smem <= 227 * 1024, "the ring and the staging rows fit the SM");
-  if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem)) return false;
-  kern<<<static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), kWideThreads, smem, s>>>(amap, wmap, omap, p);
+  if (!ensure_dynamic_smem(reinterpret_cast<const void*>(matmul_wide_kernel), smem)) return false;
+  matmul_wide_kernel<<<static_cast<unsigned>(2 * (p.pieces < pairs ? p.pieces : pairs)), kWideThreads, smem, s>>>(amap, wmap,
+                                                                                                               omap, p);
   return true;
 }
 
@@ -573,7 +610,7 @@ bool launch_matmul_tc(const MatmulArgs& a, int dtype, cudaStream_t s) {
   // a single row's stride is never used, but has to be a valid one
   if (b.M == 1) b.a_stride = (b.K + 15) / 16 * 16;
   if (b.N == 1) b.b_stride = (b.K + 15) / 16 * 16;
-  if (a.M > 256) return launch_wide<256>(b, p, s);
+  if (a.M > 256) return launch_wide(b, p, s);
   if (a.M <= 16) return launch_narrow<16>(b, p, s);
   if (a.M <= 32) return launch_narrow<32>(b, p, s);
   if (a.M <= 64) return launch_narrow<64>(b, p, s);
