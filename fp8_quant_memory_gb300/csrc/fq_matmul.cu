@@ -21,6 +21,8 @@
 //
 // Waits are bounded (fq_sync.cuh): a role that gives up flags the device status word and leaves its loop, the
 // others follow when their own waits run out, and tensor memory is freed either way.
+#include <cmath>
+
 #include "fq_device.cuh"
 #include "fq_serving.h"
 #include "fq_tcgen05.cuh"
@@ -272,6 +274,13 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   if (warp == 5) tmem_free<1>(tmem, C::kCols);
 }
 
+// CTAs that share a tile's k: as many as occupy SMs that would be idle.
+int narrow_split(int64_t tiles, int64_t nkb) {
+  int split = 1;
+  while (split < kMaxSplit && 2 * split * tiles <= sm_count() && 2 * split <= nkb) split *= 2;
+  return split;
+}
+
 template <int NT>
 bool launch_narrow(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
   CUtensorMap wmap, amap;
@@ -284,10 +293,7 @@ bool launch_narrow(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
   p.tiles_n = static_cast<int32_t>((a.N + 127) / 128);
   p.tiles_m = static_cast<int32_t>((a.M + NT - 1) / NT);
   if (p.tiles_n > 65535 || p.tiles_m > 65535) return false;
-  // Split k while that occupies SMs that would be idle.
-  const int64_t tiles = static_cast<int64_t>(p.tiles_n) * p.tiles_m;
-  int split = 1;
-  while (split < kMaxSplit && 2 * split * tiles <= sm_count() && 2 * split <= p.nkb) split *= 2;
+  const int split = narrow_split(static_cast<int64_t>(p.tiles_n) * p.tiles_m, p.nkb);
   auto kern = split == 1 ? matmul_narrow_kernel<NT, 1> : split == 2 ? matmul_narrow_kernel<NT, 2> : matmul_narrow_kernel<NT, 4>;
   constexpr size_t smem = sizeof(NarrowShared<NT>) + 1024;
   static_assert(smem <= 227 * 1024, "the ring fits the SM");
@@ -310,9 +316,9 @@ bool launch_narrow(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
 
 // =================================================================================== wide
 // Warpgroup 0: producer (warp 0), products (warp 1), two idle warps; warpgroups 1 and 2: epilogue. The epilogue's
-// registers come from warpgroup 0: 384 x 168 at launch = 128 x 40 + 256 x 232.
+// registers come from warpgroup 0: 384 x 168 at launch = 128 x 72 + 256 x 216.
 constexpr int kWideThreads = 384;
-constexpr int kIdleRegs = 40, kEpiRegs = 232;
+constexpr int kIdleRegs = 72, kEpiRegs = 216;
 
 constexpr int kTileM = 256, kTileN = 256;  // outputs of a CTA pair
 constexpr int kWideStageBytes = 256 * kBK; // one CTA's half of the pair's operands
@@ -370,21 +376,21 @@ __device__ __forceinline__ bool wide_accumulate(const MmArgs& p, WideShared& sm,
     // one verdict for the whole warp: the loads below are collective
     if (!__all_sync(0xffffffffu, mbar_wait(kWaitLimitNs, &sm.done[b], phase))) return false;
     tc_fence_after();
-    uint32_t d[2][32];
-    tmem_ld32(from + 256 * b, d[0]);
+    uint32_t d[2][16];
+    tmem_ld16(from + 256 * b, d[0]);
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
+    for (int c = 0; c < 2 * kChunks; ++c) {
       tmem_wait_ld();
-      if (c + 1 < kChunks) {
-        tmem_ld32(from + 256 * b + 32 * (c + 1), d[(c + 1) & 1]);
+      if (c + 1 < 2 * kChunks) {
+        tmem_ld16(from + 256 * b + 16 * (c + 1), d[(c + 1) & 1]);
       } else {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(b == 0 ? free0 : free1);
       }
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        float2& x = acc[16 * c + j / 2];
+      for (int j = 0; j < 16; j += 2) {
+        float2& x = acc[8 * c + j / 2];
         x = fma2(make_float2(__uint_as_float(d[c & 1][j]), __uint_as_float(d[c & 1][j + 1])), s2, x);
       }
     }
@@ -394,35 +400,44 @@ __device__ __forceinline__ bool wide_accumulate(const MmArgs& p, WideShared& sm,
   return true;
 }
 
-// The warp's outputs from (row0, col0): by boxes of 64 columns (swizzled rows of 128 bytes), or one by one where
-// the output has no tensor map.
+// The warp's outputs from (row0, col0), 64 columns at a time through staging rows of 128 bytes (16-byte pieces
+// swizzled): by a TMA box, or row by row with neighbouring lanes on neighbouring columns where the output has no
+// tensor map (rows that are not whole 16-byte pieces).
 template <int kChunks>
 __device__ __forceinline__ void wide_store(const MmArgs& p, const CUtensorMap* omap, unsigned char* stage, int row0, int col0,
                                            const float2 (&acc)[16 * kChunks]) {
   const int lane = threadIdx.x & 31;
-  if (p.tma_store) {
 #pragma unroll
-    for (int c = 0; c < kChunks / 2; ++c) {
-      if (lane == 0) bulk_wait_read();  // the last box has left the staging rows
-      __syncwarp();
+  for (int c = 0; c < kChunks / 2; ++c) {
+    if (lane == 0) bulk_wait_read();  // the last box has left the staging rows
+    __syncwarp();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2* v = &acc[32 * c + 4 * e];
-        *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
-            make_uint4(pack_out(p.dtype, v[0]), pack_out(p.dtype, v[1]), pack_out(p.dtype, v[2]), pack_out(p.dtype, v[3]));
-      }
+    for (int e = 0; e < 8; ++e) {
+      const float2* v = &acc[32 * c + 4 * e];
+      *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+          make_uint4(pack_out(p.dtype, v[0]), pack_out(p.dtype, v[1]), pack_out(p.dtype, v[2]), pack_out(p.dtype, v[3]));
+    }
+    const int col = col0 + 64 * c;
+    if (p.tma_store) {
       fence_async_shared();
       __syncwarp();
       if (lane == 0) {
-        if (row0 < p.M && col0 + 64 * c < p.N) tma_store_2d(omap, 2 * (col0 + 64 * c), row0, stage);
+        if (row0 < p.M && col < p.N) tma_store_2d(omap, 2 * col, row0, stage);
         bulk_commit();
       }
-    }
-  } else if (row0 + lane < p.M) {
-    const int64_t at = static_cast<int64_t>(row0 + lane) * p.out_stride + col0;
+    } else {
+      __syncwarp();
+      const int rows = min(32, p.M - row0);
+      uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(row0) * p.out_stride + col;
+#pragma unroll 1
+      for (int r = 0; r < rows; ++r, out += p.out_stride)
 #pragma unroll
-    for (int j = 0; j < 32 * kChunks; ++j)
-      if (col0 + j < p.N) store_out(p.dtype, p.out, at + j, j & 1 ? acc[j / 2].y : acc[j / 2].x);
+        for (int h = 0; h < 2; ++h) {
+          const int x = lane + 32 * h;
+          if (col + x < p.N) out[x] = *reinterpret_cast<const uint16_t*>(stage + r * 128 + (((x >> 3) ^ (r & 7)) << 4) + 2 * (x & 7));
+        }
+      __syncwarp();
+    }
   }
 }
 
@@ -574,14 +589,11 @@ bool launch_wide(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
   p.tiles_n = static_cast<int32_t>((a.N + kTileN - 1) / kTileN);
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   if (tiles > 0x0fffffff) return false;
-  // Whole rounds of the CTA pairs first; the rest cut in two or four where that ends sooner.
+  // Whole rounds of the CTA pairs first; the rest cut in two or four if one round takes all the cuts (a narrow
+  // piece costs about 0.85 of a whole one).
   const int64_t pairs = sm_count() / 2, rest = tiles % pairs;
   p.whole = static_cast<int32_t>(tiles - rest);
-  p.parts = 1;
-  for (int parts = 2; parts <= 4; parts *= 2) {
-    const int64_t now = (rest * p.parts + pairs - 1) / pairs * parts, then = (rest * parts + pairs - 1) / pairs * p.parts;
-    if (then < now) p.parts = parts;
-  }
+  p.parts = rest * 4 <= pairs ? 4 : rest * 2 <= pairs ? 2 : 1;
   p.pieces = static_cast<int32_t>(p.whole + rest * p.parts);
   constexpr size_t smem = sizeof(WideShared) + 1024;
   static_assert(smem <= 227 * 1024, "the ring and the staging rows fit the SM");
@@ -610,10 +622,25 @@ bool launch_matmul_tc(const MatmulArgs& a, int dtype, cudaStream_t s) {
   // a single row's stride is never used, but has to be a valid one
   if (b.M == 1) b.a_stride = (b.K + 15) / 16 * 16;
   if (b.N == 1) b.b_stride = (b.K + 15) / 16 * 16;
-  if (a.M > 256) return launch_wide(b, p, s);
-  if (a.M <= 16) return launch_narrow<16>(b, p, s);
-  if (a.M <= 32) return launch_narrow<32>(b, p, s);
-  if (a.M <= 64) return launch_narrow<64>(b, p, s);
+  // The kernel with the least estimated time. A CTA of the narrow kernel costs a start and a time per block of k,
+  // which grow with its columns; the wide kernel a start and a time per block for each round of CTA pairs. In us,
+  // fitted to a sweep over M of 1 to 2048 and (N, K) of (1111, 1968) to (8192, 8192), where the choice is the fastest
+  // or within 15% of it: at 4096 x 4096 for example M = 16 takes 6.2 us with 16 columns and 7.8 with 64, M = 64 takes
+  // 12.8 and 7.9, M = 256 takes 16.9 with 64, 16.4 with 128 and 18.8 wide, M = 512 26.1 with 128 and 19.5 wide.
+  const double nkb = static_cast<double>(p.nkb), sms = sm_count(), pairs = sm_count() / 2;
+  auto narrow = [&](int nt, double start, double block) {
+    const int64_t tiles = ((a.N + 127) / 128) * ((a.M + nt - 1) / nt);
+    const int split = narrow_split(tiles, p.nkb);
+    return std::ceil(tiles * split / sms) * (start + std::ceil(nkb / split) * block);
+  };
+  const double t16 = narrow(16, 2.8, 0.43), t32 = narrow(32, 3.0, 0.43), t64 = narrow(64, 4.0, 0.47), t128 = narrow(128, 6.0, 0.67);
+  const double tiles = static_cast<double>((a.M + kTileM - 1) / kTileM) * static_cast<double>((a.N + kTileN - 1) / kTileN);
+  const double wide = 4.5 + nkb * 0.47 * (std::floor(tiles / pairs) + (std::fmod(tiles, pairs) * 2 <= pairs ? 0.85 : 1.0));
+  const double best = std::fmin(std::fmin(std::fmin(t16, t32), std::fmin(t64, t128)), wide);
+  if (best == wide) return launch_wide(b, p, s);
+  if (best == t16) return launch_narrow<16>(b, p, s);
+  if (best == t32) return launch_narrow<32>(b, p, s);
+  if (best == t64) return launch_narrow<64>(b, p, s);
   return launch_narrow<128>(b, p, s);
 }
 
