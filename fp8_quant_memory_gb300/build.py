@@ -1,7 +1,9 @@
-"""Build libfq.so (the sm_103a kernels behind include/fq.h) in-tree, with nvcc only.
+"""Build libfq.so (the sm_103a kernels behind include/fq.h) in-tree with nvcc, and the CPython module
+of the serving operators' bindings (csrc/fq_binding.cpp) with the host compiler against torch's headers.
 
-Each translation unit compiles in its own nvcc process (in parallel), then one nvcc link step
-makes ``fp8_quant_memory_gb300/_build/libfq.so``. Nothing is installed outside the repository.
+Each translation unit compiles in its own process (in parallel), then one nvcc link step makes
+``fp8_quant_memory_gb300/_build/libfq.so``, which the module beside it is linked to. Nothing is
+installed outside the repository.
 """
 from __future__ import annotations
 
@@ -10,12 +12,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libfq.so")
+BINDING_SRC = os.path.join(CSRC, "fq_binding.cpp")
+BINDING = os.path.join(OUT_DIR, "_fq_binding.so")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -36,13 +41,13 @@ def sources() -> list[str]:
 
 def _deps() -> list[str]:
     extra = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
-    return sources() + extra + [os.path.join(INCLUDE, "fq.h"), os.path.abspath(__file__)]
+    return sources() + extra + [BINDING_SRC, os.path.join(INCLUDE, "fq.h"), os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(BINDING)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
@@ -59,20 +64,62 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _torch_paths() -> tuple[list[str], str]:
+    """torch's include directories and library directory (without torch.utils.cpp_extension, which probes
+    for a toolkit when it is imported)."""
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc = os.path.join(root, "include")
+    return [inc, os.path.join(inc, "torch", "csrc", "api", "include")], os.path.join(root, "lib")
+
+
+def _compile_binding() -> str:
+    """Compile csrc/fq_binding.cpp to an object file."""
+    import torch
+
+    obj = os.path.join(OUT_DIR, "fq_binding.o")
+    inc, _ = _torch_paths()
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I", INCLUDE, "-I", cuda, "-I", sysconfig.get_path("include")]
+    for p in inc:
+        cmd += ["-isystem", p]
+    r = subprocess.run([*cmd, "-c", BINDING_SRC, "-o", obj], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on fq_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    """Link the module to libfq.so beside it and to the torch libraries of the running interpreter."""
+    _, lib = _torch_paths()
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", OUT_DIR, "-l:libfq.so", "-Wl,-rpath,$ORIGIN", "-L", lib, "-ltorch_python",
+           "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking the binding failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every .cu under csrc/ for sm_103a and link libfq.so; returns the library path."""
+    """Compile every .cu under csrc/ for sm_103a, link libfq.so and the binding; returns the library path."""
     if not force and up_to_date():
         return LIB
     os.makedirs(OUT_DIR, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     return LIB
 
 
