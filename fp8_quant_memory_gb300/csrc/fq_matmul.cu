@@ -644,6 +644,4 @@ bool launch_matmul_tc(const MatmulArgs& a, int dtype, cudaStream_t s) {
   return launch_narrow<128>(b, p, s);
 }
 
-bool launch_append_vector(const AppendArgs&, int, int, cudaStream_t) { return false; }
-
 }  // namespace fq
