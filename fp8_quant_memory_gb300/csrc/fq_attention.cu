@@ -9,20 +9,24 @@
 // so they fit fp16 for the tensor cores (rounded by 2^-11 of themselves, or 2^-25 of the largest), and
 // partial results (m, l, M, O) join exactly: out = O * 2^(M - m) / l.
 //
-// What bounds it: every key and value byte is read once and used Hq/Hk <= 16 times, so HBM. The products
-// are legacy-shape warp matrix instructions on purpose: the 16 rows of one m16n8 tile hold all query heads
-// of a key head, and one step of 16 tokens per warp issues 8 e4m3 products (4.25 clocks each and
-// scheduler) and 16 fp16 products (8 clocks), about 230 of the ~700 clocks its 4 KB take to arrive at
-// 6.8 TB/s; tcgen05 would need the value tile transposed through shared memory and 128 rows to fill.
+// What bounds it: every key and value byte is read once and used Hq/Hk <= 16 times, so HBM. The products are
+// legacy-shape warp matrix instructions on purpose: eight query heads of a key head fill the 8 columns of m16n8k16
+// with tokens (scores) or output columns (values) on the 16 rows, and the codes become fp16, exactly, on their way
+// into the fragments; tcgen05 would need the value tile transposed through shared memory and 128 rows to fill.
+// (mma.sync takes e4m3 as well, but here that costs more than converting: the conversions of both operands at each
+// use showed as 246 ALU instructions per step of 16 tokens at head size 256, 51 us against what it is now.)
 //
-// Layout. A producer warp streams units of 128 tokens, 16 per consumer warp, through a ring of stages: one
-// TMA box of the rows of a page at a time where pages are multiples of 8 tokens, else 16-byte cp.async row by
-// row. Both products contract over an index whose order is free as long as both operands agree: thread
-// (g, c) = (lane / 4, lane % 4) reads pieces 2c and 2c + 1 of key rows g and g + 8 as the k indices of its B
-// fragments, and piece g of value rows 2c, 2c + 1, 2c + 8, 2c + 9. Pieces are stored at (piece ^ row % 8), the
-// 128-byte swizzle, which puts the eight lanes of every 16-byte access phase in different banks for both
-// readings. The value product is taken transposed (columns x heads), so the score tile's accumulators are
-// the weights' B fragment without a shuffle and eight heads need DP / 4 accumulators a thread.
+// Layout. Units of 128 tokens (64 and 32 for the larger items) stream through a ring of stages: a producer warp
+// brings one TMA box of the rows of a page at a time where pages are multiples of 8 tokens, else two producer warps
+// copy row by row with 16-byte cp.async. Both products contract over an index whose order is free as long as both
+// operands agree: thread (g, c) = (lane / 4, lane % 4) reads pieces 2c and 2c + 1 of key rows g and g + 8 as the k
+// indices of its A fragments (scores: tokens x heads), and piece g of value rows 2c, 2c + 1, 2c + 8, 2c + 9 as A
+// fragments of the value product (columns x heads). Pieces are stored at (piece ^ row % 8), the 128-byte swizzle,
+// which puts the eight lanes of every 16-byte access phase in different banks for both readings. The weights go from
+// accumulators to B fragments by two movmatrix.
+//
+// The running maxima are only brought up to date when a score exceeds one by more than 2^8 (a vote; then three
+// shuffles per head and the rescaling): weights of up to 2^8 lose nothing in fp16 and fp32.
 //
 // Split. The work is a list of units (128 tokens of one sequence and key head, 16 per warp) in the order
 // sequence, head, tokens; CTA i of n takes units [i*U/n, (i+1)*U/n). The lengths are on the device, so each
@@ -59,6 +63,7 @@ struct Item {
   // Ring depth: what two CTAs per SM leave room for (98 KB of codes; 80 KB at head size 64, whose scales weigh more).
   static constexpr int kStages = (DP == 64 ? 80 : 98) * 1024 / (2 * kUnit * DP);
 };
+constexpr float kSlack = 8.f;                // powers of two by which a score may exceed its running maximum
 constexpr float kLowest = -3.402823466e38f;  // below every score: a maximum before the first token
 
 // A unit's rows are stored as kA tiles of [rows][128 bytes], then kB of [rows][64], keys before values.
@@ -82,6 +87,8 @@ struct Shared {
   alignas(16) float scales[kStages][2][kUnit];  // K then V
   uint16_t live[kStages][Item<DP, HG>::kSlabs];  // bit t of a slab's word: its token t counts
   alignas(16) float join[kWarps][kHeads][kJoinStride];
+  // Above head size 128 the query's codes are read from here at each use: fragments in registers spill.
+  uint4 query[DP > 128 ? HG : 1][DP > 128 ? DP / 64 : 1][32];
   float stat[kWarps][kHeads][3];  // m, M, l
   alignas(8) uint64_t full[kStages];
   uint64_t empty[kStages];
@@ -136,13 +143,6 @@ __device__ __forceinline__ float lg2(float v) {
   return r;
 }
 
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -180,9 +180,25 @@ __device__ __forceinline__ uint32_t word(const uint4& v, int k) {
   return k == 0 ? v.x : (k == 1 ? v.y : (k == 2 ? v.z : v.w));
 }
 
-__device__ __forceinline__ float quad_max(float v) {
-  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+// Four codes of a word -> two fp16 pairs; exact.
+__device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 p, q;\n\tmov.b32 {p, q}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, p;\n\tcvt.rn.f16x2.e4m3x2 %1, q;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+// An 8 x 8 matrix of 16-bit values, two of a row per thread, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// The largest v of the eight lanes with the same lane % 4.
+__device__ __forceinline__ float column_max(float v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
 }
 
 // A place in the list of units: a work item of sequence b (key head item / chunks, and the item % chunks-th
@@ -355,45 +371,53 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// The producer warp for pages that are multiples of 8 tokens: lane k feeds the k-th box of each unit, 2^box_shift
-// tokens of one page. Rows of a box behind the sequence's end are loaded too (they are inside the cache) and
-// masked by the consumers.
+// The feed of a CTA where pages are multiples of 8 tokens, one warp's: lane k brings the k-th box of each unit,
+// 2^box_shift tokens of one page. Rows of a box behind the sequence's end are loaded too (they are inside the cache)
+// and masked by the consumers.
 template <int DP, int HG>
-__device__ __forceinline__ void produce_boxes(const SplitArgs& a, const Maps& maps, Shared<DP, HG>& sm, Place<DP, HG> at,
-                                              int32_t units) {
+struct BoxFeed {
   using S = Shape<DP>;
-  constexpr int kUnit = Item<DP, HG>::kUnit, kQ = kUnit / 32, kStages = Shared<DP, HG>::kStages;
-  const PagedArgs& p = a.p;
-  const CacheView& cache = p.cache;
-  const int lane = threadIdx.x & 31;
-  const int rows = 1 << a.box_shift;
-  const bool mine = (lane << a.box_shift) < kUnit;
-  int32_t base = (tiles_of<DP, HG>(at.len) - at.left) * kUnit;  // the unit's first token
-  int32_t head = 0;
-  const int32_t* table = nullptr;
-  auto enter = [&]() {
+  static constexpr int kUnit = Item<DP, HG>::kUnit;
+
+  Place<DP, HG> at;
+  int32_t base, head;  // the next unit's first token, its key head
+  const int32_t* table;
+  // Entries `window`..`window + 63` of the sequence's table row, two per lane, loaded at least 16 entries before a
+  // unit needs them (a unit spans at most 16 pages); loading each unit's entries as it came cost their latency per
+  // unit. Entries behind the sequence's last page are -1.
+  int32_t window, near, far, pages_here;
+
+  __device__ __forceinline__ int32_t index_of(const SplitArgs& a, int32_t t) const {
+    return static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(t)) * a.page_magic) >> a.page_magic_shift);
+  }
+  __device__ __forceinline__ int32_t entry(int32_t i) const { return i < pages_here ? __ldg(table + i) : -1; }
+
+  // At unit `at`, whose first token is `base`.
+  __device__ __forceinline__ void enter(const SplitArgs& a) {
+    const int lane = threadIdx.x & 31;
     head = at.item / a.chunks;
-    table = p.table + static_cast<int64_t>(at.b) * p.table_stride;
-  };
-  // Page and slot of this lane's box of the unit at `base`, loaded one unit ahead; page -1 behind the end.
-  int32_t page = -1, slot = 0;
-  auto look_up = [&]() {
-    const int32_t t = base + (lane << a.box_shift);
-    const int32_t i = static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(t)) * a.page_magic) >> a.page_magic_shift);
-    slot = t - i * cache.page_size;
-    page = mine && t < at.len ? __ldg(table + i) : -1;
-  };
-  enter();
-  look_up();
-  int stage = 0;
-  uint32_t phase = 1;  // the first round finds every stage empty
-  int32_t u = 0;
-  bool ok = true;
-  for (; u < units; ++u) {
-    if (u >= kStages && !mbar_wait(kWaitLimitNs, &sm.empty[stage], phase)) {
-      ok = false;
-      break;
+    table = a.p.table + static_cast<int64_t>(at.b) * a.p.table_stride;
+    pages_here = index_of(a, at.len - 1) + 1;
+    window = index_of(a, base);
+    near = entry(window + lane);
+    far = entry(window + 32 + lane);
+  }
+
+  // Starts the copies of the next unit into `stage` and moves on (`more`: another unit follows).
+  __device__ __forceinline__ void issue(const SplitArgs& a, const Maps& maps, Shared<DP, HG>& sm, int stage, bool more) {
+    const PagedArgs& p = a.p;
+    const CacheView& cache = p.cache;
+    const int lane = threadIdx.x & 31, rows = 1 << a.box_shift;
+    if (index_of(a, base) >= window + 32) {
+      window += 32;
+      near = far;
+      far = entry(window + 32 + lane);
     }
+    // Page and slot of this lane's box.
+    const int32_t first = base + (lane << a.box_shift), index = index_of(a, first), in = index - window;
+    const int32_t slot = first - index * cache.page_size;
+    const int32_t from_near = __shfl_sync(0xffffffffu, near, in & 31), from_far = __shfl_sync(0xffffffffu, far, in & 31);
+    const int32_t page = (lane << a.box_shift) < kUnit && first < at.len ? (in < 32 ? from_near : from_far) : -1;
     const bool live = static_cast<uint32_t>(page) < static_cast<uint32_t>(cache.pages);
     const uint32_t boxes = __ballot_sync(0xffffffffu, live);
     // Lane w makes the mask of slab w: the tokens whose box is live, up to the sequence's end.
@@ -409,14 +433,12 @@ __device__ __forceinline__ void produce_boxes(const SplitArgs& a, const Maps& ma
     uint64_t* bar = &sm.full[stage];
     if (a.bulk_scales == 0) {
 #pragma unroll
-      for (int q = 0; q < kQ; ++q) {
+      for (int q = 0; q < kUnit / 32; ++q) {
         const int from = (32 * q + lane) >> a.box_shift;  // the lane whose box holds this lane's token
         const int32_t pg = __shfl_sync(0xffffffffu, page, from), sl = __shfl_sync(0xffffffffu, slot, from);
-        const bool have = (boxes >> from) & 1u;
-        const int64_t srow = have ? pg * cache.s_page_stride + head * cache.s_head_stride +
-                                        (sl + ((32 * q + lane) & (rows - 1))) * cache.s_token_stride
-                                  : 0;
-        if (have) {
+        if ((boxes >> from) & 1u) {
+          const int64_t srow = pg * cache.s_page_stride + head * cache.s_head_stride +
+                               (sl + ((32 * q + lane) & (rows - 1))) * cache.s_token_stride;
           cp_async4(smem_addr(&sm.scales[stage][0][32 * q + lane]), cache.k_scale + srow);
           cp_async4(smem_addr(&sm.scales[stage][1][32 * q + lane]), cache.v_scale + srow);
         }
@@ -446,22 +468,39 @@ __device__ __forceinline__ void produce_boxes(const SplitArgs& a, const Maps& ma
         bulk_g2s(&sm.scales[stage][1][row], cache.v_scale + srow, 4u * rows, bar);
       }
     }
-    if (u + 1 < units) {
+    if (more) {
       base += kUnit;
       if (--at.left == 0) {
         at.next_head(a);
         base = 0;
-        enter();
+        enter(a);
       }
-      look_up();
     }
+  }
+};
+
+// The producer warp: `units` units from the one at `at` on.
+template <int DP, int HG>
+__device__ __forceinline__ void produce_boxes(const SplitArgs& a, const Maps& maps, Shared<DP, HG>& sm, Place<DP, HG> at,
+                                              int32_t units) {
+  constexpr int kStages = Shared<DP, HG>::kStages;
+  BoxFeed<DP, HG> feed;
+  feed.at = at;
+  feed.base = (tiles_of<DP, HG>(at.len) - at.left) * Item<DP, HG>::kUnit;
+  feed.enter(a);
+  int stage = 0;
+  uint32_t phase = 1;  // the first round finds every stage empty
+  int32_t u = 0;
+  for (; u < units; ++u) {
+    if (u >= kStages && !__all_sync(0xffffffffu, mbar_wait(kWaitLimitNs, &sm.empty[stage], phase))) break;
+    feed.issue(a, maps, sm, stage, u + 1 < units);
     if (++stage == kStages) {
       stage = 0;
       phase ^= 1u;
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  if (!ok) {
+  if (u < units) {
     flag_failure(a.status);
     // Let the copies already issued land before this CTA's shared memory goes away.
     for (int32_t j = max(0, u - kStages); j < u; ++j)
@@ -591,8 +630,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   // This warp's tokens of a unit, columns and heads of an item.
   constexpr int CG = Item<DP, HG>::CG;
   const int slab = warp % kSlabs, cols = CG == 1 ? 0 : warp / kSlabs % CG, group = warp / (kSlabs * CG);
-  uint4 q[DP / 64];
-  float qf = 0.f, m = kLowest, mo = kLowest, l = 0.f;  // of head g, the same in the four threads of its row
+  // Query fragments (fp16): word j of piece i of head g.
+  constexpr bool kQueryHeld = DP <= 128;
+  uint4 q[kQueryHeld ? DP / 32 : 1];
+  // Of heads 2c and 2c + 1, the same in the eight threads that share them (l: of this thread's tokens only).
+  float qf[2] = {0.f, 0.f}, m[2], mo[2], l[2];
   // Output tiles of 16 columns x 8 heads: o[n][2h + e] is column 16g + .. + h of head 2c + e.
   constexpr int kN = DP == 64 ? 4 : 8;
   float o[kN][4];
@@ -615,11 +657,24 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int i = 0; i < DP / 64; ++i) {
         const int d = i < 2 * S::kA ? 128 * (i >> 1) + 16 * (2 * c + (i & 1)) : 128 * S::kA + 16 * c;
-        q[i] = h < rows && d < p.D ? __ldg(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 v = h < rows && d < p.D ? __ldg(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (kQueryHeld) {
+          codes_f16(v.x, q[2 * i].x, q[2 * i].y);
+          codes_f16(v.y, q[2 * i].z, q[2 * i].w);
+          codes_f16(v.z, q[2 * i + 1].x, q[2 * i + 1].y);
+          codes_f16(v.w, q[2 * i + 1].z, q[2 * i + 1].w);
+        } else if (slab == 0 && cols == 0) {  // the last head's readers have passed its join
+          sm.query[group][i][lane] = v;
+        }
       }
-      qf = h < rows ? __ldg(p.q_scale + static_cast<int64_t>(use.b) * p.q_scale_stride + head0 + h) * p.scale_log2 : 0.f;
-      m = mo = kLowest;
-      l = 0.f;
+      if constexpr (!kQueryHeld) consumer_barrier();
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int32_t he = kHeads * group + 2 * c + e;
+        qf[e] = he < rows ? __ldg(p.q_scale + static_cast<int64_t>(use.b) * p.q_scale_stride + head0 + he) * p.scale_log2 : 0.f;
+        m[e] = mo[e] = kLowest;
+        l[e] = 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < kN; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     }
@@ -630,47 +685,75 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t live = sm.live[stage][slab];
     if (live != 0u) {
       const unsigned char* kt = sm.codes[stage][0];
-      float s[2][4] = {};  // rows 8..15 of the score tile stay empty
-#pragma unroll
+      // Scores of tokens g (0, 1) and g + 8 (2, 3) with heads 2c and 2c + 1; two chains of sums.
+      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll kQueryHeld ? DP / 64 : 1  // loads of more than one iteration at a time spill above head size 128
       for (int i = 0; i < DP / 64; ++i) {
         const int at = i < 2 * S::kA ? 128 * Sm::kUnit * (i >> 1) + 2048 * slab + spot128(g, 2 * c + (i & 1))
                                      : 128 * Sm::kUnit * S::kA + 1024 * slab + spot64(g, c);
         const uint4 k0 = *reinterpret_cast<const uint4*>(kt + at);
         const uint4 k1 = *reinterpret_cast<const uint4*>(kt + at + (i < 2 * S::kA ? 1024 : 512));  // row g + 8
-        mma_e4m3(s[0], q[i].x, 0u, q[i].y, 0u, k0.x, k0.y);
-        mma_e4m3(s[1], q[i].x, 0u, q[i].y, 0u, k1.x, k1.y);
-        mma_e4m3(s[0], q[i].z, 0u, q[i].w, 0u, k0.z, k0.w);
-        mma_e4m3(s[1], q[i].z, 0u, q[i].w, 0u, k1.z, k1.w);
-      }
-      // Score 2u + e of a thread is token 2c + e + 8u.
-      const float* sk = &sm.scales[stage][0][kStep * slab + 2 * c];
-      const float* sv = &sm.scales[stage][1][kStep * slab + 2 * c];
-      const float2 ka = *reinterpret_cast<const float2*>(sk), kb = *reinterpret_cast<const float2*>(sk + 8);
-      const float2 va = *reinterpret_cast<const float2*>(sv), vb = *reinterpret_cast<const float2*>(sv + 8);
-      float x[4] = {s[0][0] * (qf * ka.x), s[0][1] * (qf * ka.y), s[1][0] * (qf * kb.x), s[1][1] * (qf * kb.y)};
-      float w[4] = {x[0] + lg2(va.x), x[1] + lg2(va.y), x[2] + lg2(vb.x), x[3] + lg2(vb.y)};
-      if (live != 0xffffu) {
+        uint4 qc;
+        if constexpr (!kQueryHeld) qc = sm.query[group][i][lane];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (!((live >> (2 * c + (e & 1) + 8 * (e >> 1))) & 1u)) x[e] = w[e] = -CUDART_INF_F;
-      }
-      const float mn = quad_max(fmaxf(fmaxf(m, fmaxf(x[0], x[1])), fmaxf(x[2], x[3])));
-      const float on = quad_max(fmaxf(fmaxf(mo, fmaxf(w[0], w[1])), fmaxf(w[2], w[3])));
-      l = fmaf(l, ex2(m - mn), (ex2(x[0] - mn) + ex2(x[1] - mn)) + (ex2(x[2] - mn) + ex2(x[3] - mn)));
-      const float keep = ex2(mo - on);
-      m = mn;
-      mo = on;
-      const uint32_t p0 = pack_f16(ex2(w[0] - on), ex2(w[1] - on)), p1 = pack_f16(ex2(w[2] - on), ex2(w[3] - on));
-      if (__any_sync(0xffffffffu, keep != 1.f)) {
-        const float k0 = __shfl_sync(0xffffffffu, keep, 8 * c), k1 = __shfl_sync(0xffffffffu, keep, 8 * c + 4);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          o[i][0] *= k0;
-          o[i][1] *= k1;
-          o[i][2] *= k0;
-          o[i][3] *= k1;
+        for (int j = 0; j < 4; ++j) {
+          uint32_t a0, a1, a2, a3, b0, b1;
+          codes_f16(word(k0, j), a0, a2);
+          codes_f16(word(k1, j), a1, a3);
+          if constexpr (kQueryHeld) {
+            const uint4 qi = q[2 * i + (j >> 1)];
+            b0 = j & 1 ? qi.z : qi.x;
+            b1 = j & 1 ? qi.w : qi.y;
+          } else {
+            codes_f16(word(qc, j), b0, b1);
+          }
+          mma_f16(j & 1 ? s1 : s0, a0, a1, a2, a3, b0, b1);
         }
       }
+      const float* sk = &sm.scales[stage][0][kStep * slab + g];
+      const float* sv = &sm.scales[stage][1][kStep * slab + g];
+      const float ks[2] = {sk[0], sk[8]}, lv[2] = {lg2(sv[0]), lg2(sv[8])};
+      float x[2][2], w[2][2];  // [token][head]
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x[t][e] = (s0[2 * t + e] + s1[2 * t + e]) * (qf[e] * ks[t]);
+          w[t][e] = x[t][e] + lv[t];
+        }
+      if (live != 0xffffu) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (!((live >> (g + 8 * t)) & 1u)) x[t][0] = x[t][1] = w[t][0] = w[t][1] = -CUDART_INF_F;
+      }
+      bool above = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        above = above || fmaxf(x[0][e], x[1][e]) > m[e] + kSlack || fmaxf(w[0][e], w[1][e]) > mo[e] + kSlack;
+      if (__any_sync(0xffffffffu, above)) {
+        float keep[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float mn = fmaxf(m[e], column_max(fmaxf(x[0][e], x[1][e])));
+          const float on = fmaxf(mo[e], column_max(fmaxf(w[0][e], w[1][e])));
+          l[e] *= ex2(m[e] - mn);
+          keep[e] = ex2(mo[e] - on);
+          m[e] = mn;
+          mo[e] = on;
+        }
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          o[i][0] *= keep[0];
+          o[i][1] *= keep[1];
+          o[i][2] *= keep[0];
+          o[i][3] *= keep[1];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) l[e] += ex2(x[0][e] - m[e]) + ex2(x[1][e] - m[e]);
+      // Weights: (tokens x heads) pairs of heads -> B fragments, pairs of tokens of head g.
+      const uint32_t p0 = transpose8(pack_f16(ex2(w[0][0] - mo[0]), ex2(w[0][1] - mo[1])));
+      const uint32_t p1 = transpose8(pack_f16(ex2(w[1][0] - mo[0]), ex2(w[1][1] - mo[1])));
       const unsigned char* vt = sm.codes[stage][1];
       if (S::kA > 0 && (S::kA == CG || cols == 0)) {
         uint4 v[4];
@@ -723,12 +806,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     const bool done = --use.left == 0;
     if (done || u + 1 == units) {
       const bool whole = done && from_start;
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (c == 0) {
-        sm.stat[warp][g][0] = m;
-        sm.stat[warp][g][1] = mo;
-        sm.stat[warp][g][2] = l;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[e] += __shfl_xor_sync(0xffffffffu, l[e], d);
+        if (g == 0) {
+          sm.stat[warp][2 * c + e][0] = m[e];
+          sm.stat[warp][2 * c + e][1] = mo[e];
+          sm.stat[warp][2 * c + e][2] = l[e];
+        }
       }
       consumer_barrier();
       float f[2];  // brings heads 2c and 2c + 1 to the largest M of the warps that share them
@@ -737,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         float top = kLowest;
 #pragma unroll
         for (int w = 0; w < kSlabs; ++w) top = fmaxf(top, sm.stat[group * (CG * kSlabs) + w][2 * c + e][1]);
-        f[e] = ex2(sm.stat[warp][2 * c + e][1] - top);
+        f[e] = ex2(mo[e] - top);
       }
       // Thread (warp, lane) finishes head 8r + warp of the item, column `lane` of each piece of 32.
       const int64_t slot = 2 * static_cast<int64_t>(cta) + (first_segment ? 0 : 1);
