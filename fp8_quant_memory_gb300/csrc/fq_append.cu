@@ -49,9 +49,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   const int lane = threadIdx.x & (LPR - 1), grp = threadIdx.x / LPR;
   const int N = a.N, nv = N >> 3, hv = (N - a.R) >> 3, th = a.R >> 4, half = a.R >> 1;
   const int32_t rows = static_cast<int32_t>(a.rows);
-  for (int32_t base = blockIdx.x * kRowsPerCta; base < rows; base += gridDim.x * kRowsPerCta) {
-    const int32_t r = base + grp;
-    const bool inside = r < rows;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kRowsPerCta; base < rows; base += static_cast<int64_t>(gridDim.x) * kRowsPerCta) {
+    const bool inside = base + grp < rows;
+    const int32_t r = inside ? static_cast<int32_t>(base) + grp : 0;
     const int32_t t = inside ? r / a.H : 0, h = inside ? r - t * a.H : 0;
     const bool is_q = h < a.Hq, is_v = h >= a.Hq + p.Hk;
     const T* x = static_cast<const T*>(a.x) + (static_cast<int64_t>(t) * a.token_stride + static_cast<int64_t>(h) * N);

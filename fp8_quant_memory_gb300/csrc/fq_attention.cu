@@ -1073,6 +1073,9 @@ size_t attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hk, int64_t D, i
 bool launch_attention_split(const PagedArgs& p, int dtype, cudaStream_t s) {
   const Plan plan = plan_of(p.B, p.Hq, p.Hk, p.D, p.max_len);
   if (plan.units > 0x7fffffffLL - 0x10000) return false;  // units are counted in 32 bits
+  // A warp passes over sequences without tokens one by one, about half a microsecond each, while others wait for it in
+  // waits of a second at most.
+  if (p.B > 65536) return false;
   SplitArgs a{};
   a.p = p;
   a.G = p.Hq / p.Hk;

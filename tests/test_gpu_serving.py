@@ -111,6 +111,18 @@ def test_matmul_nan_and_zero_scales(M):
     assert bool((fq.fp8_matmul(a, sa2, b, sb)[0] == 0).all())
 
 
+def test_matmul_operand_beyond_32_bits():
+    """Rows of a behind its first 2^32 bytes."""
+    M, N, K = 33000, 48, 131072
+    a = torch.zeros(M, K, dtype=torch.uint8, device="cuda")
+    sa = torch.ones(M, K // 128, device="cuda")
+    tail, stail, b, sb = matmul_inputs(20, N, K, seed=4)
+    a[-20:], sa[-20:] = tail, stail
+    out = fq.fp8_matmul(a, sa, b, sb)
+    ref.assert_matmul(out[-20:], tail, stail, b, sb)
+    assert not bool(out[:-20].any())
+
+
 def test_matmul_empty():
     a, sa, b, sb = matmul_inputs(4, 6, 128, seed=1)
     assert fq.fp8_matmul(a[:0], sa[:0], b, sb).shape == (0, 6)
@@ -174,6 +186,9 @@ APPEND_CASES = [
     (23, 4, 4, 128, 128, 16, "bf16", "fp16", 0, 448.0, "phtd"),
     (1500, 8, 2, 128, 128, 64, "bf16", "fp32", 0, 448.0, "phtd"),
     (1300, 7, 3, 128, 128, 64, "fp16", "fp32", 0, 448.0, "pthd"),
+    (700, 16, 8, 128, 128, 24, "bf16", "bf16", 0, 240.0, "phtd"),
+    (6000, 0, 2, 128, 128, 64, "fp16", "fp16", 0, 448.0, "phtd"),
+    (400, 32, 8, 128, 128, 64, "bf16", "fp32", 0, 448.0, "hptd"),
 ]
 
 
@@ -249,6 +264,28 @@ def test_append_matches_prologue():
     at, off = slots // 64, slots % 64
     assert_codes_close(cache[0][at, :, off], pq[:, 32:].cpu())
     assert_scale_close(cache[2][at, :, off], ps[:, 32:].cpu())
+
+
+def test_append_rows_beyond_32_bits():
+    """A QKV batch of more than 2^31 elements: the last tokens as a small batch of them gives them."""
+    T, Hq, Hk, D, page, n = 360000, 32, 8, 128, 64, 40
+    d, small, _ = append_inputs((n, Hq, Hk, D, D, page, "bf16", "fp32", 0, 448.0, "phtd"))
+    qkv = torch.zeros(T, (Hq + 2 * Hk) * D, dtype=torch.bfloat16, device="cuda")
+    cos, sin = torch.ones(T, D // 2, device="cuda"), torch.zeros(T, D // 2, device="cuda")
+    qkv[-n:], cos[-n:], sin[-n:] = d["qk"], d["cos"], d["sin"]
+    P = T // page
+    big = [torch.zeros(P, Hk, page, D, dtype=torch.uint8, device="cuda") for _ in range(2)] + \
+        [torch.zeros(P, Hk, page, device="cuda") for _ in range(2)]
+    slots = torch.arange(T, device="cuda")
+    q, qs = fq.qkv_norm_rope_append(qkv, d["wq"], d["wk"], cos, sin, slots, *big, Hq, Hk)
+    q1, qs1 = fq.qkv_norm_rope_append(d["qk"], d["wq"], d["wk"], d["cos"], d["sin"], slots[:n], *small, Hq, Hk)
+    assert_codes_close(q[-n:], q1.cpu())
+    assert_scale_close(qs[-n:], qs1.cpu())
+    at, off = slots[-n:] // page, slots[-n:] % page
+    for x, y in zip(big[:2], small[:2]):
+        assert_codes_close(x[at, :, off], y[0, :, :n].transpose(0, 1).cpu())
+    for x, y in zip(big[2:], small[2:]):
+        assert_scale_close(x[at, :, off], y[0, :, :n].transpose(0, 1).cpu())
 
 
 def test_append_zero_rows_and_empty():
@@ -338,6 +375,30 @@ def test_attention(case):
 def test_attention_many_sequences():
     lens = [(37 * i) % 300 for i in range(700)]
     check_attention(attention_inputs(lens, 4, 2, 64, 16, seed=61))
+
+
+def test_attention_very_many_sequences():
+    """More sequences than the split kernel takes: most of them empty."""
+    lens = [0] * 70000
+    lens[0], lens[123], lens[69999] = 20, 5, 33
+    x = attention_inputs(lens, 2, 1, 64, 16, seed=76)
+    check_attention(x)
+    small = [t[:3000].contiguous() for t in (x[0], x[1])] + x[2:6] + [x[6][:3000].contiguous(), x[7][:3000].contiguous()]
+    check_attention(small)
+
+
+def test_attention_maxima_that_grow():
+    """Scores that rise along the sequence, by less and by more than the slack of the running maxima."""
+    for step in (0.02, 0.3, 3.0):
+        x = attention_inputs([900, 130], 8, 2, 128, 16, seed=77)
+        x[0].fill_(0x38)  # q = 1 throughout
+        x[2].fill_(0x38)
+        x[1].fill_(1.0)
+        table, lens = x[6].cpu(), x[7].cpu()
+        for b, n in enumerate(lens.tolist()):
+            pos = torch.arange(n)
+            x[4][table[b, pos // 16].long().cuda(), :, (pos % 16).cuda()] = (pos * step / 128 + 1e-3).float().cuda()[:, None]
+        check_attention(x, scale=1.0)
 
 
 def test_attention_all_empty():
