@@ -28,11 +28,12 @@
 // The running maxima are only brought up to date when a score exceeds one by more than 2^8 (a vote; then three
 // shuffles per head and the rescaling): weights of up to 2^8 lose nothing in fp16 and fp32.
 //
-// Split. The work is a list of units (128 tokens of one sequence and key head, 16 per warp) in the order
-// sequence, head, tokens; CTA i of n takes units [i*U/n, (i+1)*U/n). The lengths are on the device, so each
-// CTA finds its range itself. A run of units of one head that is not the whole head goes to the workspace
-// as a partial result, at most two per CTA (its first and its last), and a second kernel joins them in
-// order: no atomics, and the same bits on every run.
+// Split. The work is a list of units in the order sequence, head, tokens, and behind each head one place more, which
+// stands for the time its end takes (the warps' results are joined and written: about as long as a unit, 1.2 us; a
+// batch with many short sequences was held up by the CTAs that had them). The n CTAs take equal ranges of places. The
+// lengths are on the device, so each CTA finds its range itself. A run of units of one head that is not the whole head
+// goes to the workspace as a partial result, at most two per CTA (its first and its last), and a second kernel joins
+// them in order: no atomics, and the same bits on every run.
 #include <math_constants.h>
 
 #include "fq_device.cuh"
@@ -92,8 +93,9 @@ struct Shared {
   float stat[kWarps][kHeads][3];  // m, M, l
   alignas(8) uint64_t full[kStages];
   uint64_t empty[kStages];
-  int32_t scan[kThreads / 32];
-  int32_t start_unit, start_b;
+  int64_t scan[kThreads / 32];
+  int32_t start_b, start_item, start_tile;  // where this CTA's first unit is
+  int32_t before_begin, before_end;         // units before its first place and before the next CTA's
 };
 
 // What a CTA that begins inside a head leaves for the join of that head.
@@ -218,29 +220,29 @@ struct Place {
   }
 };
 
-// The units of `total` that each of n CTAs takes: the first `rest` take each + 1, the others `each`.
+// The places of `total` that each of n CTAs takes: the first `rest` take each + 1, the others `each`.
 struct Share {
   int32_t each, rest;
   __device__ __forceinline__ Share(int32_t total, int32_t n) : each(total / n), rest(total - total / n * n) {}
   __device__ __forceinline__ int32_t begin(int32_t cta) const { return cta * each + min(cta, rest); }
-  __device__ __forceinline__ int32_t owner(int32_t unit) const {
+  __device__ __forceinline__ int32_t owner(int32_t place) const {
     const int32_t wide = rest * (each + 1);
-    return unit < wide ? unit / (each + 1) : rest + (unit - wide) / each;
+    return place < wide ? place / (each + 1) : rest + (place - wide) / each;
   }
 };
 
 // The block's inclusive sum of v over its threads.
-__device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* scan, int32_t* total) {
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scan, int64_t* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   __syncthreads();
   if (lane == 31) scan[warp] = v;
   __syncthreads();
-  int32_t before = 0, all = 0;
+  int64_t before = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += scan[w];
@@ -248,6 +250,28 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* scan, int32_t*
   }
   *total = all;
   return v + before;
+}
+
+// What a sequence adds to the list: its units in the high half, its places in the low half. Sums of a whole batch fit
+// 31 bits each.
+template <int DP, int HG>
+__device__ __forceinline__ int64_t extent_of(const SplitArgs& a, int32_t b) {
+  const int32_t tiles = b < a.p.B ? tiles_of<DP, HG>(length_of(a.p, b)) : 0, heads = a.p.Hk * a.chunks;
+  return tiles == 0 ? 0 : (static_cast<int64_t>(tiles * heads) << 32) + (tiles + 1) * heads;
+}
+
+__device__ __forceinline__ int32_t units_in(int64_t extent) { return static_cast<int32_t>(extent >> 32); }
+__device__ __forceinline__ int32_t places_in(int64_t extent) { return static_cast<int32_t>(extent & 0xffffffffll); }
+
+// Sequences without tokens get zeros and -inf, spread over the CTAs; by `threads` threads of each.
+__device__ __forceinline__ void write_empty(const PagedArgs& p, int threads) {
+  for (int32_t b = blockIdx.x; b < p.B; b += gridDim.x) {
+    if (length_of(p, b) != 0) continue;
+    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(b) * p.Hq * p.D);
+    for (int32_t i = threadIdx.x; i < p.Hq * p.D / 8; i += threads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (p.lse != nullptr)
+      for (int32_t h = threadIdx.x; h < p.Hq; h += threads) p.lse[static_cast<int64_t>(b) * p.Hq + h] = -CUDART_INF_F;
+  }
 }
 
 // A producer warp, any page size and layout of scales: copies its share (tokens kTok * half ..) of the units
@@ -554,75 +578,84 @@ __global__ void __launch_bounds__(kThreads, 2)
     fence_barrier_init();
   }
 
-  // This CTA's units [begin, end) of all, and the place of the first. (block_scan's barriers also publish
-  // the mbarriers.)
-  const int32_t per_tile = p.Hk * a.chunks;
-  int32_t total = 0, incl = 0, mine = 0;
+  // This CTA's places [begin, end) of all, and its first unit. (block_scan's barriers also publish the mbarriers.)
+  int64_t total = 0, incl = 0, mine = 0;
   for (int32_t b0 = 0; b0 < p.B; b0 += kThreads) {
-    const int32_t b = b0 + static_cast<int32_t>(threadIdx.x);
-    const int32_t len = b < p.B ? length_of(p, b) : 0;
-    mine = tiles_of<DP, HG>(len) * per_tile;
-    int32_t sum;
+    mine = extent_of<DP, HG>(a, b0 + static_cast<int32_t>(threadIdx.x));
+    int64_t sum;
     incl = block_scan(mine, sm.scan, &sum);
     total += sum;
-    // Sequences without tokens: zeros and -inf, spread over the CTAs.
-    if (b < p.B && len == 0 && b % gridDim.x == blockIdx.x) {
-      uint16_t* o = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(b) * p.Hq * p.D;
-      for (int64_t i = 0; i < static_cast<int64_t>(p.Hq) * p.D; i += 8)
-        *reinterpret_cast<uint4*>(o + i) = make_uint4(0u, 0u, 0u, 0u);
-      if (p.lse != nullptr)
-        for (int32_t h = 0; h < p.Hq; ++h) p.lse[static_cast<int64_t>(b) * p.Hq + h] = -CUDART_INF_F;
-    }
   }
-  const int32_t n = min(static_cast<int32_t>(gridDim.x), total);  // CTAs with work
+  const int32_t n = min(static_cast<int32_t>(gridDim.x), units_in(total));  // CTAs with places
   const int32_t cta = blockIdx.x;
   if (cta >= n) {
     if (threadIdx.x == 0 && a.meta != nullptr) a.meta[cta].b = -1;
+    write_empty(p, kThreads);
     return;
   }
-  const Share share(total, n);
-  const int32_t begin = share.begin(cta), units = share.begin(cta + 1) - begin;
-  if (p.B <= kThreads) {
-    if (incl - mine <= begin && begin < incl) {
-      sm.start_b = threadIdx.x;
-      sm.start_unit = begin - (incl - mine);
-    }
-  } else {
-    int32_t carry = 0;
-    for (int32_t b0 = 0; b0 < p.B && carry <= begin; b0 += kThreads) {
-      const int32_t b = b0 + static_cast<int32_t>(threadIdx.x);
-      mine = b < p.B ? tiles_of<DP, HG>(length_of(p, b)) * per_tile : 0;
-      int32_t sum;
+  const Share share(places_in(total), n);
+  const int32_t begin = share.begin(cta), end = share.begin(cta + 1);
+  int64_t carry = 0;
+  for (int32_t b0 = 0; b0 < p.B; b0 += kThreads) {
+    const int32_t b = b0 + static_cast<int32_t>(threadIdx.x);
+    if (p.B > kThreads) {  // else the scan above is this one
+      mine = extent_of<DP, HG>(a, b);
+      int64_t sum;
       incl = block_scan(mine, sm.scan, &sum) + carry;
-      if (incl - mine <= begin && begin < incl) {
-        sm.start_b = b;
-        sm.start_unit = begin - (incl - mine);
-      }
       carry += sum;
+    }
+    const int32_t from = places_in(incl - mine), to = places_in(incl);
+    const bool has_begin = from <= begin && begin < to, has_end = from < end && end <= to;
+    if (has_begin || has_end) {
+      const int32_t tiles = tiles_of<DP, HG>(length_of(p, b));
+      auto units_before = [&](int32_t place, int32_t& item, int32_t& tile) {
+        item = (place - from) / (tiles + 1);
+        tile = place - from - item * (tiles + 1);
+        return units_in(incl - mine) + item * tiles + tile;
+      };
+      int32_t item, tile;
+      if (has_end) sm.before_end = units_before(end, item, tile);
+      if (has_begin) {
+        sm.before_begin = units_before(begin, item, tile);
+        sm.start_b = b;
+        sm.start_item = item;
+        sm.start_tile = tile;
+      }
     }
   }
   __syncthreads();
   Place<DP, HG> use;
   use.b = sm.start_b;
+  use.item = sm.start_item;
   use.len = length_of(p, use.b);
   const int32_t nt = tiles_of<DP, HG>(use.len);
-  use.item = sm.start_unit / nt;
-  const int32_t t = sm.start_unit - use.item * nt;
+  int32_t t = sm.start_tile;
+  const int32_t units = sm.before_end - sm.before_begin;
+  const int32_t first = begin - t;  // the head's first place
   use.left = nt - t;
+  if (units > 0 && use.left == 0) {  // the place behind a head
+    use.next_head(a);
+    t = 0;
+  }
+  if (units == 0) {
+    if (threadIdx.x == 0 && a.meta != nullptr) a.meta[cta].b = -1;
+    write_empty(p, kThreads);
+    return;
+  }
   if (warp >= kWarps) {
     if constexpr (!kBoxes) produce_rows<DP, HG>(a, sm, use, units, warp - kWarps);
     else if (warp == kWarps) produce_boxes<DP, HG>(a, maps, sm, use, units);
     return;
   }
   if (threadIdx.x == 0 && a.meta != nullptr) {
-    // The head this CTA begins inside is joined by the second CTA that has a part of it.
-    const int32_t first = begin - t;  // the head's first unit
+    // The head this CTA begins inside is joined by the second CTA that has a part of it. The head's first part is the
+    // first thing its CTA does if that begins at the head's first place, or one before it, behind the head before.
     const int32_t i0 = share.owner(first);
     Meta m;
     m.b = t > 0 && i0 == cta - 1 ? use.b : -1;
     m.item = use.item;
     m.last = share.owner(first + nt - 1);
-    m.slot = share.begin(i0) == first ? 0 : 1;
+    m.slot = share.begin(i0) >= first - 1 ? 0 : 1;
     a.meta[cta] = m;
   }
 
@@ -882,6 +915,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (u + 1 < units) use.next_head(a);
     }
   }
+  write_empty(p, kConsumers);
 }
 
 // Joins the partial results of one head: CTA (k, row) takes the head that CTA k of the first kernel began
@@ -1072,7 +1106,7 @@ size_t attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hk, int64_t D, i
 
 bool launch_attention_split(const PagedArgs& p, int dtype, cudaStream_t s) {
   const Plan plan = plan_of(p.B, p.Hq, p.Hk, p.D, p.max_len);
-  if (plan.units > 0x7fffffffLL - 0x10000) return false;  // units are counted in 32 bits
+  if (plan.units > 0x3fffffffLL) return false;  // units, and places up to twice as many, are counted in 32 bits
   // A warp passes over sequences without tokens one by one, about half a microsecond each, while others wait for it in
   // waits of a second at most.
   if (p.B > 65536) return false;
