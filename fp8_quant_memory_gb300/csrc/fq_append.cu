@@ -49,6 +49,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   const int lane = threadIdx.x & (LPR - 1), grp = threadIdx.x / LPR;
   const int N = a.N, nv = N >> 3, hv = (N - a.R) >> 3, th = a.R >> 4, half = a.R >> 1;
   const int32_t rows = static_cast<int32_t>(a.rows);
+  pdl_trigger();
+  pdl_wait();
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * kRowsPerCta; base < rows; base += static_cast<int64_t>(gridDim.x) * kRowsPerCta) {
     const bool inside = base + grp < rows;
     const int32_t r = inside ? static_cast<int32_t>(base) + grp : 0;
@@ -115,7 +117,7 @@ bool launch_shape(const AppendArgs& p, cudaStream_t s) {
   auto kern = append_kernel<T, TT, LPR, HS, TS>;
   constexpr int kRowsPerCta = kThreads / LPR;
   const int64_t need = (p.rows.rows + kRowsPerCta - 1) / kRowsPerCta, cap = static_cast<int64_t>(sm_count()) * 8;
-  kern<<<static_cast<unsigned>(need < cap ? need : cap), kThreads, 0, s>>>(p);
+  launch_overlapped(kern, dim3(static_cast<unsigned>(need < cap ? need : cap)), kThreads, 0, 1, s, p);
   return true;
 }
 
@@ -321,6 +323,8 @@ __global__ void __launch_bounds__(kSThreads, 2) append_stream_kernel(const __gri
     }
     fence_barrier_init();
   }
+  pdl_trigger();
+  pdl_wait();
   if (threadIdx.x < 32)
     *reinterpret_cast<uint4*>(weights + 16 * threadIdx.x) =
         ld_cached16(static_cast<const T*>(threadIdx.x < 16 ? r.wq : r.wk) + 8 * (threadIdx.x & 15));
@@ -435,7 +439,7 @@ bool launch_stream(const AppendArgs& p, cudaStream_t s) {
   auto kern = p.rows.fp8_max != 448.0f ? append_stream_kernel<T, TT, true> : append_stream_kernel<T, TT, false>;
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem)) return false;
   const int32_t resident = 2 * sm_count();
-  kern<<<static_cast<unsigned>(a.chunks < resident ? a.chunks : resident), kSThreads, smem, s>>>(a);
+  launch_overlapped(kern, dim3(static_cast<unsigned>(a.chunks < resident ? a.chunks : resident)), kSThreads, smem, 1, s, a);
   return true;
 }
 

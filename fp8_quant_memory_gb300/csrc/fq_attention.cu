@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   const PagedArgs& p = a.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  pdl_trigger();
   if (kBoxes && threadIdx.x == kConsumers) {
     if (S::kA > 0) {
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.k128)) : "memory");
@@ -563,6 +563,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&maps.v64)) : "memory");
     }
   }
+  if (threadIdx.x < Sm::kStages) {
+    // full: lane 0 of a producer for its masks and boxes, and each lane's own copies where there are any
+    mbar_init(&sm.full[threadIdx.x], kBoxes ? (a.bulk_scales != 0 ? 1 : 33) : 33 * kProducers);
+    mbar_init(&sm.empty[threadIdx.x], kWarps);
+    fence_barrier_init();
+  }
+
+  pdl_wait();
   // Bring the page table to the L2 cache while the lengths are on their way: one line per thread of the grid,
   // as far as that goes.
   if (p.max_len > 0) {
@@ -571,13 +579,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (b < static_cast<uint32_t>(p.B))
       asm volatile("prefetch.global.L2 [%0];" ::"l"(p.table + b * p.table_stride + (i - b * width)));
   }
-  if (threadIdx.x < Sm::kStages) {
-    // full: lane 0 of a producer for its masks and boxes, and each lane's own copies where there are any
-    mbar_init(&sm.full[threadIdx.x], kBoxes ? (a.bulk_scales != 0 ? 1 : 33) : 33 * kProducers);
-    mbar_init(&sm.empty[threadIdx.x], kWarps);
-    fence_barrier_init();
-  }
-
   // This CTA's places [begin, end) of all, and its first unit. (block_scan's barriers also publish the mbarriers.)
   int64_t total = 0, incl = 0, mine = 0;
   for (int32_t b0 = 0; b0 < p.B; b0 += kThreads) {
@@ -926,7 +927,8 @@ __global__ void __launch_bounds__(kConsumers) attention_join_kernel(const __grid
   constexpr int kV = DP / 64;  // float2 per lane
   __shared__ float2 sum[kWarps][DP / 2];
   __shared__ float4 stat[kWarps];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  pdl_trigger();
+  pdl_wait();
   const int64_t k = blockIdx.x + 1;
   const Meta me = a.meta[k];
   const PagedArgs& p = a.p;
@@ -1034,18 +1036,11 @@ bool launch_fed(const SplitArgs& a, const Maps& maps, const Plan& plan, cudaStre
   constexpr size_t smem = sizeof(Shared<DP, HG>) + 1024;
   static_assert(smem <= 227 * 1024 && (smem + 1024) * 2 <= 228 * 1024, "the ring fits the SM");
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem)) return false;
-  kern<<<static_cast<unsigned>(plan.grid), kThreads, smem, s>>>(maps, a);
-  if (!plan.join) return true;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(plan.grid - 1), a.G < Item<DP, HG>::kRows ? a.G : Item<DP, HG>::kRows);
-  cfg.blockDim = dim3(kConsumers);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, attention_join_kernel<DP, HG>, a);  // a failure is reported by the caller's check
+  launch_overlapped(kern, dim3(static_cast<unsigned>(plan.grid)), kThreads, smem, 1, s, maps, a);
+  if (plan.join)
+    launch_overlapped(attention_join_kernel<DP, HG>,
+                      dim3(static_cast<unsigned>(plan.grid - 1), a.G < Item<DP, HG>::kRows ? a.G : Item<DP, HG>::kRows), kConsumers, 0,
+                      1, s, a);
   return true;
 }
 

@@ -109,7 +109,11 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
       mbar_init(&sm.free_[b], 4);
     }
     fence_barrier_init();
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&wmap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&amap)) : "memory");
   }
+  pdl_trigger();
+  pdl_wait();
   if (warp == 5) tmem_alloc<1>(&sm.tmem, C::kCols);
   tc_fence_before();
   __syncthreads();
@@ -298,19 +302,8 @@ bool launch_narrow(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
   constexpr size_t smem = sizeof(NarrowShared<NT>) + 1024;
   static_assert(smem <= 227 * 1024, "the ring fits the SM");
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem)) return false;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(split), static_cast<unsigned>(p.tiles_n), static_cast<unsigned>(p.tiles_m));
-  cfg.blockDim = dim3(kNarrowThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kern, wmap, amap, p);  // a failure is reported by the caller's check
+  launch_overlapped(kern, dim3(static_cast<unsigned>(split), static_cast<unsigned>(p.tiles_n), static_cast<unsigned>(p.tiles_m)),
+                    kNarrowThreads, smem, static_cast<unsigned>(split), s, wmap, amap, p);
   return true;
 }
 
@@ -441,7 +434,7 @@ __device__ __forceinline__ void wide_store(const MmArgs& p, const CUtensorMap* o
   }
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
+__global__ void __launch_bounds__(kWideThreads, 1)
     matmul_wide_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
                        const __grid_constant__ CUtensorMap omap, const __grid_constant__ MmArgs p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -460,7 +453,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWideThreads, 1)
       mbar_init(&sm.free_[b], 16);
     }
     fence_barrier_init();
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&amap)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&wmap)) : "memory");
   }
+  pdl_trigger();
+  pdl_wait();
   if (warp == 1) tmem_alloc<2>(&sm.tmem, 512);
   tc_fence_before();
   __syncthreads();
@@ -598,8 +595,8 @@ bool launch_wide(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
   constexpr size_t smem = sizeof(WideShared) + 1024;
   static_assert(smem <= 227 * 1024, "the ring and the staging rows fit the SM");
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(matmul_wide_kernel), smem)) return false;
-  matmul_wide_kernel<<<static_cast<unsigned>(2 * (p.pieces < pairs ? p.pieces : pairs)), kWideThreads, smem, s>>>(amap, wmap,
-                                                                                                               omap, p);
+  launch_overlapped(matmul_wide_kernel, dim3(static_cast<unsigned>(2 * (p.pieces < pairs ? p.pieces : pairs))), kWideThreads, smem, 2, s,
+                    amap, wmap, omap, p);
   return true;
 }
 

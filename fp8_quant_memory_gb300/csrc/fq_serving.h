@@ -57,6 +57,28 @@ struct PagedArgs {
   float scale_log2;  // softmax_scale * log2(e)
 };
 
+// Launches `kern` so that its set-up overlaps the tail of the previous kernel in the stream (it calls pdl_wait before
+// its first global access), in clusters of `cluster` CTAs along x. A failure is reported by the caller's check.
+template <typename... P, typename... A>
+void launch_overlapped(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t s,
+                       const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // tcgen05 kernels: 16-byte aligned operands and strides. False (nothing launched) otherwise.
 bool launch_matmul_tc(const MatmulArgs& a, int dtype, cudaStream_t s);
 void launch_matmul_scalar(const MatmulArgs& a, int dtype, cudaStream_t s);

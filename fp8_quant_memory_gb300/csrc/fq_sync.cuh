@@ -174,6 +174,12 @@ __device__ __forceinline__ void fence_barrier_init() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
+// Programmatic dependent launch: let the next kernel in the stream start its set-up; wait until the previous one has
+// finished and its writes are visible. A kernel launched with the attribute makes no global access before the wait,
+// and every CTA of it waits.
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ void flag_failure(unsigned int* status) {
   if (status != nullptr) atomicOr(status, 1u);
 }
