@@ -61,8 +61,9 @@ struct Item {
   static constexpr int kSlabs = kWarps / (HG * CG);
   static constexpr int kUnit = kStep * kSlabs;    // tokens per unit
   static constexpr int kRows = kHeads * HG;       // query heads
-  // Ring depth: what two CTAs per SM leave room for (98 KB of codes; 80 KB at head size 64, whose scales weigh more).
-  static constexpr int kStages = (DP == 64 ? 80 : 98) * 1024 / (2 * kUnit * DP);
+  // Ring depth: what two CTAs per SM leave room for beside the scales (heavy at head size 64) and the query fragments
+  // of the largest items.
+  static constexpr int kStages = (DP == 64 ? 80 : DP > 128 && HG == 2 ? 88 : 98) * 1024 / (2 * kUnit * DP);
 };
 constexpr float kSlack = 8.f;                // powers of two by which a score may exceed its running maximum
 constexpr float kLowest = -3.402823466e38f;  // below every score: a maximum before the first token
@@ -88,8 +89,8 @@ struct Shared {
   alignas(16) float scales[kStages][2][kUnit];  // K then V
   uint16_t live[kStages][Item<DP, HG>::kSlabs];  // bit t of a slab's word: its token t counts
   alignas(16) float join[kWarps][kHeads][kJoinStride];
-  // Above head size 128 the query's codes are read from here at each use: fragments in registers spill.
-  uint4 query[DP > 128 ? HG : 1][DP > 128 ? DP / 64 : 1][32];
+  // Above head size 128 the query fragments are read from here at each use: in registers they spill.
+  uint4 query[DP > 128 ? HG : 1][DP > 128 ? DP / 32 : 1][32];
   float stat[kWarps][kHeads][3];  // m, M, l
   alignas(8) uint64_t full[kStages];
   uint64_t empty[kStages];
@@ -692,13 +693,17 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int i = 0; i < DP / 64; ++i) {
         const int d = i < 2 * S::kA ? 128 * (i >> 1) + 16 * (2 * c + (i & 1)) : 128 * S::kA + 16 * c;
         const uint4 v = h < rows && d < p.D ? __ldg(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0u, 0u, 0u, 0u);
+        uint4 lo, hi;
+        codes_f16(v.x, lo.x, lo.y);
+        codes_f16(v.y, lo.z, lo.w);
+        codes_f16(v.z, hi.x, hi.y);
+        codes_f16(v.w, hi.z, hi.w);
         if constexpr (kQueryHeld) {
-          codes_f16(v.x, q[2 * i].x, q[2 * i].y);
-          codes_f16(v.y, q[2 * i].z, q[2 * i].w);
-          codes_f16(v.z, q[2 * i + 1].x, q[2 * i + 1].y);
-          codes_f16(v.w, q[2 * i + 1].z, q[2 * i + 1].w);
+          q[2 * i] = lo;
+          q[2 * i + 1] = hi;
         } else if (slab == 0 && cols == 0) {  // the last head's readers have passed its join
-          sm.query[group][i][lane] = v;
+          sm.query[group][2 * i][lane] = lo;
+          sm.query[group][2 * i + 1][lane] = hi;
         }
       }
       if constexpr (!kQueryHeld) consumer_barrier();
@@ -727,21 +732,18 @@ __global__ void __launch_bounds__(kThreads, 2)
                                      : 128 * Sm::kUnit * S::kA + 1024 * slab + spot64(g, c);
         const uint4 k0 = *reinterpret_cast<const uint4*>(kt + at);
         const uint4 k1 = *reinterpret_cast<const uint4*>(kt + at + (i < 2 * S::kA ? 1024 : 512));  // row g + 8
-        uint4 qc;
-        if constexpr (!kQueryHeld) qc = sm.query[group][i][lane];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t a0, a1, a2, a3, b0, b1;
-          codes_f16(word(k0, j), a0, a2);
-          codes_f16(word(k1, j), a1, a3);
-          if constexpr (kQueryHeld) {
-            const uint4 qi = q[2 * i + (j >> 1)];
-            b0 = j & 1 ? qi.z : qi.x;
-            b1 = j & 1 ? qi.w : qi.y;
-          } else {
-            codes_f16(word(qc, j), b0, b1);
-          }
-          mma_f16(j & 1 ? s1 : s0, a0, a1, a2, a3, b0, b1);
+        for (int j = 0; j < 2; ++j) {
+          uint4 qi;
+          if constexpr (kQueryHeld) qi = q[2 * i + j];
+          else qi = sm.query[group][2 * i + j][lane];
+          uint32_t a0, a1, a2, a3;
+          codes_f16(word(k0, 2 * j), a0, a2);
+          codes_f16(word(k1, 2 * j), a1, a3);
+          mma_f16(s0, a0, a1, a2, a3, qi.x, qi.y);
+          codes_f16(word(k0, 2 * j + 1), a0, a2);
+          codes_f16(word(k1, 2 * j + 1), a1, a3);
+          mma_f16(s1, a0, a1, a2, a3, qi.z, qi.w);
         }
       }
       const float* sk = &sm.scales[stage][0][kStep * slab + g];
