@@ -5,9 +5,9 @@
 //   x_j = (q . k_j) * (q_scale * softmax_scale * log2 e * k_scale_j),  m = max x,  l = sum 2^(x_j - m),
 //   out = (sum 2^(x_j - m) v_scale_j v_j) / l,  lse = (m + log2 l) * ln 2.
 // One pass with running m and l. The value sum has a running maximum of its own, M = max (x_j + log2
-// v_scale_j): its weights 2^(x_j + log2 v_scale_j - M) are at most 1 whatever the scales of the rows are,
-// so they fit fp16 for the tensor cores (rounded by 2^-11 of themselves, or 2^-25 of the largest), and
-// partial results (m, l, M, O) join exactly: out = O * 2^(M - m) / l.
+// v_scale_j), so its weights 2^(x_j + log2 v_scale_j - M) fit fp16 for the tensor cores whatever the scales of
+// the rows are (rounded by 2^-11 of themselves, or 2^-25 of the largest), and partial results (m, l, M, O) join
+// exactly: out = O * 2^(M - m) / l.
 //
 // What bounds it: every key and value byte is read once and used Hq/Hk <= 16 times, so HBM. The products are
 // legacy-shape warp matrix instructions on purpose: eight query heads of a key head fill the 8 columns of m16n8k16
@@ -99,9 +99,10 @@ struct Shared {
   int32_t before_begin, before_end;         // units before its first place and before the next CTA's
 };
 
-// What a CTA that begins inside a head leaves for the join of that head.
-struct Meta {
-  int32_t b, item, last, slot;  // b < 0: nothing to join here; slot: which partial of CTA (this - 1)
+// What a CTA that begins inside a head leaves for the join of that head: the CTAs that have its first and last part,
+// and which partial result of the first one's it is. b < 0: this CTA begins with a head.
+struct alignas(16) Meta {
+  int32_t b, item, first, last, slot;
 };
 
 struct SplitArgs {
@@ -650,14 +651,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     return;
   }
   if (threadIdx.x == 0 && a.meta != nullptr) {
-    // The head this CTA begins inside is joined by the second CTA that has a part of it. The head's first part is the
-    // first thing its CTA does if that begins at the head's first place, or one before it, behind the head before.
-    const int32_t i0 = share.owner(first);
+    // The head's first part is the first thing its CTA does if that begins at the head's first place, or one before
+    // it, behind the head before.
     Meta m;
-    m.b = t > 0 && i0 == cta - 1 ? use.b : -1;
+    m.b = t > 0 ? use.b : -1;
     m.item = use.item;
+    m.first = share.owner(first);
     m.last = share.owner(first + nt - 1);
-    m.slot = share.begin(i0) >= first - 1 ? 0 : 1;
+    m.slot = share.begin(m.first) >= first - 1 ? 0 : 1;
     a.meta[cta] = m;
   }
 
@@ -921,90 +922,127 @@ __global__ void __launch_bounds__(kThreads, 2)
   write_empty(p, kConsumers);
 }
 
-// Joins the partial results of one head: CTA (k, row) takes the head that CTA k of the first kernel began
-// inside. The warps share the parts, each in a fixed order.
+// Joins partial results. Every CTA of the first kernel but a head's first has a counterpart here, and these share the
+// head's rows: CTA k takes each (parts - 1)-th. A head of few parts takes a warp per row, one of many (it then has as
+// many CTAs here) the whole CTA, whose warps share the parts, each in a fixed order.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinAhead = 4;  // parts whose statistics and values are on their way at the same time
+
+// Running maxima, sum and values of parts `from`, `from + step`, ... of a row; lane l has columns 2l, 2l + 1, 2l + 64, ...
+template <int DP>
+struct JoinRow {
+  static constexpr int kV = DP / 64;
+  float top = kLowest, topo = kLowest, l = 0.f;
+  float2 v[kV];
+
+  template <typename Slot>
+  __device__ __forceinline__ void add(const SplitArgs& a, int rows, int row, int from, int step, int parts, Slot slot_of) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int j = 0; j < kV; ++j) v[j] = make_float2(0.f, 0.f);
+    for (int i0 = from; i0 < parts; i0 += step * kJoinAhead) {
+      float4 st[kJoinAhead];
+      float2 x[kJoinAhead][kV];
+#pragma unroll
+      for (int e = 0; e < kJoinAhead; ++e) {
+        const bool have = i0 + step * e < parts;
+        const int64_t at = slot_of(have ? i0 + step * e : i0) * rows + row;
+        st[e] = have ? *reinterpret_cast<const float4*>(a.stats + at * 4) : make_float4(kLowest, kLowest, 0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < kV; ++j) {
+          const int d = 2 * (lane + 32 * j);
+          x[e][j] = have && d < a.p.D ? *reinterpret_cast<const float2*>(a.part + at * DP + d) : make_float2(0.f, 0.f);
+        }
+      }
+      float mn = top, on = topo;
+#pragma unroll
+      for (int e = 0; e < kJoinAhead; ++e) {
+        mn = fmaxf(mn, st[e].x);
+        on = fmaxf(on, st[e].y);
+      }
+      l *= ex2(top - mn);
+      const float keep = ex2(topo - on);
+#pragma unroll
+      for (int j = 0; j < kV; ++j) v[j] = mul2(v[j], splat2(keep));
+#pragma unroll
+      for (int e = 0; e < kJoinAhead; ++e) {
+        l = fmaf(st[e].z, ex2(st[e].x - mn), l);
+        const float f = ex2(st[e].y - on);
+#pragma unroll
+        for (int j = 0; j < kV; ++j) v[j] = fma2(x[e][j], splat2(f), v[j]);
+      }
+      top = mn;
+      topo = on;
+    }
+  }
+};
+
+__device__ __forceinline__ float norm_of(float top, float topo, float l) { return l == 0.f ? 0.f : ex2(topo - top) / l; }
+
+__device__ __forceinline__ float lse_of(float top, float l) {
+  return l == 0.f ? -CUDART_INF_F : (top + log2f(l)) * 0.693147180559945309f;
+}
+
+__device__ __forceinline__ void store_pair(const SplitArgs& a, int64_t row, int pair, float2 y) {
+  static_cast<uint32_t*>(a.p.out)[row * (a.p.D / 2) + pair] =
+      a.dtype == DT_BF16 ? Elem<__nv_bfloat16>::pack(y) : Elem<__half>::pack(y);
+}
+
 template <int DP, int HG>
-__global__ void __launch_bounds__(kConsumers) attention_join_kernel(const __grid_constant__ SplitArgs a) {
-  constexpr int kRows = Item<DP, HG>::kRows;
-  constexpr int kV = DP / 64;  // float2 per lane
-  __shared__ float2 sum[kWarps][DP / 2];
-  __shared__ float4 stat[kWarps];
+__global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const __grid_constant__ SplitArgs a) {
+  constexpr int kRows = Item<DP, HG>::kRows, kV = DP / 64;
+  __shared__ float2 sum[kJoinWarps][DP / 2];
+  __shared__ float4 stat[kJoinWarps];
   pdl_trigger();
   pdl_wait();
   const int64_t k = blockIdx.x + 1;
   const Meta me = a.meta[k];
   const PagedArgs& p = a.p;
   if (me.b < 0) return;
-  const int32_t row = blockIdx.y;
-  const int32_t rows = min(kRows, a.G - kRows * (me.item % a.chunks));
-  if (row >= rows) return;
+  const int chunk = me.item % a.chunks, rows = min(kRows, a.G - kRows * chunk);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int parts = static_cast<int>(me.last - k + 2);
-  auto slot_of = [&](int i) { return i == 0 ? 2 * (k - 1) + me.slot : 2 * (k - 1 + i); };
-  // Each warp's own running maxima, so that statistics and values are on their way at the same time.
-  float top = kLowest, topo = kLowest, l = 0.f;
-  float2 v[kV];
+  const int parts = me.last - me.first + 1, others = parts - 1;
+  auto slot_of = [&](int i) { return i == 0 ? 2 * static_cast<int64_t>(me.first) + me.slot : 2 * static_cast<int64_t>(me.first + i); };
+  const int64_t orow0 = static_cast<int64_t>(me.b) * p.Hq + me.item / a.chunks * a.G + kRows * chunk;
+  const int first = static_cast<int>(k) - me.first - 1;  // this CTA's first row
+  JoinRow<DP> r;
+  if (parts <= kJoinWarps) {
+    for (int row = first + others * warp; row < rows; row += others * kJoinWarps) {
+      r = JoinRow<DP>();
+      r.add(a, kRows, row, 0, 1, parts, slot_of);
+      const float norm = norm_of(r.top, r.topo, r.l);
 #pragma unroll
-  for (int j = 0; j < kV; ++j) v[j] = make_float2(0.f, 0.f);
-  constexpr int kAhead = 4;
-  for (int i0 = warp; i0 < parts; i0 += kWarps * kAhead) {
-    float4 st[kAhead];
-    float2 x[kAhead][kV];
-#pragma unroll
-    for (int e = 0; e < kAhead; ++e) {
-      const bool have = i0 + kWarps * e < parts;
-      const int64_t at = slot_of(have ? i0 + kWarps * e : i0) * kRows + row;
-      st[e] = have ? *reinterpret_cast<const float4*>(a.stats + at * 4) : make_float4(kLowest, kLowest, 0.f, 0.f);
-#pragma unroll
-      for (int j = 0; j < kV; ++j) {
-        const int d = 2 * (lane + 32 * j);
-        x[e][j] = have && d < p.D ? *reinterpret_cast<const float2*>(a.part + at * DP + d) : make_float2(0.f, 0.f);
-      }
+      for (int j = 0; j < kV; ++j)
+        if (2 * (lane + 32 * j) < p.D) store_pair(a, orow0 + row, lane + 32 * j, mul2(r.v[j], splat2(norm)));
+      if (p.lse != nullptr && lane == 0) p.lse[orow0 + row] = lse_of(r.top, r.l);
     }
-    float mn = top, on = topo;
+    return;
+  }
+  for (int row = first; row < rows; row += others) {
+    r = JoinRow<DP>();
+    r.add(a, kRows, row, warp, kJoinWarps, parts, slot_of);
+    if (lane == 0) stat[warp] = make_float4(r.top, r.topo, r.l, 0.f);
 #pragma unroll
-    for (int e = 0; e < kAhead; ++e) {
-      mn = fmaxf(mn, st[e].x);
-      on = fmaxf(on, st[e].y);
+    for (int j = 0; j < kV; ++j) sum[warp][lane + 32 * j] = r.v[j];
+    __syncthreads();
+    float mj = kLowest, oj = kLowest, lj = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      mj = fmaxf(mj, stat[w].x);
+      oj = fmaxf(oj, stat[w].y);
     }
-    l *= ex2(top - mn);
-    const float keep = ex2(topo - on);
 #pragma unroll
-    for (int j = 0; j < kV; ++j) v[j] = mul2(v[j], splat2(keep));
+    for (int w = 0; w < kJoinWarps; ++w) lj = fmaf(stat[w].z, ex2(stat[w].x - mj), lj);
+    const float norm = norm_of(mj, oj, lj);
+    for (int d = threadIdx.x; 2 * d < p.D; d += kJoinWarps * 32) {
+      float2 y = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int e = 0; e < kAhead; ++e) {
-      l = fmaf(st[e].z, ex2(st[e].x - mn), l);
-      const float f = ex2(st[e].y - on);
-#pragma unroll
-      for (int j = 0; j < kV; ++j) v[j] = fma2(x[e][j], splat2(f), v[j]);
+      for (int w = 0; w < kJoinWarps; ++w) y = fma2(sum[w][d], splat2(ex2(stat[w].y - oj)), y);
+      store_pair(a, orow0 + row, d, mul2(y, splat2(norm)));
     }
-    top = mn;
-    topo = on;
+    if (p.lse != nullptr && threadIdx.x == 0) p.lse[orow0 + row] = lse_of(mj, lj);
+    __syncthreads();
   }
-  if (lane == 0) stat[warp] = make_float4(top, topo, l, 0.f);
-#pragma unroll
-  for (int j = 0; j < kV; ++j) sum[warp][lane + 32 * j] = v[j];
-  __syncthreads();
-  float mj = kLowest, oj = kLowest, lj = 0.f;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    mj = fmaxf(mj, stat[w].x);
-    oj = fmaxf(oj, stat[w].y);
-  }
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) lj = fmaf(stat[w].z, ex2(stat[w].x - mj), lj);
-  const float norm = lj == 0.f ? 0.f : ex2(oj - mj) / lj;
-  const int64_t orow = static_cast<int64_t>(me.b) * p.Hq + me.item / a.chunks * a.G + kRows * (me.item % a.chunks) + row;
-  for (int d = threadIdx.x; 2 * d < p.D; d += kConsumers) {
-    float2 y = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) y = fma2(sum[w][d], splat2(ex2(stat[w].y - oj)), y);
-    y = mul2(y, splat2(norm));
-    static_cast<uint32_t*>(p.out)[(orow * p.D) / 2 + d] =
-        a.dtype == DT_BF16 ? Elem<__nv_bfloat16>::pack(y) : Elem<__half>::pack(y);
-  }
-  if (p.lse != nullptr && threadIdx.x == 0)
-    p.lse[orow] = lj == 0.f ? -CUDART_INF_F : (mj + log2f(lj)) * 0.693147180559945309f;
 }
 
 // ---------------------------------------------------------------------------------- host side
@@ -1040,9 +1078,7 @@ bool launch_fed(const SplitArgs& a, const Maps& maps, const Plan& plan, cudaStre
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem)) return false;
   launch_overlapped(kern, dim3(static_cast<unsigned>(plan.grid)), kThreads, smem, 1, s, maps, a);
   if (plan.join)
-    launch_overlapped(attention_join_kernel<DP, HG>,
-                      dim3(static_cast<unsigned>(plan.grid - 1), a.G < Item<DP, HG>::kRows ? a.G : Item<DP, HG>::kRows), kConsumers, 0,
-                      1, s, a);
+    launch_overlapped(attention_join_kernel<DP, HG>, dim3(static_cast<unsigned>(plan.grid - 1)), kJoinWarps * 32, 0, 1, s, a);
   return true;
 }
 
