@@ -58,7 +58,15 @@ __device__ __forceinline__ void store_out(int dtype, void* out, int64_t i, float
 }
 
 // ================================================================================= narrow
-constexpr int kNarrowThreads = 192;  // four epilogue warps, producer, products
+// Epilogue warps in G groups of four, then the producer's and the products' warp. A block costs an epilogue warp a
+// chain of latencies (barrier, tensor memory, scales) with nothing else on its scheduler. Two groups take the blocks in
+// turn and add their sums at the end, 0.3 us. Measured at 64 columns: 64 x 8192 x 4096 (16 blocks a CTA) takes 11.3 us
+// with two and 11.6 with one, 64 x 8192 x 8320 (33) 17.9 and 21.3, but 333 x 1111 x 1968 (8) 7.7 and 7.4. Fewer columns
+// gain nothing (24 x 6144 x 8192: 15.1 and 15.2) and 128 leave no registers for it.
+constexpr int kTwoGroupBlocks = 12;  // blocks of k per CTA
+
+template <int G>
+constexpr int kNarrowThreads = 32 * (4 * G + 2);
 
 // One CTA per SM with as deep a ring as fits: a few CTAs then keep HBM busy (90 KB in flight on each of 48 SMs
 // moved 2 TB/s), and no cluster larger than a pair is needed to occupy the GPU (clusters of 4 to 8 CTAs started
@@ -77,7 +85,7 @@ template <int NT>
 struct NarrowShared {
   alignas(1024) unsigned char ring[Narrow<NT>::kStages][Narrow<NT>::kStageBytes];  // weights, then rows of a
   float part[NT / 4 * 3][128];                                                    // partial sums from the cluster's others
-  alignas(16) float scale[4][2][NT];                                              // per epilogue warp, two blocks
+  alignas(16) float scale[NT == 64 ? 8 : 4][2][NT];                               // per epilogue warp, two blocks
   alignas(8) uint64_t full[Narrow<NT>::kStages];
   uint64_t empty[Narrow<NT>::kStages];
   uint64_t done[Narrow<NT>::kBufs];   // a block's products are in tensor memory
@@ -85,12 +93,12 @@ struct NarrowShared {
   uint32_t tmem;
 };
 
-template <int NT, int SPLIT>
-__global__ void __launch_bounds__(kNarrowThreads, 1)
-    matmul_narrow_kernel(const __grid_constant__ CUtensorMap wmap,
-                                                                      const __grid_constant__ CUtensorMap amap,
-                                                                      const __grid_constant__ MmArgs p) {
+template <int NT, int SPLIT, int G>
+__global__ void __launch_bounds__(kNarrowThreads<G>, 1)
+    matmul_narrow_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
+                         const __grid_constant__ MmArgs p) {
   using C = Narrow<NT>;
+  constexpr int kProducer = 4 * G, kProducts = kProducer + 1;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   // The swizzle repeats every 1024 bytes: align the ring to 1024.
   NarrowShared<NT>& sm = *reinterpret_cast<NarrowShared<NT>*>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
@@ -114,14 +122,14 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   }
   pdl_trigger();
   pdl_wait();
-  if (warp == 5) tmem_alloc<1>(&sm.tmem, C::kCols);
+  if (warp == kProducts) tmem_alloc<1>(&sm.tmem, C::kCols);
   tc_fence_before();
   __syncthreads();
   if (SPLIT > 1) cluster_arrive();  // waited for before the first access to another CTA: it runs by then
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
 
-  if (warp == 4) {
+  if (warp == kProducer) {
     // ------------------------------------------------------------------------ producer
     if (lane == 0) {
       int s = 0;
@@ -144,7 +152,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
           if (!mbar_wait(kWaitLimitNs, &sm.full[j % C::kStages], static_cast<uint32_t>(j / C::kStages) & 1u)) break;
       }
     }
-  } else if (warp == 5) {
+  } else if (warp == kProducts) {
     // ------------------------------------------------------------------------ products
     if (lane == 0) {
       constexpr uint32_t idesc = e4m3_idesc(128, NT);
@@ -176,11 +184,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     }
   } else {
     // ------------------------------------------------------------------------ epilogue
-    // Thread (warp, lane) owns weight row n0 + 32*warp + lane; acc[j] is row t0 + j of a.
+    // Thread (quarter, lane) of a group owns weight row n0 + 32*quarter + lane; acc[j] is row t0 + j of a.
+    const int quarter = warp & 3, group = warp >> 2;
     float2 acc[NT / 2];
 #pragma unroll
     for (int j = 0; j < NT / 2; ++j) acc[j] = make_float2(0.f, 0.f);
-    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * warp) << 16);
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
     const float* sb = p.sb + static_cast<int64_t>(blockIdx.y) * p.sb_stride;
     constexpr int kL = (NT + 31) / 32;  // scales of a that a lane brings per block
     float next[kL];
@@ -192,16 +201,17 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
         next[i] = j < NT && t0 + j < p.M ? __ldg(p.sa + static_cast<int64_t>(t0 + j) * p.sa_stride + k) * b : 0.f;
       }
     };
-    if (kb0 < kb1) fetch(kb0);
-    int b = 0;
+    const int first = kb0 + group;
+    if (first < kb1) fetch(first);
+    int b = group, turn = 0;
     uint32_t phase = 0;
-    for (int k = kb0; k < kb1; ++k) {
-      float* sc = sm.scale[warp][k & 1];
+    for (int k = first; k < kb1; k += G, turn ^= 1) {
+      float* sc = sm.scale[warp][turn];
 #pragma unroll
       for (int i = 0; i < kL; ++i)
         if (lane + 32 * i < NT) sc[lane + 32 * i] = next[i];
       __syncwarp();  // the other buffer's readers have passed the last block's barrier
-      if (k + 1 < kb1) fetch(k + 1);
+      if (k + G < kb1) fetch(k + G);
       // one verdict for the whole warp: the loads below are collective
       if (!__all_sync(0xffffffffu, mbar_wait(kWaitLimitNs, &sm.done[b], phase))) {
         flag_failure(p.status);
@@ -228,44 +238,67 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
           hi = fma2(make_float2(__uint_as_float(d[j + 2]), __uint_as_float(d[j + 3])), make_float2(s4.z, s4.w), hi);
         }
       }
-      if (++b == C::kBufs) {
-        b = 0;
+      b += G;
+      if (b >= C::kBufs) {
+        b = group;
         phase ^= 1u;
       }
     }
-    // Each CTA of the cluster finishes NT / SPLIT of the columns: the others push their partial sums of these into
-    // its shared memory, and it adds them in rank order.
-    const int row = 32 * warp + lane;
-    auto value = [&](int j) { return j & 1 ? acc[j / 2].y : acc[j / 2].x; };
-    if constexpr (SPLIT == 1) {
+    if constexpr (G == 2) {
+      // Once both groups have seen their last block, nothing uses the ring: the second group's sums pass through it.
+      float (*sums)[128] = reinterpret_cast<float (*)[128]>(sm.ring);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (group == 1) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        if (t0 + j < p.M && n0 + row < p.N) store_out(p.dtype, p.out, static_cast<int64_t>(t0 + j) * p.out_stride + n0 + row, value(j));
-    } else {
-      constexpr int kOwn = NT / SPLIT;
-      cluster_wait();
-#pragma unroll
-      for (int r = 0; r < SPLIT; ++r)
-        if (r != rank) {
-          // the part of rank q lies at (q < r ? q : q - 1) of rank r's
-          const uint32_t to = in_cta(&sm.part[kOwn * (rank < r ? rank : rank - 1)][row], r);
-#pragma unroll
-          for (int j = 0; j < kOwn; ++j)
-            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + j * 512), "f"(value(kOwn * r + j)) : "memory");
+        for (int j = 0; j < NT / 2; ++j) {
+          sums[2 * j][32 * quarter + lane] = acc[j].x;
+          sums[2 * j + 1][32 * quarter + lane] = acc[j].y;
         }
-      cluster_barrier();
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (group == 0) {
 #pragma unroll
-      for (int r = 0; r < SPLIT; ++r)
-        if (r == rank) {
+        for (int j = 0; j < NT / 2; ++j) {
+          acc[j].x += sums[2 * j][32 * quarter + lane];
+          acc[j].y += sums[2 * j + 1][32 * quarter + lane];
+        }
+      }
+    }
+    if (group == 0) {
+      // Each CTA of the cluster finishes NT / SPLIT of the columns: the others push their partial sums of these into
+      // its shared memory, and it adds them in rank order.
+      const int row = 32 * quarter + lane;
+      auto value = [&](int j) { return j & 1 ? acc[j / 2].y : acc[j / 2].x; };
+      if constexpr (SPLIT == 1) {
 #pragma unroll
-          for (int j = 0; j < kOwn; ++j) {
-            float v = 0.f;
+        for (int j = 0; j < NT; ++j)
+          if (t0 + j < p.M && n0 + row < p.N) store_out(p.dtype, p.out, static_cast<int64_t>(t0 + j) * p.out_stride + n0 + row, value(j));
+      } else {
+        constexpr int kOwn = NT / SPLIT;
+        cluster_wait();
 #pragma unroll
-            for (int q = 0; q < SPLIT; ++q) v += q == r ? value(kOwn * r + j) : sm.part[kOwn * (q < r ? q : q - 1) + j][row];
-            const int col = t0 + kOwn * r + j;
-            if (col < p.M && n0 + row < p.N) store_out(p.dtype, p.out, static_cast<int64_t>(col) * p.out_stride + n0 + row, v);
+        for (int r = 0; r < SPLIT; ++r)
+          if (r != rank) {
+            // the part of rank q lies at (q < r ? q : q - 1) of rank r's
+            const uint32_t to = in_cta(&sm.part[kOwn * (rank < r ? rank : rank - 1)][row], r);
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j)
+              asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + j * 512), "f"(value(kOwn * r + j)) : "memory");
           }
-        }
+        cluster_barrier();
+#pragma unroll
+        for (int r = 0; r < SPLIT; ++r)
+          if (r == rank) {
+#pragma unroll
+            for (int j = 0; j < kOwn; ++j) {
+              float v = 0.f;
+#pragma unroll
+              for (int q = 0; q < SPLIT; ++q) v += q == r ? value(kOwn * r + j) : sm.part[kOwn * (q < r ? q : q - 1) + j][row];
+              const int col = t0 + kOwn * r + j;
+              if (col < p.M && n0 + row < p.N) store_out(p.dtype, p.out, static_cast<int64_t>(col) * p.out_stride + n0 + row, v);
+            }
+          }
+      }
     }
   }
   if (SPLIT > 1 && warp >= 4) {
@@ -275,7 +308,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) tmem_free<1>(tmem, C::kCols);
+  if (warp == kProducts) tmem_free<1>(tmem, C::kCols);
 }
 
 // CTAs that share a tile's k: as many as occupy SMs that would be idle.
@@ -298,12 +331,19 @@ bool launch_narrow(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
   p.tiles_m = static_cast<int32_t>((a.M + NT - 1) / NT);
   if (p.tiles_n > 65535 || p.tiles_m > 65535) return false;
   const int split = narrow_split(static_cast<int64_t>(p.tiles_n) * p.tiles_m, p.nkb);
-  auto kern = split == 1 ? matmul_narrow_kernel<NT, 1> : split == 2 ? matmul_narrow_kernel<NT, 2> : matmul_narrow_kernel<NT, 4>;
+  auto kern = split == 1 ? matmul_narrow_kernel<NT, 1, 1> : split == 2 ? matmul_narrow_kernel<NT, 2, 1> : matmul_narrow_kernel<NT, 4, 1>;
+  int threads = kNarrowThreads<1>;
+  if constexpr (NT == 64) {
+    if (p.nkb / split >= kTwoGroupBlocks) {
+      kern = split == 1 ? matmul_narrow_kernel<NT, 1, 2> : split == 2 ? matmul_narrow_kernel<NT, 2, 2> : matmul_narrow_kernel<NT, 4, 2>;
+      threads = kNarrowThreads<2>;
+    }
+  }
   constexpr size_t smem = sizeof(NarrowShared<NT>) + 1024;
   static_assert(smem <= 227 * 1024, "the ring fits the SM");
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem)) return false;
   launch_overlapped(kern, dim3(static_cast<unsigned>(split), static_cast<unsigned>(p.tiles_n), static_cast<unsigned>(p.tiles_m)),
-                    kNarrowThreads, smem, static_cast<unsigned>(split), s, wmap, amap, p);
+                    threads, smem, static_cast<unsigned>(split), s, wmap, amap, p);
   return true;
 }
 

@@ -60,6 +60,18 @@ def test_matmul(size, dt):
     ref.assert_matmul(got, a, sa, b, sb)
 
 
+@pytest.mark.parametrize("size", [(60, 16000, 1712), (33, 8100, 3216), (64, 4100, 6928)], ids=str)
+def test_matmul_weights_of_many_tiles(size):
+    """33 to 64 rows of 13 to 14 blocks of k per CTA, whose sums are kept in two halves; k whole, in two, in four."""
+    M, N, K = size
+    a, sa, b, sb = matmul_inputs(M, N, K, seed=N)
+    out = Guarded((M, N), torch.bfloat16, fill=math.nan)
+    got = fq.fp8_matmul(a, sa, b, sb, out=out.t)
+    out.check()
+    ref.assert_matmul(got, a, sa, b, sb)
+    assert torch.equal(fq.fp8_matmul(a, sa, b, sb), got)
+
+
 @pytest.mark.parametrize("size", [(7, 200, 256), (70, 200, 1024), (300, 400, 512)], ids=str)
 def test_matmul_strided(size):
     """Padded rows of every operand and of the output; the padding stays as it was."""
