@@ -924,7 +924,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // Joins partial results. Every CTA of the first kernel but a head's first has a counterpart here, and these share the
 // head's rows: CTA k takes each (parts - 1)-th. A head of few parts takes a warp per row, one of many (it then has as
-// many CTAs here) the whole CTA, whose warps share the parts, each in a fixed order.
+// many CTAs here) the whole CTA, whose warps share the parts, each in a fixed order. What bounds it is its start and
+// three dependent loads (which head, statistics, values): 4 us behind the 47 us of one sequence of 131072 tokens,
+// 2.5 to 4.7 us elsewhere; with a CTA for each row of each head, most of them idle, it took 5 to 9.5 us.
 constexpr int kJoinWarps = 8;
 constexpr int kJoinAhead = 4;  // parts whose statistics and values are on their way at the same time
 
