@@ -384,6 +384,18 @@ def test_attention(case):
     check_attention(attention_inputs(lens, Hq, Hk, D, page, seed=60, order=order), dt)
 
 
+@pytest.mark.parametrize("Hq,Hk,D,B,step,most", [(32, 2, 128, 48, 97, 1000), (16, 2, 256, 30, 131, 1500), (10, 2, 96, 60, 61, 2000),
+                                                 (32, 2, 256, 30, 89, 700), (32, 2, 64, 64, 53, 1100)])
+def test_attention_heads_over_few_blocks(Hq, Hk, D, B, step, most):
+    """A few units of the work list per block: heads begin, end and are joined at every place in one."""
+    lens = [step * i % most for i in range(B)]
+    x = attention_inputs(lens, Hq, Hk, D, 32, seed=78)
+    check_attention(x)
+    first = fq.paged_attention(*x, want_lse=True)
+    again = fq.paged_attention(*x, want_lse=True)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
 def test_attention_many_sequences():
     lens = [(37 * i) % 300 for i in range(700)]
     check_attention(attention_inputs(lens, 4, 2, 64, 16, seed=61))
