@@ -925,28 +925,28 @@ __global__ void __launch_bounds__(kThreads, 2)
 // Joins partial results. Every CTA of the first kernel but a head's first has a counterpart here, and these share the
 // head's rows: CTA k takes each (parts - 1)-th. A head of few parts takes a warp per row, one of many (it then has as
 // many CTAs here) the whole CTA, whose warps share the parts, each in a fixed order. What bounds it is its start and
-// three dependent loads (which head, statistics, values): 4 us behind the 47 us of one sequence of 131072 tokens,
+// two dependent loads (which head; statistics and values): 3 us behind the 47 us of one sequence of 131072 tokens,
 // 2.5 to 4.7 us elsewhere; with a CTA for each row of each head, most of them idle, it took 5 to 9.5 us.
 constexpr int kJoinWarps = 8;
-constexpr int kJoinAhead = 4;  // parts whose statistics and values are on their way at the same time
 
 // Running maxima, sum and values of parts `from`, `from + step`, ... of a row; lane l has columns 2l, 2l + 1, 2l + 64, ...
+// Statistics and values of kAhead parts are on their way at the same time.
 template <int DP>
 struct JoinRow {
   static constexpr int kV = DP / 64;
   float top = kLowest, topo = kLowest, l = 0.f;
   float2 v[kV];
 
-  template <typename Slot>
+  template <int kAhead, typename Slot>
   __device__ __forceinline__ void add(const SplitArgs& a, int rows, int row, int from, int step, int parts, Slot slot_of) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int j = 0; j < kV; ++j) v[j] = make_float2(0.f, 0.f);
-    for (int i0 = from; i0 < parts; i0 += step * kJoinAhead) {
-      float4 st[kJoinAhead];
-      float2 x[kJoinAhead][kV];
+    for (int i0 = from; i0 < parts; i0 += step * kAhead) {
+      float4 st[kAhead];
+      float2 x[kAhead][kV];
 #pragma unroll
-      for (int e = 0; e < kJoinAhead; ++e) {
+      for (int e = 0; e < kAhead; ++e) {
         const bool have = i0 + step * e < parts;
         const int64_t at = slot_of(have ? i0 + step * e : i0) * rows + row;
         st[e] = have ? *reinterpret_cast<const float4*>(a.stats + at * 4) : make_float4(kLowest, kLowest, 0.f, 0.f);
@@ -958,7 +958,7 @@ struct JoinRow {
       }
       float mn = top, on = topo;
 #pragma unroll
-      for (int e = 0; e < kJoinAhead; ++e) {
+      for (int e = 0; e < kAhead; ++e) {
         mn = fmaxf(mn, st[e].x);
         on = fmaxf(on, st[e].y);
       }
@@ -967,7 +967,7 @@ struct JoinRow {
 #pragma unroll
       for (int j = 0; j < kV; ++j) v[j] = mul2(v[j], splat2(keep));
 #pragma unroll
-      for (int e = 0; e < kJoinAhead; ++e) {
+      for (int e = 0; e < kAhead; ++e) {
         l = fmaf(st[e].z, ex2(st[e].x - mn), l);
         const float f = ex2(st[e].y - on);
 #pragma unroll
@@ -993,6 +993,9 @@ __device__ __forceinline__ void store_pair(const SplitArgs& a, int64_t row, int 
 template <int DP, int HG>
 __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const __grid_constant__ SplitArgs a) {
   constexpr int kRows = Item<DP, HG>::kRows, kV = DP / 64;
+  // Parts of a warp at a time where a head has many: 4 took 51.0 us for one sequence of 131072 tokens, 8 50.1 (heads of
+  // 256 slow down by the registers).
+  constexpr int kMany = DP <= 128 ? 8 : 4;
   __shared__ float2 sum[kJoinWarps][DP / 2];
   __shared__ float4 stat[kJoinWarps];
   pdl_trigger();
@@ -1011,7 +1014,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
   if (parts <= kJoinWarps) {
     for (int row = first + others * warp; row < rows; row += others * kJoinWarps) {
       r = JoinRow<DP>();
-      r.add(a, kRows, row, 0, 1, parts, slot_of);
+      r.template add<4>(a, kRows, row, 0, 1, parts, slot_of);
       const float norm = norm_of(r.top, r.topo, r.l);
 #pragma unroll
       for (int j = 0; j < kV; ++j)
@@ -1022,7 +1025,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
   }
   for (int row = first; row < rows; row += others) {
     r = JoinRow<DP>();
-    r.add(a, kRows, row, warp, kJoinWarps, parts, slot_of);
+    r.template add<kMany>(a, kRows, row, warp, kJoinWarps, parts, slot_of);
     if (lane == 0) stat[warp] = make_float4(r.top, r.topo, r.l, 0.f);
 #pragma unroll
     for (int j = 0; j < kV; ++j) sum[warp][lane + 32 * j] = r.v[j];
