@@ -455,7 +455,7 @@ __device__ __forceinline__ void wide_store(const MmArgs& p, const CUtensorMap* o
       fence_async_shared();
       __syncwarp();
       if (lane == 0) {
-        if (row0 < p.M && col < p.N) tma_store_2d(omap, 2 * col, row0, stage);
+        if (row0 < p.M && col < p.N) tma_store_2d(omap, col, row0, stage);
         bulk_commit();
       }
     } else {
@@ -617,11 +617,12 @@ bool launch_wide(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
   if (!byte_tensor_map(&amap, 2, a.a, ad, as, ab, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !byte_tensor_map(&wmap, 2, a.b, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B))
     return false;
-  // Output boxes as bytes: 64 columns = 128 bytes; rows that are not whole 16-byte pieces are stored directly.
-  const uint64_t od[2] = {static_cast<uint64_t>(a.N) * 2, static_cast<uint64_t>(a.M)}, os[1] = {static_cast<uint64_t>(a.out_stride) * 2};
-  const uint32_t ob[2] = {128, 32};
+  // Output boxes of 64 columns, 128 bytes; rows that are not whole 16-byte pieces are stored directly. The map counts
+  // 16-bit elements: coordinates are 32-bit, and as bytes those of columns from 2^30 on would not fit.
+  const uint64_t od[2] = {static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.M)}, os[1] = {static_cast<uint64_t>(a.out_stride) * 2};
+  const uint32_t ob[2] = {64, 32};
   p.tma_store = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && os[0] % 16 == 0 &&
-                byte_tensor_map(&omap, 2, a.out, od, os, ob, CU_TENSOR_MAP_SWIZZLE_128B);
+                half_tensor_map(&omap, 2, a.out, od, os, ob, CU_TENSOR_MAP_SWIZZLE_128B);
   p.tiles_m = static_cast<int32_t>((a.M + kTileM - 1) / kTileM);
   p.tiles_n = static_cast<int32_t>((a.N + kTileN - 1) / kTileN);
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;

@@ -1,4 +1,4 @@
-// fq_tensormap.cu -- tensor maps of byte matrices for the TMA-fed serving kernels.
+// fq_tensormap.cu -- tensor maps for the TMA-fed serving kernels.
 #include "fq_tensormap.h"
 
 #include <cuda_runtime.h>
@@ -8,8 +8,10 @@
 
 namespace fq {
 
-bool byte_tensor_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
-                     const uint32_t* box, CUtensorMapSwizzle swizzle) {
+namespace {
+
+bool tensor_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base, const uint64_t* dims,
+                const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -28,9 +30,21 @@ bool byte_tensor_map(CUtensorMap* map, int rank, const void* base, const uint64_
     one[i] = 1;
     if (i + 1 < rank) s[i] = strides[i];
   }
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, s, b, one,
+  return encode(map, type, static_cast<cuuint32_t>(rank), const_cast<void*>(base), d, s, b, one,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+bool byte_tensor_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box, CUtensorMapSwizzle swizzle) {
+  return tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, base, dims, strides, box, swizzle);
+}
+
+bool half_tensor_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                     const uint32_t* box, CUtensorMapSwizzle swizzle) {
+  return tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, base, dims, strides, box, swizzle);
 }
 
 }  // namespace fq

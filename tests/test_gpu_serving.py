@@ -135,6 +135,20 @@ def test_matmul_operand_beyond_32_bits():
     assert not bool(out[:-20].any())
 
 
+def test_matmul_columns_beyond_2_to_the_30():
+    """One row, more columns than 2^30: those on either side of it, and nothing else, have weights."""
+    M, N, K = 1, (1 << 30) + 256, 16
+    tail = 512
+    a, sa, bt, sbt = matmul_inputs(M, tail, K, seed=12)
+    b = torch.zeros(N, K, dtype=torch.uint8, device="cuda")
+    sb = torch.ones(N // 128, 1, device="cuda")
+    b[-tail:], sb[-tail // 128:] = bt, sbt
+    out = torch.full((M, N), math.nan, dtype=torch.bfloat16, device="cuda")
+    fq.fp8_matmul(a, sa, b, sb, out=out)
+    ref.assert_matmul(out[:, -tail:], a, sa, bt, sbt)
+    assert not bool(out[:, :-tail].any())
+
+
 def test_matmul_empty():
     a, sa, b, sb = matmul_inputs(4, 6, 128, seed=1)
     assert fq.fp8_matmul(a[:0], sa[:0], b, sb).shape == (0, 6)
