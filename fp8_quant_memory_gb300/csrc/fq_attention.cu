@@ -313,7 +313,8 @@ __device__ __forceinline__ void produce_rows(const SplitArgs& a, Shared<DP, HG>&
   int stage = 0;
   uint32_t phase = 1;  // the first round finds every stage empty
   for (int32_t u = 0; u < units; ++u) {
-    if (u >= kStages && !mbar_wait(kWaitLimitNs, &sm.empty[stage], phase)) {
+    // one verdict for the whole warp: the votes and shuffles below are collective
+    if (u >= kStages && !__all_sync(0xffffffffu, mbar_wait(kWaitLimitNs, &sm.empty[stage], phase))) {
       flag_failure(a.status);
       break;
     }
@@ -679,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   int32_t rows = 0, head0 = 0;  // query heads of the item, and the first of them
   int stage = 0;
   uint32_t phase = 0;
-  bool arrived = true;  // false once a wait gave up: the rest runs through without waiting
+  bool arrived = true;  // false once a wait gave up: the rest runs through without waiting, its tokens left out
 
   for (int32_t u = 0; u < units; ++u) {
     if (fresh) {
@@ -718,11 +719,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int i = 0; i < kN; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     }
-    if (arrived && !mbar_wait(kWaitLimitNs, &sm.full[stage], phase)) {
+    // one verdict for the whole warp: the products and shuffles below are collective
+    if (arrived && !__all_sync(0xffffffffu, mbar_wait(kWaitLimitNs, &sm.full[stage], phase))) {
       flag_failure(a.status);
       arrived = false;
     }
-    const uint32_t live = sm.live[stage][slab];
+    const uint32_t live = arrived ? sm.live[stage][slab] : 0u;  // a stage that has not landed may change while it is read
     if (live != 0u) {
       const unsigned char* kt = sm.codes[stage][0];
       // Scores of tokens g (0, 1) and g + 8 (2, 3) with heads 2c and 2c + 1; two chains of sums.
