@@ -4,10 +4,12 @@
 // Mathematics. For a query head with codes q, key rows k_j and value rows v_j (codes), in base 2:
 //   x_j = (q . k_j) * (q_scale * softmax_scale * log2 e * k_scale_j),  m = max x,  l = sum 2^(x_j - m),
 //   out = (sum 2^(x_j - m) v_scale_j v_j) / l,  lse = (m + log2 l) * ln 2.
-// One pass with running m and l. The value sum has a running maximum of its own, M = max (x_j + log2
-// v_scale_j), so its weights 2^(x_j + log2 v_scale_j - M) fit fp16 for the tensor cores whatever the scales of
-// the rows are (rounded by 2^-11 of themselves, or 2^-25 of the largest), and partial results (m, l, M, O) join
-// exactly: out = O * 2^(M - m) / l.
+// One pass with running m and l. The value sum has a running reference of its own, M = max (x_j + log2
+// v_scale_j) - 7, so its weights 2^(x_j + log2 v_scale_j - M) fit fp16 for the tensor cores whatever the scales of
+// the rows are, and partial results (m, l, M, O) join exactly: out = O * 2^(M - m) / l. The 7 uses fp16's range to
+// the end: the largest weight is 2^7 when M is set and may grow to 2^15 before M follows (below), and weights are
+// rounded by 2^-11 of themselves, or 2^-32 of the largest. (fp16 because it halves the value product's operands and
+// carries 8 times the precision of the 8-bit codes it multiplies; sums stay in fp32.)
 //
 // What bounds it: every key and value byte is read once and used Hq/Hk <= 16 times, so HBM. The products are
 // legacy-shape warp matrix instructions on purpose: eight query heads of a key head fill the 8 columns of m16n8k16
@@ -26,7 +28,7 @@
 // accumulators to B fragments by two movmatrix.
 //
 // The running maxima are only brought up to date when a score exceeds one by more than 2^8 (a vote; then three
-// shuffles per head and the rescaling): weights of up to 2^8 lose nothing in fp16 and fp32.
+// shuffles per head and the rescaling): weights of up to 2^8, and 2^15 for the values, lose nothing in fp32 and fp16.
 //
 // Split. The work is a list of units in the order sequence, head, tokens, and behind each head one place more, which
 // stands for the time its end takes (the warps' results are joined and written: about as long as a unit, 1.2 us; a
@@ -66,6 +68,7 @@ struct Item {
   static constexpr int kStages = (DP == 64 ? 80 : DP > 128 && HG == 2 ? 88 : 98) * 1024 / (2 * kUnit * DP);
 };
 constexpr float kSlack = 8.f;                // powers of two by which a score may exceed its running maximum
+constexpr float kRoom = 7.f;                 // powers of two of the largest value weight when M is set; 2^(7 + 8) fits fp16
 constexpr float kLowest = -3.402823466e38f;  // below every score: a maximum before the first token
 
 // A unit's rows are stored as kA tiles of [rows][128 bytes], then kB of [rows][64], keys before values.
@@ -768,13 +771,13 @@ __global__ void __launch_bounds__(kThreads, 2)
       bool above = false;
 #pragma unroll
       for (int e = 0; e < 2; ++e)
-        above = above || fmaxf(x[0][e], x[1][e]) > m[e] + kSlack || fmaxf(w[0][e], w[1][e]) > mo[e] + kSlack;
+        above = above || fmaxf(x[0][e], x[1][e]) > m[e] + kSlack || fmaxf(w[0][e], w[1][e]) > mo[e] + (kRoom + kSlack);
       if (__any_sync(0xffffffffu, above)) {
         float keep[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float mn = fmaxf(m[e], column_max(fmaxf(x[0][e], x[1][e])));
-          const float on = fmaxf(mo[e], column_max(fmaxf(w[0][e], w[1][e])));
+          const float on = fmaxf(mo[e], column_max(fmaxf(w[0][e], w[1][e])) - kRoom);
           l[e] *= ex2(m[e] - mn);
           keep[e] = ex2(mo[e] - on);
           m[e] = mn;

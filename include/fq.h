@@ -327,7 +327,8 @@ size_t fq_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hk, int
  *   out[b,h,d] = dtype( sum_j p_j * v_scale_j * v_j[d] ),   lse[b,h] = log sum_j exp(s_j)
  * where row j of sequence b is slot j % page_size of page page_table[b*table_stride + j / page_size] and
  * query head h reads key head h / (Hq/Hk). fp32 throughout (the probabilities times V scales are rounded
- * once to fp16, relative to a running maximum of theirs, for the tensor cores); one rounding to dtype.
+ * once to fp16 for the tensor cores: by at most 2^-11 of themselves or 2^-32 of the largest so far, whichever is
+ * more); one rounding to dtype.
  * Scales are non-negative, as the quantisers above write them (a negative V scale gives NaN).
  * q: [B, Hq, D] codes, rows of a sequence q_stride elements apart (so the q heads of a prologue's
  * [T, H, D] output can be passed in place), q_scale and page_table likewise (strides of what is only

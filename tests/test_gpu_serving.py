@@ -439,6 +439,34 @@ def test_attention_maxima_that_grow():
         check_attention(x, scale=1.0)
 
 
+@pytest.mark.parametrize("Hq,Hk,D,page", [(8, 2, 128, 16), (32, 2, 128, 16), (4, 4, 64, 24), (32, 2, 256, 32), (6, 2, 192, 7)])
+def test_attention_small_weights_beside_large_ones(Hq, Hk, D, page):
+    """Every 16th token has 2^26 times the weight of the others, but zeros in the upper half of its values: there the
+    output is what the small weights give.
+
+    All scores are exact products (codes of 1), so a weight is off by the exponential alone (2^-20 of it, of a
+    difference of scores of 26 held in 2^-19), and by its rounding to fp16, at most 2^-11 of it or 2^-32 of the largest:
+    2^-6 of a weight 2^-26 of the largest. The sum of weights: 2^-12 of it. Output: half a step of bf16.
+    """
+    n = 1024
+    x = attention_inputs([n, 37], Hq, Hk, D, page, seed=79)
+    q, qs, k, v, ks, vs, table, lens = x
+    for t, c in ((q, 0x38), (k, 0x38), (v, 0x38)):
+        t.fill_(c)
+    qs.fill_(1.0)
+    ks.fill_(2.0 ** -40)
+    vs.fill_(1.0)
+    pos = torch.arange(0, n, 16)
+    for b, m in enumerate(lens.tolist()):
+        at, off = table.cpu()[b, pos[pos < m] // page].long().cuda(), (pos[pos < m] % page).cuda()
+        ks[at, :, off] = 26 * math.log(2.0) / D
+        v[at, :, off, D // 2:] = 0
+    out = fq.paged_attention(*x, softmax_scale=1.0)[0].cpu().double()
+    want = ref.attention(*x, 1.0)[0]
+    tol = (2.0 ** -6 + 2.0 ** -8 + 2.0 ** -11 + 2.0 ** -12) * want
+    assert bool(((out - want).abs() <= tol).all()), float(((out - want).abs() / want).max())
+
+
 def test_attention_all_empty():
     check_attention(attention_inputs([0, 0, -5], 8, 2, 128, 16, seed=62))
 
