@@ -190,7 +190,8 @@ int fq_qkv_norm_rope_append(const void* qkv, int64_t token_stride, const void* w
 
 size_t fq_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t max_seq_len) {
   if (B <= 0 || Hk <= 0 || Hq <= 0 || D <= 0 || D > 256 || max_seq_len <= 0 || Hq % Hk != 0) return 0;
-  return fq::attention_workspace_bytes(B, Hq, Hk, D, max_seq_len);
+  // a larger bound is no bound: no call takes longer sequences
+  return fq::attention_workspace_bytes(B, Hq, Hk, D, max_seq_len < kMaxDim ? max_seq_len : kMaxDim);
 }
 
 int fq_paged_attention(const uint8_t* q, int64_t q_stride, const float* q_scale, int64_t q_scale_stride,

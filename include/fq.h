@@ -317,7 +317,8 @@ int fq_qkv_norm_rope_append(const void* qkv, int64_t token_stride, const void* w
                             cudaStream_t stream);
 
 /* Bytes of caller-provided device workspace fq_paged_attention needs on the current device: the fp32
- * partial results of sequences that several CTAs share. 0 when no sequence can be shared. */
+ * partial results of sequences that several CTAs share. 0 when no sequence can be shared. A bound that holds for a
+ * larger max_seq_len holds for a smaller one; INT64_MAX gives what any length needs. */
 size_t fq_paged_attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t max_seq_len);
 
 /*

@@ -598,6 +598,17 @@ def test_attention_refusals():
             fq.paged_attention(*long, workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"), max_seq_len=3000)
 
 
+@pytest.mark.parametrize("bound", [2 ** 31, 2 ** 62, 2 ** 63 - 1])
+def test_attention_workspace_without_a_bound(bound):
+    """A max_seq_len that is no bound at all: the workspace of the longest sequence, and the call takes both."""
+    x = attention_inputs([3000, 20], 8, 2, 128, 16, seed=81)
+    need = fq.paged_attention_workspace_bytes(2, 8, 2, 128, bound)
+    assert need == fq.paged_attention_workspace_bytes(2, 8, 2, 128, 2 ** 31 - 1025) > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    out, _ = fq.paged_attention(*x, max_seq_len=bound, workspace=ws)
+    assert torch.equal(out, fq.paged_attention(*x)[0])
+
+
 # -------------------------------------------------------------------------------- used together
 def decode_step(s):
     """Norm + group-wise FP8 of the hidden rows, the QKV projection, the prologue into the cache, attention."""
