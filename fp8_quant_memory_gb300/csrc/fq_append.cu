@@ -11,6 +11,8 @@
 // append_kernel: a group of LPR lanes owns a (token, head) row, as in fq_rows.cu; consecutive groups take consecutive rows,
 // so loads cover whole contiguous runs of the QKV row. Rows of q and k and rows of v meet in a warp only where the
 // head counts are not multiples of its rows; such a warp runs both bodies, each with its own rows live.
+#include <math_constants.h>
+
 #include "fq_device.cuh"
 #include "fq_rows.cuh"
 #include "fq_serving.h"
@@ -40,6 +42,10 @@ __device__ __forceinline__ void locate(const CacheView& c, int64_t slot, int64_t
     *off = slot - *page * c.page_size;
   }
 }
+
+// The divisor in div2_by's correction. A row that holds an infinity has an infinite scale, whose reciprocal is 0: its
+// finite values' quotients are their products with that, 0, and a correction by infinity times 0 would make them NaN.
+__device__ __forceinline__ float corrected_by(float scale) { return scale == CUDART_INF_F ? 0.f : scale; }
 
 template <typename T, typename TT, int LPR, int HS, int TS>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs p) {
@@ -82,7 +88,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       RowArgs row = a;  // row 0 of these outputs is this row's place
       row.q = codes;
       row.scale = scale;
-      row_body<T, TT, MODE_QK, LPR, HS, TS, false>(row, 0, live && !is_v, h, xv, lane, hv, th, static_cast<float>(N), a.cos,
+      row_body<T, TT, MODE_QK, LPR, HS, TS, false, false, true>(row, 0, live && !is_v, h, xv, lane, hv, th, static_cast<float>(N), a.cos,
                                                    a.sin, static_cast<int64_t>(t) * half);
     }
     if (__any_sync(0xffffffffu, inside && is_v)) {
@@ -92,7 +98,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 #pragma unroll
         for (int k = 0; k < 4; k += 2) amax = absmax4(amax, Elem<T>::unpack(word(xv[s], k)), Elem<T>::unpack(word(xv[s], k + 1)));
       amax = fmaxf(group_max<LPR>(amax), 1e-4f);
-      const float sc = __fdiv_rn(amax, a.fp8_max), rc = __frcp_rn(sc);
+      const float sc = __fdiv_rn(amax, a.fp8_max), rc = __frcp_rn(sc), by = corrected_by(sc);
       const bool clamp = a.fp8_max != 448.0f;
       if (live && is_v) {
 #pragma unroll
@@ -101,8 +107,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
           float2 v[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            v[k] = div2_by(Elem<T>::unpack(word(xv[s], k)), sc, rc);
-            if (clamp) v[k] = make_float2(clamp_abs(v[k].x, a.fp8_max), clamp_abs(v[k].y, a.fp8_max));
+            v[k] = div2_by(Elem<T>::unpack(word(xv[s], k)), by, rc);
+            if (clamp) v[k] = make_float2(clamp_or_nan(v[k].x, a.fp8_max), clamp_or_nan(v[k].y, a.fp8_max));
           }
           st_stream8(codes + 8 * (lane + s * LPR), pack_e4m3x8(v[0], v[1], v[2], v[3]));
         }
@@ -250,8 +256,8 @@ __device__ __forceinline__ void stream_qk(const StreamArgs& a, uint32_t xrow, ui
       l[e] = mul2(zl[m][e], m2);
       h[e] = mul2(zh[m][e], m2);
       if constexpr (kClamp) {
-        l[e] = make_float2(clamp_abs(l[e].x, r.fp8_max), clamp_abs(l[e].y, r.fp8_max));
-        h[e] = make_float2(clamp_abs(h[e].x, r.fp8_max), clamp_abs(h[e].y, r.fp8_max));
+        l[e] = make_float2(clamp_or_nan(l[e].x, r.fp8_max), clamp_or_nan(l[e].y, r.fp8_max));
+        h[e] = make_float2(clamp_or_nan(h[e].x, r.fp8_max), clamp_or_nan(h[e].y, r.fp8_max));
       }
     }
     lo[m] = pack_e4m3x8(l[0], l[1], l[2], l[3]);
@@ -279,18 +285,18 @@ __device__ __forceinline__ void stream_v(const StreamArgs& a, uint32_t xrow, int
   }
 #pragma unroll
   for (int o = 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
-  const float sc = __fdiv_rn(fmaxf(am, 1e-4f), fp8_max), rc = __frcp_rn(sc);
+  const float sc = __fdiv_rn(fmaxf(am, 1e-4f), fp8_max), rc = __frcp_rn(sc), by = corrected_by(sc);
   uint2 lo[2], hi[2];
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
     float2 l[4], h[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      l[e] = div2_by(Elem<T>::unpack(word(xl[m], e)), sc, rc);
-      h[e] = div2_by(Elem<T>::unpack(word(xh[m], e)), sc, rc);
+      l[e] = div2_by(Elem<T>::unpack(word(xl[m], e)), by, rc);
+      h[e] = div2_by(Elem<T>::unpack(word(xh[m], e)), by, rc);
       if constexpr (kClamp) {
-        l[e] = make_float2(clamp_abs(l[e].x, fp8_max), clamp_abs(l[e].y, fp8_max));
-        h[e] = make_float2(clamp_abs(h[e].x, fp8_max), clamp_abs(h[e].y, fp8_max));
+        l[e] = make_float2(clamp_or_nan(l[e].x, fp8_max), clamp_or_nan(l[e].y, fp8_max));
+        h[e] = make_float2(clamp_or_nan(h[e].x, fp8_max), clamp_or_nan(h[e].y, fp8_max));
       }
     }
     lo[m] = pack_e4m3x8(l[0], l[1], l[2], l[3]);

@@ -262,6 +262,14 @@ __device__ __forceinline__ uint2 pack_e4m3x8(float2 a, float2 b, float2 c, float
 
 __device__ __forceinline__ float clamp_abs(float v, float m) { return fminf(fmaxf(v, -m), m); }
 
+// The same, but a NaN stays one (fminf and fmaxf take the bound instead).
+__device__ __forceinline__ float clamp_or_nan(float v, float m) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(-m));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(r), "f"(m));
+  return r;
+}
+
 // ------------------------------------------------------------------------------------------------
 // Reductions over a group of G consecutive lanes (G a power of two <= 32). Every lane of the warp
 // must call these (full-mask shuffles); each lane receives its own group's result.

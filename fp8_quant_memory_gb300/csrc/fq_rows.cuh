@@ -88,8 +88,9 @@ __device__ __forceinline__ bool slot_ok(int s, int lane, int hv, int th) {
 // Table entries of this row: cos_base/sin_base + trow + pair index (global memory, or a staged block
 // in shared memory when SMEM_TAB). WPRE: the caller holds this lane's weight vectors in `wpre` (one
 // per slot, loaded once for every row it processes; single-weight modes only), else they are read
-// from global memory per row.
-template <typename T, typename TT, int MODE, int LPR, int HS, int TS, bool SMEM_TAB, bool WPRE = false>
+// from global memory per row. KEEP_NAN: where fp8_max < 448, a NaN passes the clamp (else it becomes -fp8_max).
+template <typename T, typename TT, int MODE, int LPR, int HS, int TS, bool SMEM_TAB, bool WPRE = false,
+          bool KEEP_NAN = false>
 __device__ __forceinline__ void row_body(const RowArgs& a, int32_t r, bool rv, int32_t h,
                                          const uint4 (&xv)[HS + 2 * TS], int lane, int hv, int th, float fN,
                                          const void* cos_base, const void* sin_base, int64_t trow,
@@ -280,7 +281,9 @@ __device__ __forceinline__ void row_body(const RowArgs& a, int32_t r, bool rv, i
         for (int k = 0; k < 4; ++k) {
           const float2 yy = (MODE == MODE_QK) ? yf[s][k] : Elem<T>::unpack(word(yp[s], k));
           v[k] = div2_by(yy, sc, rc);
-          if (clamp) v[k] = make_float2(clamp_abs(v[k].x, a.fp8_max), clamp_abs(v[k].y, a.fp8_max));
+          if (clamp)
+            v[k] = KEEP_NAN ? make_float2(clamp_or_nan(v[k].x, a.fp8_max), clamp_or_nan(v[k].y, a.fp8_max))
+                            : make_float2(clamp_abs(v[k].x, a.fp8_max), clamp_abs(v[k].y, a.fp8_max));
         }
         st_stream8(qrow + slot_col<LPR, HS, TS>(s, lane, hv, th), pack_e4m3x8(v[0], v[1], v[2], v[3]));
       }

@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kThreads) append_scalar_kernel(const AppendArg
     for (int j = lane; j < N; j += 32) amax = fmaxf(amax, fabsf(value(j)));
     const float sc = __fdiv_rn(fmaxf(group_max<32>(amax), 1e-4f), a.fp8_max);
     for (int j = lane; j < N; j += 32)
-      codes[j] = static_cast<uint8_t>(e4m3x2(make_float2(clamp_abs(__fdiv_rn(value(j), sc), a.fp8_max), 0.f)));
+      codes[j] = static_cast<uint8_t>(e4m3x2(make_float2(clamp_or_nan(__fdiv_rn(value(j), sc), a.fp8_max), 0.f)));
     if (lane == 0) *scale = sc;
   }
 }

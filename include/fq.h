@@ -307,7 +307,8 @@ typedef struct fq_paged_cache {
  * q codes go to q_out [T, Hq, D], their scales to q_scale [T, Hq]; k and v codes and scales of token t go
  * to slot slots[t] = page * page_size + offset of the cache. A slot outside [0, pages*page_size) (a
  * negative one, say) marks padding: its q row is computed, nothing is written to the cache. Slots that
- * no token names keep their contents. Two tokens of one call must not name the same slot (its contents
+ * no token names keep their contents. A NaN is left out of its row's maximum and keeps a NaN code; a v row that holds
+ * an infinity has an infinite scale, code 0 for finite values and NaN for infinities. Two tokens of one call must not name the same slot (its contents
  * would be either token's, or parts of both). T = 0 is a no-op; Hq = 0 is allowed.
  */
 int fq_qkv_norm_rope_append(const void* qkv, int64_t token_stride, const void* wq, const void* wk, const void* cos,

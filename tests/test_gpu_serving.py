@@ -328,6 +328,61 @@ def test_append_zero_rows_and_empty():
     assert q.shape == (0, 4, 128) and all(torch.equal(x, y) for x, y in zip(before, cache))
 
 
+NON_FINITE = [(400, 32, 8, 128, "bf16"), (400, 32, 8, 128, "fp16"), (9, 4, 2, 128, "bf16"), (7, 2, 2, 64, "fp16"),
+              (5, 1, 3, 256, "bf16"), (6, 4, 2, 100, "bf16")]
+
+
+@pytest.mark.parametrize("fmax", [448.0, 240.0])
+@pytest.mark.parametrize("T,Hq,Hk,D,dt", NON_FINITE)
+def test_append_infinities_and_nan_in_values(T, Hq, Hk, D, dt, fmax):
+    """A V row that holds an infinity has an infinite scale, code 0 for its finite values (x / inf) and NaN for the
+    infinity (inf / inf); a NaN is left out of the row's maximum and stays one. Other rows are as without them."""
+    case = (T, Hq, Hk, D, D if D % 4 == 0 else 0, 16, dt, "fp32", 0, fmax, "phtd")
+    d, cache, _ = append_inputs(case)
+    slots = torch.arange(T, device="cuda")
+    v = d["qk"][:, (Hq + Hk) * D:(Hq + 2 * Hk) * D].view(T, Hk, D)
+    v[0, 0, 3], v[1, Hk - 1, D - 1], v[2, 0, D // 2] = math.inf, -math.inf, math.nan
+    v[3, Hk - 1, 1], v[3, Hk - 1, D - 2] = math.inf, math.nan
+    fq.qkv_norm_rope_append(d["qk"], d["wq"], d["wk"], d["cos"], d["sin"], slots, *cache, Hq, Hk, fp8_max=fmax)
+    x = v.cpu().float()
+    s = x.abs().nan_to_num(nan=0.0, posinf=math.inf).amax(-1).clamp(min=1e-4) / torch.tensor(fmax)
+    want = (x / s[..., None]).double()
+    at, off = slots.cpu() // 16, slots.cpu() % 16
+    got = cache[1].cpu()[at, :, off]
+    assert torch.equal(cache[3].cpu()[at, :, off], s)
+    nan = want.isnan()
+    assert int(nan.sum()) == 5 and torch.equal((got & 0x7F) == 0x7F, nan)
+    assert torch.equal(got[~nan], ref.e4m3_codes(want.clamp(-fmax, fmax))[~nan])
+
+
+@pytest.mark.parametrize("fmax", [448.0, 240.0])
+@pytest.mark.parametrize("T,Hq,Hk,D,dt", NON_FINITE)
+def test_append_infinities_and_nan_in_normed_rows(T, Hq, Hk, D, dt, fmax):
+    """Of a q or k row with an infinity (rstd = 0) its two rotated places are NaN and the others zero; a NaN makes the
+    whole row NaN. Either way the scale is the floor's, and the token's other rows are as without them."""
+    case = (T, Hq, Hk, D, D, 16, dt, "fp32", 0, fmax, "phtd")
+    d, cache, _ = append_inputs(case)
+    slots = torch.arange(T, device="cuda")
+
+    def rows():
+        q, qs = fq.qkv_norm_rope_append(d["qk"], d["wq"], d["wk"], d["cos"], d["sin"], slots, *cache, Hq, Hk, fp8_max=fmax)
+        at, off = slots // 16, slots % 16
+        return torch.cat([q, cache[0][at, :, off]], 1).cpu(), torch.cat([qs, cache[2][at, :, off]], 1).cpu()
+
+    clean, clean_scale = rows()
+    x = d["qk"][:, :(Hq + Hk) * D].view(T, Hq + Hk, D)
+    x[0, 0, 3], x[1, Hq, 5], x[2, Hq + Hk - 1, D - 1], x[3, Hq - 1, 0] = math.inf, -math.inf, math.nan, math.nan
+    codes, scale = rows()
+    nan = torch.zeros(codes.shape, dtype=torch.bool)
+    hit = torch.zeros(scale.shape, dtype=torch.bool)
+    for t, h, at in ((0, 0, [3, 3 + D // 2]), (1, Hq, [5, 5 + D // 2]), (2, Hq + Hk - 1, slice(None)), (3, Hq - 1, slice(None))):
+        nan[t, h, at], hit[t, h] = True, True
+    assert torch.equal((codes & 0x7F) == 0x7F, nan)
+    assert bool(((codes[hit] & 0x7F)[~nan[hit]] == 0).all())
+    assert bool((scale[hit] == torch.tensor(1e-4) / torch.tensor(fmax)).all())
+    assert torch.equal(codes[~hit], clean[~hit]) and torch.equal(scale[~hit], clean_scale[~hit])
+
+
 def test_append_refusals():
     case = (6, 4, 2, 128, 128, 16, "bf16", "fp32", 0, 448.0, "phtd")
     d, cache, slots = append_inputs(case)
