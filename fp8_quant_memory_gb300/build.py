@@ -112,14 +112,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
         binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        binding_obj = binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
+    if os.path.exists(BINDING):
+        os.remove(BINDING)  # made for the library before this one
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+    # The library is in place whatever becomes of the binding, which needs Python's and torch's headers.
+    _link_binding(binding.result())
     return LIB
 
 
