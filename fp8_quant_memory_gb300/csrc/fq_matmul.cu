@@ -617,11 +617,13 @@ bool launch_wide(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
   if (!byte_tensor_map(&amap, 2, a.a, ad, as, ab, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !byte_tensor_map(&wmap, 2, a.b, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B))
     return false;
-  // Output boxes of 64 columns, 128 bytes; rows that are not whole 16-byte pieces are stored directly. The map counts
-  // 16-bit elements: coordinates are 32-bit, and as bytes those of columns from 2^30 on would not fit.
+  // Output boxes of 64 columns, 128 bytes. The map counts 16-bit elements: coordinates are 32-bit, and as bytes those of
+  // columns from 2^30 on would not fit. Rows that are not whole 16-byte pieces are stored directly, by their stride and
+  // by their length: a box store cut off by the end of a row writes zeros up to the next 16-byte boundary (measured: 4
+  // elements behind rows of 2300), which in an output whose rows are further apart is not the call's to write.
   const uint64_t od[2] = {static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.M)}, os[1] = {static_cast<uint64_t>(a.out_stride) * 2};
   const uint32_t ob[2] = {64, 32};
-  p.tma_store = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && os[0] % 16 == 0 &&
+  p.tma_store = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && os[0] % 16 == 0 && a.N % 8 == 0 &&
                 half_tensor_map(&omap, 2, a.out, od, os, ob, CU_TENSOR_MAP_SWIZZLE_128B);
   p.tiles_m = static_cast<int32_t>((a.M + kTileM - 1) / kTileM);
   p.tiles_n = static_cast<int32_t>((a.N + kTileN - 1) / kTileN);

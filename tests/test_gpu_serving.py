@@ -88,6 +88,16 @@ def test_matmul_strided(size):
     assert bool((buf[:, N:] == 7.0).all())
 
 
+@pytest.mark.parametrize("M,N,stride", [(2500, 2300, 2312), (2500, 2297, 2304), (2400, 2302, 2302 * 2), (2400, 2296, 2304), (2400, 2303, 2309)])
+def test_matmul_padded_output_of_many_rows(M, N, stride):
+    """Rows of the output a multiple of 16 bytes apart whose length is not one: what lies between them stays."""
+    a, sa, b, sb = matmul_inputs(M, N, 1040, seed=11)
+    buf = torch.full((M, stride), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = fq.fp8_matmul(a, sa, b, sb, out=buf[:, :N])
+    assert bool((buf[:, N:] == 7.0).all())
+    ref.assert_matmul(got, a, sa, b, sb)
+
+
 @pytest.mark.parametrize("size", [(9, 130, 256), (150, 260, 384)], ids=str)
 def test_matmul_misaligned(size):
     """Operands one byte past a 16-byte boundary take the scalar kernel."""
