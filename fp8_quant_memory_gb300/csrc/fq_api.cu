@@ -168,7 +168,7 @@ extern "C" {
 
 const char* fq_last_error(void) { return g_err.c_str(); }
 
-int fq_version(void) { return 3; }
+int fq_version(void) { return 4; }
 
 int fq_device_status(unsigned int* word, int clear, cudaStream_t stream) {
   if (word == nullptr) return fail(FQ_ERR_INVALID_ARG, "fq_device_status: word is null");

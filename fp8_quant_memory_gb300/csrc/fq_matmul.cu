@@ -311,15 +311,8 @@ __global__ void __launch_bounds__(kNarrowThreads<G>, 1)
   if (warp == kProducts) tmem_free<1>(tmem, C::kCols);
 }
 
-// CTAs that share a tile's k: as many as occupy SMs that would be idle.
-int narrow_split(int64_t tiles, int64_t nkb) {
-  int split = 1;
-  while (split < kMaxSplit && 2 * split * tiles <= sm_count() && 2 * split <= nkb) split *= 2;
-  return split;
-}
-
 template <int NT>
-bool launch_narrow(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
+bool launch_narrow(const MatmulArgs& a, MmArgs p, const MatmulPlan& plan, cudaStream_t s) {
   CUtensorMap wmap, amap;
   const uint64_t wd[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.N)}, ws[1] = {static_cast<uint64_t>(a.b_stride)};
   const uint64_t ad[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.M)}, as[1] = {static_cast<uint64_t>(a.a_stride)};
@@ -330,11 +323,11 @@ bool launch_narrow(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
   p.tiles_n = static_cast<int32_t>((a.N + 127) / 128);
   p.tiles_m = static_cast<int32_t>((a.M + NT - 1) / NT);
   if (p.tiles_n > 65535 || p.tiles_m > 65535) return false;
-  const int split = narrow_split(static_cast<int64_t>(p.tiles_n) * p.tiles_m, p.nkb);
+  const int split = plan.split;
   auto kern = split == 1 ? matmul_narrow_kernel<NT, 1, 1> : split == 2 ? matmul_narrow_kernel<NT, 2, 1> : matmul_narrow_kernel<NT, 4, 1>;
   int threads = kNarrowThreads<1>;
   if constexpr (NT == 64) {
-    if (p.nkb / split >= kTwoGroupBlocks) {
+    if (plan.groups == 2) {
       kern = split == 1 ? matmul_narrow_kernel<NT, 1, 2> : split == 2 ? matmul_narrow_kernel<NT, 2, 2> : matmul_narrow_kernel<NT, 4, 2>;
       threads = kNarrowThreads<2>;
     }
@@ -609,7 +602,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   if (warp == 1) tmem_free<2>(tmem, 512);
 }
 
-bool launch_wide(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
+bool launch_wide(const MatmulArgs& a, MmArgs p, const MatmulPlan& plan, cudaStream_t s) {
   CUtensorMap amap, wmap, omap{};
   const uint64_t ad[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.M)}, as[1] = {static_cast<uint64_t>(a.a_stride)};
   const uint64_t wd[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.N)}, ws[1] = {static_cast<uint64_t>(a.b_stride)};
@@ -629,11 +622,9 @@ bool launch_wide(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
   p.tiles_n = static_cast<int32_t>((a.N + kTileN - 1) / kTileN);
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   if (tiles > 0x0fffffff) return false;
-  // Whole rounds of the CTA pairs first; the rest cut in two or four if one round takes all the cuts (a narrow
-  // piece costs about 0.85 of a whole one).
   const int64_t pairs = sm_count() / 2, rest = tiles % pairs;
   p.whole = static_cast<int32_t>(tiles - rest);
-  p.parts = rest * 4 <= pairs ? 4 : rest * 2 <= pairs ? 2 : 1;
+  p.parts = plan.parts;
   p.pieces = static_cast<int32_t>(p.whole + rest * p.parts);
   constexpr size_t smem = sizeof(WideShared) + 1024;
   static_assert(smem <= 227 * 1024, "the ring and the staging rows fit the SM");
@@ -644,6 +635,37 @@ bool launch_wide(const MatmulArgs& a, MmArgs p, cudaStream_t s) {
 }
 
 }  // namespace
+
+MatmulPlan matmul_plan(int64_t M, int64_t N, int64_t K, int sm_total) {
+  const int64_t nkb = (K + kBK - 1) / kBK;
+  const double blocks = static_cast<double>(nkb), sms = sm_total, pairs = sm_total / 2;
+  // CTAs that share a tile's k: as many as occupy SMs that would be idle.
+  auto narrow_tiles = [&](int nt) { return ((N + 127) / 128) * ((M + nt - 1) / nt); };
+  auto split_of = [&](int nt) {
+    int split = 1;
+    while (split < kMaxSplit && 2 * split * narrow_tiles(nt) <= sm_total && 2 * split <= nkb) split *= 2;
+    return split;
+  };
+  // The kernel with the least estimated time. A CTA of the narrow kernel costs a start and a time per block of k,
+  // which grow with its columns; the wide kernel a start and a time per block for each round of CTA pairs. In us,
+  // fitted to a sweep over M of 1 to 2048 and (N, K) of (1111, 1968) to (8192, 8192), where the choice is the fastest
+  // or within 15% of it: at 4096 x 4096 for example M = 16 takes 6.2 us with 16 columns and 7.8 with 64, M = 64 takes
+  // 12.8 and 7.9, M = 256 takes 16.9 with 64, 16.4 with 128 and 18.8 wide, M = 512 26.1 with 128 and 19.5 wide.
+  auto narrow = [&](int nt, double start, double block) {
+    const int split = split_of(nt);
+    return std::ceil(narrow_tiles(nt) * split / sms) * (start + std::ceil(blocks / split) * block);
+  };
+  const double t16 = narrow(16, 2.8, 0.43), t32 = narrow(32, 3.0, 0.43), t64 = narrow(64, 4.0, 0.47), t128 = narrow(128, 6.0, 0.67);
+  const double tiles = static_cast<double>((M + kTileM - 1) / kTileM) * static_cast<double>((N + kTileN - 1) / kTileN);
+  const double rest = std::fmod(tiles, pairs);
+  const double wide = 4.5 + blocks * 0.47 * (std::floor(tiles / pairs) + (rest * 2 <= pairs ? 0.85 : 1.0));
+  const double best = std::fmin(std::fmin(std::fmin(t16, t32), std::fmin(t64, t128)), wide);
+  // Of the wide kernel, whole rounds of the CTA pairs first; the rest cut in two or four if one round takes all the
+  // cuts (a narrow piece costs about 0.85 of a whole one).
+  if (best == wide) return {kTileM, 1, 1, rest == 0 ? 1 : rest * 4 <= pairs ? 4 : rest * 2 <= pairs ? 2 : 1};
+  const int rows = best == t16 ? 16 : best == t32 ? 32 : best == t64 ? 64 : 128, split = split_of(rows);
+  return {rows, split, rows == 64 && nkb / split >= kTwoGroupBlocks ? 2 : 1, 1};
+}
 
 bool launch_matmul_tc(const MatmulArgs& a, int dtype, cudaStream_t s) {
   MmArgs p{};
@@ -662,26 +684,14 @@ bool launch_matmul_tc(const MatmulArgs& a, int dtype, cudaStream_t s) {
   // a single row's stride is never used, but has to be a valid one
   if (b.M == 1) b.a_stride = (b.K + 15) / 16 * 16;
   if (b.N == 1) b.b_stride = (b.K + 15) / 16 * 16;
-  // The kernel with the least estimated time. A CTA of the narrow kernel costs a start and a time per block of k,
-  // which grow with its columns; the wide kernel a start and a time per block for each round of CTA pairs. In us,
-  // fitted to a sweep over M of 1 to 2048 and (N, K) of (1111, 1968) to (8192, 8192), where the choice is the fastest
-  // or within 15% of it: at 4096 x 4096 for example M = 16 takes 6.2 us with 16 columns and 7.8 with 64, M = 64 takes
-  // 12.8 and 7.9, M = 256 takes 16.9 with 64, 16.4 with 128 and 18.8 wide, M = 512 26.1 with 128 and 19.5 wide.
-  const double nkb = static_cast<double>(p.nkb), sms = sm_count(), pairs = sm_count() / 2;
-  auto narrow = [&](int nt, double start, double block) {
-    const int64_t tiles = ((a.N + 127) / 128) * ((a.M + nt - 1) / nt);
-    const int split = narrow_split(tiles, p.nkb);
-    return std::ceil(tiles * split / sms) * (start + std::ceil(nkb / split) * block);
-  };
-  const double t16 = narrow(16, 2.8, 0.43), t32 = narrow(32, 3.0, 0.43), t64 = narrow(64, 4.0, 0.47), t128 = narrow(128, 6.0, 0.67);
-  const double tiles = static_cast<double>((a.M + kTileM - 1) / kTileM) * static_cast<double>((a.N + kTileN - 1) / kTileN);
-  const double wide = 4.5 + nkb * 0.47 * (std::floor(tiles / pairs) + (std::fmod(tiles, pairs) * 2 <= pairs ? 0.85 : 1.0));
-  const double best = std::fmin(std::fmin(std::fmin(t16, t32), std::fmin(t64, t128)), wide);
-  if (best == wide) return launch_wide(b, p, s);
-  if (best == t16) return launch_narrow<16>(b, p, s);
-  if (best == t32) return launch_narrow<32>(b, p, s);
-  if (best == t64) return launch_narrow<64>(b, p, s);
-  return launch_narrow<128>(b, p, s);
+  const MatmulPlan plan = matmul_plan(a.M, a.N, a.K, sm_count());
+  switch (plan.rows) {
+    case 16: return launch_narrow<16>(b, p, plan, s);
+    case 32: return launch_narrow<32>(b, p, plan, s);
+    case 64: return launch_narrow<64>(b, p, plan, s);
+    case 128: return launch_narrow<128>(b, p, plan, s);
+    default: return launch_wide(b, p, plan, s);
+  }
 }
 
 }  // namespace fq

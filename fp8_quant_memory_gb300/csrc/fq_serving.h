@@ -79,6 +79,14 @@ void launch_overlapped(void (*kern)(P...), dim3 grid, unsigned threads, size_t s
   cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// How the tensor cores take a product on a GPU of `sms` SMs: rows of `a` per tile (16 to 128: the narrow kernel, 256: the
+// wide one); narrow: CTAs that share a tile's k, and groups of epilogue warps; wide: column ranges that each tile of
+// the last round is cut into.
+struct MatmulPlan {
+  int rows, split, groups, parts;
+};
+MatmulPlan matmul_plan(int64_t M, int64_t N, int64_t K, int sms);
+
 // tcgen05 kernels: 16-byte aligned operands and strides. False (nothing launched) otherwise.
 bool launch_matmul_tc(const MatmulArgs& a, int dtype, cudaStream_t s);
 void launch_matmul_scalar(const MatmulArgs& a, int dtype, cudaStream_t s);

@@ -127,6 +127,19 @@ int fq_fp8_matmul(const uint8_t* a, int64_t a_stride, const float* a_scale, int6
   return fq::finish_launch(fn, stream);
 }
 
+int fq_fp8_matmul_plan(int64_t M, int64_t N, int64_t K, int sms, int* plan) {
+  const char* fn = "fq_fp8_matmul_plan";
+  if (plan == nullptr) return fq::set_error(FQ_ERR_INVALID_ARG, "%s: plan is null", fn);
+  if (M < 1 || N < 1 || K < 1 || M > kMaxDim || N > kMaxDim || K > kMaxDim || sms < 2)
+    return fq::set_error(FQ_ERR_INVALID_ARG, "%s: need 1 <= M, N, K < 2^31 - 1024 and at least 2 SMs", fn);
+  const fq::MatmulPlan p = fq::matmul_plan(M, N, K, sms);
+  plan[0] = p.rows;
+  plan[1] = p.split;
+  plan[2] = p.groups;
+  plan[3] = p.parts;
+  return fq::succeed();
+}
+
 int fq_qkv_norm_rope_append(const void* qkv, int64_t token_stride, const void* wq, const void* wk, const void* cos,
                             const void* sin, const int64_t* slots, uint8_t* q_out, float* q_scale,
                             const fq_paged_cache* cache, int64_t T, int64_t Hq, int64_t Hk, int64_t D,

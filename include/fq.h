@@ -283,6 +283,15 @@ int fq_fp8_matmul(const uint8_t* a, int64_t a_stride, const float* a_scale, int6
                   int64_t M, int64_t N, int64_t K, int dtype, cudaStream_t stream);
 
 /*
+ * Diagnostic, host only: the kernel that fq_fp8_matmul takes for aligned operands on a GPU of `sms` SMs (152 on GB300).
+ *   plan[0]: rows of a per tile, 16, 32, 64 or 128 (few rows: weights on the tensor-memory lanes) or 256 (CTA pairs)
+ *   plan[1]: CTAs that share a tile's k (1, 2 or 4);  plan[2]: groups of epilogue warps (1 or 2);
+ *   plan[3]: column ranges that each tile of the last round is cut into (1, 2 or 4; with plan[0] = 256)
+ * Returns FQ_OK or FQ_ERR_INVALID_ARG (plan null, a size outside [1, 2^31 - 1024), sms < 2).
+ */
+int fq_fp8_matmul_plan(int64_t M, int64_t N, int64_t K, int sms, int* plan);
+
+/*
  * A paged FP8 key-value cache: `pages` pages of `page_size` tokens. Token slot o of page p holds, for
  * key head h, the K row of head_dim codes at k + p*page_stride + h*head_stride + o*token_stride and its
  * scale at k_scale[p*scale_page_stride + h*scale_head_stride + o*scale_token_stride]; the V row likewise
