@@ -322,7 +322,6 @@ bool launch_narrow(const MatmulArgs& a, MmArgs p, const MatmulPlan& plan, cudaSt
     return false;
   p.tiles_n = static_cast<int32_t>((a.N + 127) / 128);
   p.tiles_m = static_cast<int32_t>((a.M + NT - 1) / NT);
-  if (p.tiles_n > 65535 || p.tiles_m > 65535) return false;
   const int split = plan.split;
   auto kern = split == 1 ? matmul_narrow_kernel<NT, 1, 1> : split == 2 ? matmul_narrow_kernel<NT, 2, 1> : matmul_narrow_kernel<NT, 4, 1>;
   int threads = kNarrowThreads<1>;
@@ -652,6 +651,8 @@ MatmulPlan matmul_plan(int64_t M, int64_t N, int64_t K, int sm_total) {
   // or within 15% of it: at 4096 x 4096 for example M = 16 takes 6.2 us with 16 columns and 7.8 with 64, M = 64 takes
   // 12.8 and 7.9, M = 256 takes 16.9 with 64, 16.4 with 128 and 18.8 wide, M = 512 26.1 with 128 and 19.5 wide.
   auto narrow = [&](int nt, double start, double block) {
+    // its tiles are the y and z axes of its grid, 65535 at most
+    if ((N + 127) / 128 > 65535 || (M + nt - 1) / nt > 65535) return static_cast<double>(INFINITY);
     const int split = split_of(nt);
     return std::ceil(narrow_tiles(nt) * split / sms) * (start + std::ceil(blocks / split) * block);
   };

@@ -30,6 +30,12 @@ def test_every_variant_has_a_size():
     assert set(cases.WIDE) == {(256, 1, 1, cuts) for cuts in (1, 2, 4)}
 
 
+@pytest.mark.parametrize("size", [(1, 128 * 65535 + 1, 16384), (16, 128 * 65536, 12000), (40, 1 << 30, 1 << 16), (128 * 65535 + 1, 16, 1 << 20)], ids=str)
+def test_more_tiles_than_a_grid_axis(size):
+    """The few-row kernel has a tile per place of two grid axes of at most 65535: beyond, the CTA pairs take it."""
+    assert cases.plan(*size)[0] == 256
+
+
 def test_plan_refusals(lib):
     p = (ctypes.c_int * 4)()
     assert lib.fq_fp8_matmul_plan(1, 1, 1, 2, p) == 0
