@@ -65,3 +65,26 @@ def test_one_block_long_ring():
     first = fq.paged_attention(*x, want_lse=True)
     again = fq.paged_attention(*x, want_lse=True)
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("page", [7, 32])
+@pytest.mark.parametrize("G", [5, 12, 20])
+@pytest.mark.parametrize("D", [48, 112, 176, 240])
+def test_every_kernel(D, G, page):
+    """Head sizes below each padded one, groups of up to 8 query heads, up to 16 and more, rows copied one by one and as
+    boxes; heads that end in the middle of a block and of a unit."""
+    lens = [1700, 0, 900, 33, 16, 511, 1, 1024, 77]
+    x = attention_inputs(lens, 2 * G, 2, D, page, seed=115, q_extra=1)
+    x[6][0, 9], x[6][5, 0] = -1, -1
+    check_attention(x, "fp16" if G == 12 else "bf16")
+
+
+@pytest.mark.parametrize("D,page", [(128, 16), (96, 32), (80, 7), (240, 16), (64, 24), (16, 64)])
+def test_rows_of_a_wider_cache(D, page):
+    """A cache that is the first D columns of wider rows, NaN codes behind them."""
+    x = attention_inputs([400, 31, 0, 1000], 8, 2, D, page, seed=116)
+    for i in (2, 3):
+        wide = torch.full((*x[i].shape[:3], D + 32), 0x7F, dtype=torch.uint8, device="cuda")
+        wide[..., :D] = x[i]
+        x[i] = wide[..., :D]
+    check_attention(x)

@@ -288,6 +288,22 @@ def test_append_misaligned_cache():
     check_append(d, before, cache, slots, q.cpu(), qs.cpu(), case)
 
 
+@pytest.mark.parametrize("T,D,page", [(40, 128, 16), (400, 128, 64), (30, 96, 7), (20, 256, 16), (9, 100, 16)])
+def test_append_into_rows_of_a_wider_cache(T, D, page):
+    """A cache that is the first D columns of wider rows; what lies behind them stays."""
+    Hq, Hk = 32, 8
+    case = (T, Hq, Hk, D, D if D % 16 == 0 else 0, page, "bf16", "fp32", 0, 448.0, "phtd")
+    d, cache, slots = append_inputs(case)
+    wide = [torch.full((*c.shape[:3], D + 32), 0x55, dtype=torch.uint8, device="cuda") for c in cache[:2]]
+    for w, c in zip(wide, cache):
+        w[..., :D] = c
+    cache = [w[..., :D] for w in wide] + cache[2:]
+    before = [t.clone() for t in cache]
+    q, qs = fq.qkv_norm_rope_append(d["qk"], d["wq"], d["wk"], d["cos"], d["sin"], slots, *cache, Hq, Hk, rope_dim=case[4])
+    check_append(d, before, cache, slots, q.cpu(), qs.cpu(), case)
+    assert all(bool((w[..., D:] == 0x55).all()) for w in wide)
+
+
 def test_append_matches_prologue():
     """q and k rows are the prologue's, up to the last place of its fp32 arithmetic."""
     case = (300, 32, 8, 128, 128, 64, "bf16", "fp32", 0, 448.0, "phtd")
