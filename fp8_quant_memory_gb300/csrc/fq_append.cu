@@ -150,8 +150,9 @@ bool launch_typed(const AppendArgs& p, cudaStream_t s) {
 // Arithmetic (q and k): u = x*w exactly in fp32 (two 8- or 11-bit significands), z = rope(u), rstd = 1/sqrt(sum x^2
 // / 128 + eps); the definition's y equals rstd * z up to rounding, and so do amax = rstd * max |z| and the codes
 // e4m3(z * m) with m = rstd / scale. rstd and m come from the hardware's approximations with one Newton step each,
-// which brings them within an ulp: the codes sit as near to the 64-bit definition as those of fp32 steps. v rows are
-// divided by their scale exactly, as everywhere.
+// which brings them within an ulp: the codes sit as near to the 64-bit definition as those of fp32 steps, though a few in
+// a million, at ties, are not the other kernel's. The scale is amax / fp8_max correctly rounded, by Markstein's
+// correction of a quotient from a correctly rounded reciprocal. v rows are divided by their scale exactly, as everywhere.
 constexpr int kSD = 128;
 constexpr int kSRows = 32;                         // rows per stage
 constexpr int kSWarps = 8;                         // consumer warps
@@ -242,7 +243,7 @@ __device__ __forceinline__ void stream_qk(const StreamArgs& a, uint32_t xrow, ui
   const float rstd = fabsf(e0) < 0.5f ? __fmaf_rn(0.5f * r0, e0, r0) : r0;
   const float amax = fmaxf(__fmul_rn(rstd, am), 1e-4f);
   const float s0 = __fmul_rn(amax, a.rcp_fp8_max);
-  const float sc = __fmaf_rn(__fmaf_rn(-s0, r.fp8_max, amax), a.rcp_fp8_max, s0);  // RN(amax / fp8_max)
+  const float sc = __fmaf_rn(__fmaf_rn(-s0, r.fp8_max, amax), a.rcp_fp8_max, s0);  // amax / fp8_max (Markstein)
   float rc;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rc) : "f"(sc));
   rc = __fmaf_rn(rc, __fmaf_rn(-sc, rc, 1.0f), rc);

@@ -650,6 +650,9 @@ MatmulPlan matmul_plan(int64_t M, int64_t N, int64_t K, int sm_total) {
   // fitted to a sweep over M of 1 to 2048 and (N, K) of (1111, 1968) to (8192, 8192), where the choice is the fastest
   // or within 15% of it: at 4096 x 4096 for example M = 16 takes 6.2 us with 16 columns and 7.8 with 64, M = 64 takes
   // 12.8 and 7.9, M = 256 takes 16.9 with 64, 16.4 with 128 and 18.8 wide, M = 512 26.1 with 128 and 19.5 wide.
+  // It counts starts and blocks, no bytes, and was not fitted beyond these sizes: 1 x 28672 x 8192 goes to the CTA pairs
+  // by an estimate of 60 us and takes 81 there (16 rows 59), 1 x 151936 x 4096 takes 177 (16 rows 134; the weights
+  // alone, at the copy rate, 35 and 92 us); 64 x 8192 x 28672 takes 45 (35).
   auto narrow = [&](int nt, double start, double block) {
     // its tiles are the y and z axes of its grid, 65535 at most
     if ((N + 127) / 128 > 65535 || (M + nt - 1) / nt > 65535) return static_cast<double>(INFINITY);

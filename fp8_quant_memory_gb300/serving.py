@@ -63,14 +63,15 @@ def qkv_norm_rope_append(qkv: torch.Tensor, wq: torch.Tensor, wk: torch.Tensor, 
 
     qkv: [T, S], S >= (Hq + 2*Hk)*D: q heads, k heads, v heads. slots: [T] int64, page * page_size +
     offset per token; a slot outside the cache (-1) writes nothing there. The tokens' slots must differ.
-    Returns (q codes uint8 [T, Hq, D], q_scale fp32 [T, Hq]); the cache is updated in place.
+    Returns (q codes uint8 [T, Hq, D], q_scale fp32 [T, Hq]); the cache is updated in place. The last place of q and k
+    scales, and a few of their codes in a million, at ties, depend on how a prompt is cut into calls.
     """
     return (_native or _load()).qkv_norm_rope_append(qkv, wq, wk, cos, sin, slots, k_cache, v_cache, k_scale, v_scale,
                                                      Hq, Hk, eps, fp8_max, rope_dim, q_out, q_scale)
 
 
 def paged_attention_workspace_bytes(B: int, Hq: int, Hk: int, D: int, max_seq_len: int) -> int:
-    """Workspace bytes of paged_attention on the current device."""
+    """Workspace bytes of paged_attention on the current device (enough for any smaller max_seq_len too)."""
     return int(_capi.load().fq_paged_attention_workspace_bytes(B, Hq, Hk, D, max_seq_len))
 
 

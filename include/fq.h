@@ -274,9 +274,10 @@ int fq_rmsnorm_bwd_noalloc(const void* x, const void* w, const void* grad_y, voi
  * fp32 and one rounding to dtype. a: [M, K] e4m3 codes, a_scale: [M, ceil(K/128)] fp32; b: [N, K] codes
  * (a weight stored row by output column), b_scale: [ceil(N/128), ceil(K/128)] fp32, one scale per
  * 128 x 128 block; out: [M, N] dtype. Rows are contiguous, *_stride elements apart; the strides of what
- * is only read may be 0. M, N >= 0 (0: no-op), K >= 1.
+ * is only read may be 0. M, N >= 0 (0: no-op), K >= 1. What lies between the rows of out stays as it was.
  * Operands that are 16-byte aligned with strides that are multiples of 16 take the tensor cores; other
- * layouts take a scalar kernel with the same results up to the order of the sums.
+ * layouts take a scalar kernel with the same results up to the order of the sums. That order also depends
+ * on M, N, K and the GPU's size (fq_fp8_matmul_plan), not on timing: the same call gives the same bits.
  */
 int fq_fp8_matmul(const uint8_t* a, int64_t a_stride, const float* a_scale, int64_t a_scale_stride, const uint8_t* b,
                   int64_t b_stride, const float* b_scale, int64_t b_scale_stride, void* out, int64_t out_stride,
@@ -315,7 +316,10 @@ typedef struct fq_paged_cache {
  *   v rows: scale = max(max_j |v_j|, 1e-4) / fp8_max, codes e4m3(clamp(v_j / scale, +-fp8_max)).
  * q codes go to q_out [T, Hq, D], their scales to q_scale [T, Hq]; k and v codes and scales of token t go
  * to slot slots[t] = page * page_size + offset of the cache. A slot outside [0, pages*page_size) (a
- * negative one, say) marks padding: its q row is computed, nothing is written to the cache. Slots that
+ * negative one, say) marks padding: its q row is computed, nothing is written to the cache. Calls of many
+ * rows, of few, and of other layouts take kernels whose fp32 steps differ in the last place: the last place
+ * of q and k scales, and a few of their codes in a million, at ties, depend on how a prompt is cut into calls
+ * (v rows do not). Slots that
  * no token names keep their contents. A NaN is left out of its row's maximum and keeps a NaN code; a v row that holds
  * an infinity has an infinite scale, code 0 for finite values and NaN for infinities. Two tokens of one call must not name the same slot (its contents
  * would be either token's, or parts of both). T = 0 is a no-op; Hq = 0 is allowed.
