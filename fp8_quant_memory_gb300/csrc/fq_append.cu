@@ -200,6 +200,25 @@ __device__ __forceinline__ void store_codes(uint8_t* row, int j, int flip, const
   st_stream16(row + kSD / 2 + 16 * j, make_uint4(h0.x, h0.y, h1.x, h1.y));
 }
 
+// The codes of a row whose sum of squares left fp32 (rstd = 0), where x*w or its rotation may have left it too: by the
+// definition's order y = rope((x * 0) * w), zeros, and NaN where one of a pair is not finite.
+template <typename T>
+__device__ __noinline__ void store_zero_row(uint32_t xrow, uint32_t w, int j, uint8_t* codes) {
+  uint2 c[2];
+#pragma unroll
+  for (int m = 0; m < 2; ++m) {
+    const uint32_t at = xrow + (2 * j + m) * 16, wat = w + (2 * j + m) * 16;
+    const uint4 xl = lds16(at), xh = lds16(at + kSRowBytes / 2), wl = lds16(wat), wh = lds16(wat + kSRowBytes / 2);
+    float2 z[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      z[e] = add2(mul2(mul2(Elem<T>::unpack(word(xl, e)), splat2(0.f)), Elem<T>::unpack(word(wl, e))),
+                  mul2(mul2(Elem<T>::unpack(word(xh, e)), splat2(0.f)), Elem<T>::unpack(word(wh, e))));
+    c[m] = pack_e4m3x8(z[0], z[1], z[2], z[3]);
+  }
+  store_codes(codes, j, 0, c, c);
+}
+
 // One q or k row by its four lanes; `xrow`, `tab` and `w` are shared-memory addresses (cos row, sin is one block
 // further; the head type's weight row).
 template <typename T, typename TT, bool kClamp>
@@ -267,6 +286,7 @@ __device__ __forceinline__ void stream_qk(const StreamArgs& a, uint32_t xrow, ui
   if (live) {
     store_codes(codes, j, flip, lo, hi);
     if (j == 0) *scale = sc;
+    if (rstd == 0.f) store_zero_row<T>(xrow, w, j, codes);
   }
 }
 

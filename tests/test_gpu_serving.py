@@ -409,6 +409,25 @@ def test_append_infinities_and_nan_in_normed_rows(T, Hq, Hk, D, dt, fmax):
     assert torch.equal(codes[~hit], clean[~hit]) and torch.equal(scale[~hit], clean_scale[~hit])
 
 
+@pytest.mark.parametrize("T,Hq,Hk,D", [(400, 32, 8, 128), (9, 4, 2, 128), (7, 2, 2, 64), (6, 4, 2, 100)])
+def test_append_rows_whose_squares_leave_fp32(T, Hq, Hk, D):
+    """rstd is 0 and so is every finite value of the row, also where x * w or its rotation alone would overflow."""
+    case = (T, Hq, Hk, D, D, 16, "bf16", "fp32", 0, 448.0, "phtd")
+    d, cache, _ = append_inputs(case)
+    slots = torch.arange(T, device="cuda")
+    x = d["qk"][:, :(Hq + Hk) * D].view(T, Hq + Hk, D)
+    rows = [(0, 0, 3.3e38), (1, Hq, -3e38), (2, Hq + Hk - 1, 1.5e38), (3, 1, 1e30), (4, Hq - 1, 2e19)]
+    for t, h, v in rows:
+        x[t, h] = v
+    x[5, 0, 7:9] = 3.3e38
+    q, qs = fq.qkv_norm_rope_append(d["qk"], d["wq"], d["wk"], d["cos"], d["sin"], slots, *cache, Hq, Hk)
+    at, off = slots // 16, slots % 16
+    codes, scale = torch.cat([q, cache[0][at, :, off]], 1).cpu(), torch.cat([qs, cache[2][at, :, off]], 1).cpu()
+    for t, h in [(t, h) for t, h, _ in rows] + [(5, 0)]:
+        assert bool(((codes[t, h] & 0x7F) == 0).all()), (t, h)
+        assert scale[t, h] == torch.tensor(1e-4) / torch.tensor(448.0)
+
+
 def test_append_refusals():
     case = (6, 4, 2, 128, 128, 16, "bf16", "fp32", 0, 448.0, "phtd")
     d, cache, slots = append_inputs(case)
