@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import fp8_quant_memory_gb300 as fq
+import serving_ref as ref
 from test_gpu_serving import attention_inputs, check_attention
 
 pytestmark = pytest.mark.gpu
@@ -88,3 +89,45 @@ def test_rows_of_a_wider_cache(D, page):
         wide[..., :D] = x[i]
         x[i] = wide[..., :D]
     check_attention(x)
+
+
+@pytest.mark.parametrize("Hq,Hk,D", [(32, 8, 128), (32, 2, 256)])
+def test_captured_with_other_lengths(Hq, Hk, D):
+    """One captured call, replayed as sequences grow, end and start: its split follows the lengths of each replay."""
+    most, page = 3000, 16
+    x = attention_inputs([most] * 6, Hq, Hk, D, page, seed=117)
+    lens = x[7]
+    held = lens.clone()
+    fq.paged_attention(*x, max_seq_len=most, want_lse=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = fq.paged_attention(*x, max_seq_len=most, want_lse=True)
+    for now in ([0] * 6, [1, 0, most, 5, 0, 0], [2999, 2048, 0, 1, 130, 700], [0, 0, 0, 0, 0, 17], [most] * 6, [1] * 6):
+        lens.copy_(torch.tensor(now, dtype=torch.int32))
+        out.fill_(7.0)
+        lse.fill_(7.0)
+        graph.replay()
+        ref.assert_attention(out, lse, *x, D ** -0.5)
+        eager = fq.paged_attention(*x, max_seq_len=most, want_lse=True)
+        assert torch.equal(out, eager[0]) and torch.equal(lse, eager[1])
+    lens.copy_(held)
+
+
+def test_two_threads():
+    """Calls of two host threads at once, each on its own stream with its own tensors."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    xs = [attention_inputs([500 + 300 * i, 40, 0, 1200], 8, 2, 128, 16, seed=118 + i) for i in range(2)]
+    alone = [fq.paged_attention(*x, want_lse=True) for x in xs]
+    torch.cuda.synchronize()
+
+    def many(x):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            got = [fq.paged_attention(*x, want_lse=True) for _ in range(50)]
+        stream.synchronize()
+        return got
+
+    with ThreadPoolExecutor(2) as pool:
+        for want, got in zip(alone, pool.map(many, xs)):
+            assert all(torch.equal(g[0], want[0]) and torch.equal(g[1], want[1]) for g in got)
