@@ -71,6 +71,7 @@ struct Item {
 };
 constexpr float kSlack = 8.f;                // powers of two by which a score may exceed its running maximum
 constexpr float kRoom = 7.f;                 // powers of two of the largest value weight when M is set; 2^(7 + 8) fits fp16
+constexpr float kUnroom = 0.0078125f;        // 2^-kRoom
 constexpr float kLowest = -3.402823466e38f;  // below every score: a maximum before the first token
 
 // A unit's rows are stored as kA tiles of [rows][128 bytes], then kB of [rows][64], keys before values.
@@ -146,10 +147,29 @@ __device__ __forceinline__ float ex2(float v) {
   return r;
 }
 
-__device__ __forceinline__ float lg2(float v) {
+// With subnormal results and arguments, for V scales at the lower end of fp32.
+__device__ __forceinline__ float ex2_all(float v) {
   float r;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
+}
+
+__device__ __forceinline__ float lg2_all(float v) {
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// What turns a sum of weighted values into the output, 2^(M - m) / l, as factors 2^(M + 7 - m) and 2^-7 / l: their product
+// may leave fp32's normal range where the output does not.
+struct Norm {
+  float scale, inv;
+  __device__ __forceinline__ float operator()(float v) const { return v * inv * scale; }
+  __device__ __forceinline__ float2 operator()(float2 v) const { return mul2(mul2(v, splat2(inv)), splat2(scale)); }
+};
+
+__device__ __forceinline__ Norm norm_of(float top, float topo, float l) {
+  return l == 0.f ? Norm{0.f, 0.f} : Norm{ex2_all(topo + kRoom - top), kUnroom / l};
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -756,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       const float* sk = &sm.scales[stage][0][kStep * slab + g];
       const float* sv = &sm.scales[stage][1][kStep * slab + g];
-      const float ks[2] = {sk[0], sk[8]}, lv[2] = {lg2(sv[0]), lg2(sv[8])};
+      const float ks[2] = {sk[0], sk[8]}, lv[2] = {lg2_all(sv[0]), lg2_all(sv[8])};
       float x[2][2], w[2][2];  // [token][head]
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -872,7 +892,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       // Thread (warp, lane) finishes head 8r + warp of the item, column `lane` of each piece of 32.
       const int64_t slot = 2 * static_cast<int64_t>(cta) + (first_segment ? 0 : 1);
       first_segment = false;
-      float norm[HG];
+      Norm norm[HG];
 #pragma unroll
       for (int r = 0; r < HG; ++r) {
         float top = kLowest, topo = kLowest, sum = 0.f;
@@ -884,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int w = 0; w < kSlabs; ++w)
           sum = fmaf(sm.stat[r * (CG * kSlabs) + w][warp][2], ex2(sm.stat[r * (CG * kSlabs) + w][warp][0] - top), sum);
-        norm[r] = sum == 0.f ? 0.f : ex2(topo - top) / sum;
+        norm[r] = norm_of(top, topo, sum);
         const int row = kHeads * r + warp;
         if (row < rows && lane == 0) {
           if (!whole)
@@ -916,7 +936,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int w = 0; w < kSlabs; ++w) v += sm.join[(r * CG + y) * kSlabs + w][warp][lane];
             const int row = kHeads * r + warp, d = 128 * y + (slim ? 8 : 16) * (lane >> 2) + 4 * k + (lane & 3);
             if (row < rows && d < p.D) {
-              if (whole) store_out(a.dtype, p.out, (static_cast<int64_t>(use.b) * p.Hq + head0 + row) * p.D + d, v * norm[r]);
+              if (whole) store_out(a.dtype, p.out, (static_cast<int64_t>(use.b) * p.Hq + head0 + row) * p.D + d, norm[r](v));
               else a.part[(slot * Item<DP, HG>::kRows + row) * DP + d] = v;
             }
           }
@@ -986,8 +1006,6 @@ struct JoinRow {
   }
 };
 
-__device__ __forceinline__ float norm_of(float top, float topo, float l) { return l == 0.f ? 0.f : ex2(topo - top) / l; }
-
 __device__ __forceinline__ float lse_of(float top, float l) {
   return l == 0.f ? -CUDART_INF_F : (top + log2f(l)) * 0.693147180559945309f;
 }
@@ -1022,10 +1040,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
     for (int row = first + others * warp; row < rows; row += others * kJoinWarps) {
       r = JoinRow<DP>();
       r.template add<4>(a, kRows, row, 0, 1, parts, slot_of);
-      const float norm = norm_of(r.top, r.topo, r.l);
+      const Norm norm = norm_of(r.top, r.topo, r.l);
 #pragma unroll
       for (int j = 0; j < kV; ++j)
-        if (2 * (lane + 32 * j) < p.D) store_pair(a, orow0 + row, lane + 32 * j, mul2(r.v[j], splat2(norm)));
+        if (2 * (lane + 32 * j) < p.D) store_pair(a, orow0 + row, lane + 32 * j, norm(r.v[j]));
       if (p.lse != nullptr && lane == 0) p.lse[orow0 + row] = lse_of(r.top, r.l);
     }
     return;
@@ -1045,12 +1063,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attention_join_kernel(const _
     }
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) lj = fmaf(stat[w].z, ex2(stat[w].x - mj), lj);
-    const float norm = norm_of(mj, oj, lj);
+    const Norm norm = norm_of(mj, oj, lj);
     for (int d = threadIdx.x; 2 * d < p.D; d += kJoinWarps * 32) {
       float2 y = make_float2(0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kJoinWarps; ++w) y = fma2(sum[w][d], splat2(ex2(stat[w].y - oj)), y);
-      store_pair(a, orow0 + row, d, mul2(y, splat2(norm)));
+      store_pair(a, orow0 + row, d, norm(y));
     }
     if (p.lse != nullptr && threadIdx.x == 0) p.lse[orow0 + row] = lse_of(mj, lj);
     __syncthreads();

@@ -567,6 +567,23 @@ def test_attention_small_weights_beside_large_ones(Hq, Hk, D, page):
     assert bool(((out - want).abs() <= tol).all()), float(((out - want).abs() / want).max())
 
 
+@pytest.mark.parametrize("Hq,Hk,D,page", [(8, 2, 128, 16), (32, 2, 256, 32), (4, 4, 64, 24)])
+@pytest.mark.parametrize("scale", [1e-36, 1e-35, 1e-34, 1e-32, 1e34])
+def test_attention_value_scales_at_the_ends(scale, Hq, Hk, D, page):
+    """V scales near the ends of fp32's range, subnormals among them; bf16 outputs share the range.
+
+    Beside the usual bounds (which grant each weight 2^-11 of itself): logarithms of up to 130 are held in steps of
+    2^-16, 2^-17 of a weight; 2^(M - m), from 2^-130 on, in steps of 2^-149, 2^-20 of the output, itself at most 2^11
+    of the bound; together less than 2^-4 of it. Below 2^-126 half a step of bf16 is 2^-134."""
+    x = attention_inputs([900, 20, 130], Hq, Hk, D, page, seed=82)
+    x[5].mul_(scale)
+    out, lse = fq.paged_attention(*x, want_lse=True)
+    want, want_lse, bound, lse_bound = ref.attention(*x, D ** -0.5)
+    tol = 2.0 ** -8 * want.abs() + bound * (1 + 2.0 ** -4) + 2.0 ** -134
+    assert bool(((out.cpu().double() - want).abs() <= tol).all())
+    assert bool(((lse.cpu().double() - want_lse).abs() <= lse_bound).all())
+
+
 def test_attention_all_empty():
     check_attention(attention_inputs([0, 0, -5], 8, 2, 128, 16, seed=62))
 
