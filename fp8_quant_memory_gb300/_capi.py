@@ -49,12 +49,18 @@ SIGNATURES = {
     "fq_rmsnorm_bwd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i64, _i64, _int, _f32, _vp]),
     "fq_rmsnorm_bwd_rstd": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _i64, _i64, _int, _vp]),
     "fq_fp8_matmul": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _int, _vp]),
+    "fq_fp8_matmul_epilogue": (_int, [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _int, _vp, _i64, _i64, _i64,
+                                      _i64, _int, _vp]),
     "fq_fp8_matmul_plan": (_int, [_i64, _i64, _i64, _int, ctypes.POINTER(_int)]),
     "fq_qkv_norm_rope_append": (_int, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64,
                                        _i64, _int, _int, _f32, _f32, _vp]),
     "fq_paged_attention_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i64]),
     "fq_paged_attention": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _i64, _i64, _i64,
                                   _i64, _i64, _i64, _f32, _int, _vp]),
+    "fq_paged_attention_window": (_int, [_vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _sz, _i64, _i64, _i64,
+                                         _i64, _i64, _i64, _i64, _i64, _f32, _int, _vp]),
+    "fq_paged_extend": (_int, [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp]),
+    "fq_sample": (_int, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _vp]),
     "fq_rmsnorm_bwd_noalloc": (_int, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _int, _f32, _vp]),
 }
 

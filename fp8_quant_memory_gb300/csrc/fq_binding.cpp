@@ -1,4 +1,4 @@
-// fq_binding.cpp -- CPython module over the FP8 serving entry points of include/fq.h. It checks devices, dtypes
+// fq_binding.cpp -- CPython module over the serving entry points of include/fq.h. It checks devices, dtypes
 // and shapes of torch tensors, allocates outputs and workspaces with torch, and calls libfq on the current stream
 // of the tensors' device. It is compiled, where the other entry points go through ctypes, because a decoding step
 // makes these calls with a few microseconds of GPU work in each: checking a dozen tensors attribute by attribute
@@ -107,13 +107,24 @@ T* ptr(Tensor t) {
 }
 
 // --------------------------------------------------------------------------- matrix product
-// (a, a_scale, b, b_scale, out_dtype, out or None) -> out
+int activation_arg(const char* fn, PyObject* o) {
+  static constexpr const char* kNames[] = {"relu", "gelu", "gelu_tanh", "silu"};
+  if (o == Py_None) return FQ_ACT_NONE;
+  if (PyUnicode_Check(o))
+    for (int i = 0; i < 4; ++i)
+      if (PyUnicode_CompareWithASCIIString(o, kNames[i]) == 0) return FQ_ACT_RELU + i;
+  refuse("%s: activation must be None, 'relu', 'gelu', 'gelu_tanh' or 'silu'", fn);
+}
+
+// (a, a_scale, b, b_scale, out_dtype, out or None, bias or None, activation or None, residual or None) -> out
 PyObject* matmul(PyObject* const* args, Py_ssize_t n) {
   const char* fn = "fp8_matmul";
-  want_args(fn, n, 6);
+  want_args(fn, n, 9);
   Tensor a = tensor(fn, "a", args[0]), sa = tensor(fn, "a_scale", args[1]), b = tensor(fn, "b", args[2]),
-         sb = tensor(fn, "b_scale", args[3]), given = tensor(fn, "out", args[5], true);
-  same_device(fn, {&a, &sa, &b, &sb, &given});
+         sb = tensor(fn, "b_scale", args[3]), given = tensor(fn, "out", args[5], true), bias = tensor(fn, "bias", args[6], true),
+         res = tensor(fn, "residual", args[8], true);
+  const int act = activation_arg(fn, args[7]);
+  same_device(fn, {&a, &sa, &b, &sb, &given, &bias, &res});
   if (a.dim() != 2 || b.dim() != 2) refuse("%s: a and b must be [M, K] and [N, K]", fn);
   const int64_t M = a.size(0), K = a.size(1), N = b.size(0), g = (K + 127) / 128, blocks = (N + 127) / 128;
   if (b.size(1) != K || K < 1) refuse("%s: a and b must share K >= 1, got %lld and %lld", fn, (long long)K, (long long)b.size(1));
@@ -129,6 +140,19 @@ PyObject* matmul(PyObject* const* args, Py_ssize_t n) {
     out = at::empty({M, N}, a.options().dtype(dtype_arg(fn, args[4])));
   } else if (out_code(out.scalar_type()) < 0 || !shape(out, {M, N}) || (N > 1 && out.stride(1) != 1)) {
     refuse("%s: out must be [%lld, %lld] bfloat16 or float16 with contiguous rows", fn, (long long)M, (long long)N);
+  }
+  if (bias.defined() || res.defined() || act != FQ_ACT_NONE) {
+    if (bias.defined() && (bias.scalar_type() != out.scalar_type() || !shape(bias, {N}) || (N > 1 && bias.stride(0) != 1)))
+      refuse("%s: bias must be contiguous [%lld] of the output's type", fn, (long long)N);
+    if (res.defined() && (res.scalar_type() != out.scalar_type() || !shape(res, {M, N}) || (N > 1 && res.stride(1) != 1)))
+      refuse("%s: residual must be [%lld, %lld] of the output's type with contiguous rows", fn, (long long)M, (long long)N);
+    launch("fq_fp8_matmul_epilogue", [&] {
+      return fq_fp8_matmul_epilogue(ptr<uint8_t>(a), a.stride(0), ptr<float>(sa), sa.stride(0), ptr<uint8_t>(b), b.stride(0),
+                                    ptr<float>(sb), sb.stride(0), out.data_ptr(), out.stride(0),
+                                    bias.defined() ? bias.data_ptr() : nullptr, act, res.defined() ? res.data_ptr() : nullptr,
+                                    res.defined() ? res.stride(0) : 0, M, N, K, out_code(out.scalar_type()), stream_of(a));
+    });
+    return THPVariable_Wrap(out);
   }
   launch("fq_fp8_matmul", [&] {
     return fq_fp8_matmul(ptr<uint8_t>(a), a.stride(0), ptr<float>(sa), sa.stride(0), ptr<uint8_t>(b), b.stride(0), ptr<float>(sb),
@@ -213,10 +237,10 @@ PyObject* append(PyObject* const* args, Py_ssize_t n) {
 
 // -------------------------------------------------------------------------------- attention
 // (q, q_scale, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, softmax_scale or None, out_dtype,
-//  max_seq_len or None, want_lse, out or None, lse or None, workspace or None) -> (out, lse or None)
+//  max_seq_len or None, want_lse, out or None, lse or None, workspace or None, window or None, sinks) -> (out, lse or None)
 PyObject* attention(PyObject* const* args, Py_ssize_t n) {
   const char* fn = "paged_attention";
-  want_args(fn, n, 15);
+  want_args(fn, n, 17);
   Tensor q = tensor(fn, "q", args[0]), qs = tensor(fn, "q_scale", args[1]), k = tensor(fn, "k_cache", args[2]),
          v = tensor(fn, "v_cache", args[3]), ks = tensor(fn, "k_scale", args[4]), vs = tensor(fn, "v_scale", args[5]),
          table = tensor(fn, "page_table", args[6]), lens = tensor(fn, "seq_lens", args[7]),
@@ -240,6 +264,8 @@ PyObject* attention(PyObject* const* args, Py_ssize_t n) {
   if (args[10] != Py_None) max_len = std::min(max_len, whole(args[10]));
   if (max_len < 0) refuse("%s: max_seq_len must be >= 0", fn);
   const double scale = args[8] == Py_None ? 1.0 / std::sqrt(static_cast<double>(D)) : real(args[8]);
+  const int64_t window = args[15] == Py_None ? INT64_MAX : whole(args[15]), sinks = whole(args[16]);
+  if (window < 1 || sinks < 0) refuse("%s: window must be >= 1 and sinks >= 0", fn);
   const int want_lse = PyObject_IsTrue(args[11]);
   if (want_lse < 0) throw Refused{};
   const c10::DeviceGuard guard(q.device());
@@ -261,12 +287,21 @@ PyObject* attention(PyObject* const* args, Py_ssize_t n) {
     bytes = fq_paged_attention_workspace_bytes(B, Hq, Hk, D, max_len);
     if (bytes > 0) ws = at::empty({static_cast<int64_t>(bytes)}, q.options().dtype(at::kByte));
   }
-  launch("fq_paged_attention", [&] {
-    return fq_paged_attention(ptr<uint8_t>(q), q.stride(0), ptr<float>(qs), qs.stride(0), &c, ptr<int32_t>(table), table.stride(0),
-                              ptr<int32_t>(lens), out.data_ptr(), lse.defined() ? ptr<float>(lse) : nullptr,
-                              ws.defined() ? ws.data_ptr() : nullptr, bytes, B, Hq, Hk, D, max_pages, max_len,
-                              static_cast<float>(scale), out_code(out.scalar_type()), stream_of(q));
-  });
+  float* const lse_at = lse.defined() ? ptr<float>(lse) : nullptr;
+  void* const ws_at = ws.defined() ? ws.data_ptr() : nullptr;
+  if (window == INT64_MAX)
+    launch("fq_paged_attention", [&] {
+      return fq_paged_attention(ptr<uint8_t>(q), q.stride(0), ptr<float>(qs), qs.stride(0), &c, ptr<int32_t>(table), table.stride(0),
+                                ptr<int32_t>(lens), out.data_ptr(), lse_at, ws_at, bytes, B, Hq, Hk, D, max_pages, max_len,
+                                static_cast<float>(scale), out_code(out.scalar_type()), stream_of(q));
+    });
+  else
+    launch("fq_paged_attention_window", [&] {
+      return fq_paged_attention_window(ptr<uint8_t>(q), q.stride(0), ptr<float>(qs), qs.stride(0), &c, ptr<int32_t>(table),
+                                       table.stride(0), ptr<int32_t>(lens), out.data_ptr(), lse_at, ws_at, bytes, B, Hq, Hk, D,
+                                       max_pages, max_len, window, sinks, static_cast<float>(scale), out_code(out.scalar_type()),
+                                       stream_of(q));
+    });
   PyObject* pair = PyTuple_New(2);
   if (pair == nullptr) throw Refused{};
   PyTuple_SET_ITEM(pair, 0, THPVariable_Wrap(out));
@@ -277,6 +312,98 @@ PyObject* attention(PyObject* const* args, Py_ssize_t n) {
     PyTuple_SET_ITEM(pair, 1, Py_None);
   }
   return pair;
+}
+
+// ----------------------------------------------------------------------------- block tables
+// A tuple of the tensors, or of None where one is undefined.
+PyObject* tuple_of(std::initializer_list<const at::Tensor*> ts) {
+  PyObject* t = PyTuple_New(static_cast<Py_ssize_t>(ts.size()));
+  if (t == nullptr) throw Refused{};
+  Py_ssize_t i = 0;
+  for (const at::Tensor* x : ts) {
+    PyObject* o = Py_None;
+    if (x->defined()) o = THPVariable_Wrap(*x);
+    else Py_INCREF(o);
+    PyTuple_SET_ITEM(t, i++, o);
+  }
+  return t;
+}
+
+// The given tensor, checked to be a contiguous `t` of `n` elements, or a new one.
+at::Tensor vector_or_new(const char* fn, const char* name, Tensor given, int64_t n, at::ScalarType t, Tensor like) {
+  if (!given.defined()) return at::empty({n}, like.options().dtype(t));
+  if (given.scalar_type() != t || !shape(given, {n}) || !given.is_contiguous())
+    refuse("%s: %s must be contiguous %s [%lld]", fn, name, c10::toString(t), (long long)n);
+  return given;
+}
+
+void need_vector(const char* fn, const char* name, Tensor x, int64_t n, at::ScalarType t) {
+  if (x.defined()) vector_or_new(fn, name, x, n, t, x);
+}
+
+// (page_table, seq_lens, new_lens, free_pages, pool, page_size, max_tokens, slots or None, positions or None, starts or
+//  None, seq_lens_out or None, pool_out or None) -> (slots, positions, starts, seq_lens_out, pool_out)
+PyObject* extend(PyObject* const* args, Py_ssize_t n) {
+  const char* fn = "paged_extend";
+  want_args(fn, n, 12);
+  Tensor table = tensor(fn, "page_table", args[0]), lens = tensor(fn, "seq_lens", args[1]), added = tensor(fn, "new_lens", args[2]),
+         ring = tensor(fn, "free_pages", args[3]), pool = tensor(fn, "pool", args[4]), g_slots = tensor(fn, "slots", args[7], true),
+         g_pos = tensor(fn, "positions", args[8], true), g_starts = tensor(fn, "starts", args[9], true),
+         g_lens = tensor(fn, "seq_lens_out", args[10], true), g_pool = tensor(fn, "pool_out", args[11], true);
+  same_device(fn, {&table, &lens, &added, &ring, &pool, &g_slots, &g_pos, &g_starts, &g_lens, &g_pool});
+  const int64_t page = whole(args[5]), T = whole(args[6]);
+  if (page < 1 || T < 0) refuse("%s: page_size must be >= 1 and max_tokens >= 0", fn);
+  if (table.dim() != 2 || table.scalar_type() != at::kInt || (table.size(1) > 1 && table.stride(1) != 1))
+    refuse("%s: page_table must be int32 [B, max_pages] with contiguous rows", fn);
+  const int64_t B = table.size(0), W = table.size(1);
+  need_vector(fn, "seq_lens", lens, B, at::kInt);
+  need_vector(fn, "new_lens", added, B, at::kInt);
+  if (ring.dim() != 1 || ring.size(0) < 1) refuse("%s: free_pages must be int32 [ring], ring >= 1", fn);
+  need_vector(fn, "free_pages", ring, ring.size(0), at::kInt);
+  need_vector(fn, "pool", pool, 3, at::kInt);
+  const c10::DeviceGuard guard(table.device());
+  const at::Tensor slots = vector_or_new(fn, "slots", g_slots, T, at::kLong, table), pos = vector_or_new(fn, "positions", g_pos, T, at::kInt, table),
+                   starts = vector_or_new(fn, "starts", g_starts, B + 1, at::kInt, table),
+                   out = vector_or_new(fn, "seq_lens_out", g_lens, B, at::kInt, table), pool_out = vector_or_new(fn, "pool_out", g_pool, 3, at::kInt, table);
+  launch("fq_paged_extend", [&] {
+    return fq_paged_extend(ptr<int32_t>(table), table.stride(0), ptr<int32_t>(lens), ptr<int32_t>(added), ptr<int32_t>(ring),
+                           ring.size(0), ptr<int32_t>(pool), ptr<int32_t>(out), ptr<int32_t>(pool_out), ptr<int64_t>(slots),
+                           ptr<int32_t>(pos), ptr<int32_t>(starts), B, W, page, T, stream_of(table));
+  });
+  return tuple_of({&slots, &pos, &starts, &out, &pool_out});
+}
+
+// --------------------------------------------------------------------------------- sampling
+// (logits, u, temperature or None, top_k or None, top_p or None, min_p or None, want_logprob, token or None, logprob or
+//  None) -> (token, logprob or None)
+PyObject* sample(PyObject* const* args, Py_ssize_t n) {
+  const char* fn = "sample";
+  want_args(fn, n, 9);
+  Tensor x = tensor(fn, "logits", args[0]), u = tensor(fn, "u", args[1]), heat = tensor(fn, "temperature", args[2], true),
+         top_k = tensor(fn, "top_k", args[3], true), top_p = tensor(fn, "top_p", args[4], true), min_p = tensor(fn, "min_p", args[5], true),
+         g_token = tensor(fn, "token", args[7], true), g_logprob = tensor(fn, "logprob", args[8], true);
+  same_device(fn, {&x, &u, &heat, &top_k, &top_p, &min_p, &g_token, &g_logprob});
+  if (x.dim() != 2 || out_code(x.scalar_type()) < 0 || x.size(1) < 1 || (x.size(1) > 1 && x.stride(1) != 1))
+    refuse("%s: logits must be bfloat16 or float16 [B, V], V >= 1, with contiguous rows", fn);
+  const int64_t B = x.size(0), V = x.size(1);
+  need_vector(fn, "u", u, B, at::kFloat);
+  need_vector(fn, "temperature", heat, B, at::kFloat);
+  need_vector(fn, "top_k", top_k, B, at::kInt);
+  need_vector(fn, "top_p", top_p, B, at::kFloat);
+  need_vector(fn, "min_p", min_p, B, at::kFloat);
+  const int want = PyObject_IsTrue(args[6]);
+  if (want < 0) throw Refused{};
+  const c10::DeviceGuard guard(x.device());
+  const at::Tensor token = vector_or_new(fn, "token", g_token, B, at::kLong, x);
+  at::Tensor logprob = g_logprob;
+  if (logprob.defined() || want) logprob = vector_or_new(fn, "logprob", g_logprob, B, at::kFloat, x);
+  auto at_or_null = [](Tensor t) { return t.defined() ? static_cast<float*>(t.data_ptr()) : nullptr; };
+  launch("fq_sample", [&] {
+    return fq_sample(x.data_ptr(), x.stride(0), ptr<float>(u), at_or_null(heat), top_k.defined() ? ptr<int32_t>(top_k) : nullptr,
+                     at_or_null(top_p), at_or_null(min_p), ptr<int64_t>(token), at_or_null(logprob), B, V,
+                     out_code(x.scalar_type()), stream_of(x));
+  });
+  return tuple_of({&token, &logprob});
 }
 
 // No C++ exception leaves the module: a refusal has set its Python error, torch's own become theirs.
@@ -300,7 +427,8 @@ PyObject* set_error_class(PyObject*, PyObject* cls) {
 
 #define FQ_METHOD(name, f) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(guarded<f>)), METH_FASTCALL, nullptr}
 PyMethodDef g_methods[] = {FQ_METHOD("fp8_matmul", matmul), FQ_METHOD("qkv_norm_rope_append", append),
-                           FQ_METHOD("paged_attention", attention), {"set_error_class", set_error_class, METH_O, nullptr},
+                           FQ_METHOD("paged_attention", attention), FQ_METHOD("paged_extend", extend), FQ_METHOD("sample", sample),
+                           {"set_error_class", set_error_class, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fq_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

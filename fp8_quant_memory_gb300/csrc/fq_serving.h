@@ -1,5 +1,6 @@
-// fq_serving.h -- host-side launch interface of the FP8 serving operators: the block-scaled matrix
-// product, the QKV prologue that appends to a paged cache, and paged attention of one new token.
+// fq_serving.h -- host-side launch interface of the serving operators: the block-scaled FP8 matrix
+// product, the QKV prologue that appends to a paged cache, paged attention of one new token, block tables and
+// slot maps, and sampling.
 #pragma once
 
 #include "fq_internal.h"
@@ -18,6 +19,13 @@ struct MatmulArgs {
   void* out;
   int64_t a_stride, b_stride, a_scale_stride, b_scale_stride, out_stride;
   int64_t M, N, K, groups;
+  // the epilogue: out = dtype(activation(product + bias) + residual)
+  const void* bias;      // nullable, [N] dtype
+  const void* residual;  // nullable, [M, N] dtype
+  int64_t residual_stride;
+  int activation;  // fq_activation
+
+  bool fused() const { return bias != nullptr || residual != nullptr || activation != 0; }
 };
 
 // The cache as the kernels see it: row (page, head, slot) of K starts at k + page*page_stride +
@@ -55,6 +63,36 @@ struct PagedArgs {
   int32_t B, Hq, Hk, D;
   int32_t max_len;  // lengths are cut to this (the caller's bound and what the page table holds)
   float scale_log2;  // softmax_scale * log2(e)
+  // token j of a sequence of len is visible if j < sinks or j >= len - window; at most max_len each
+  int32_t window, sinks;
+};
+
+struct ExtendArgs {
+  int32_t* table;
+  int64_t table_stride;
+  const int32_t* lens;
+  const int32_t* added;
+  int32_t* ring;
+  const int32_t* pool;
+  int32_t* lens_out;
+  int32_t* pool_out;
+  int64_t* slots;
+  int32_t* positions;
+  int32_t* starts;
+  int32_t B, width, page_size, tokens, places;  // places: the ring's
+};
+
+struct SampleArgs {
+  const uint16_t* logits;
+  int64_t stride;
+  const float* u;
+  const float* temperature;  // nullable, as the next three
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int64_t* token;
+  float* logprob;  // nullable
+  int32_t B, V;
 };
 
 // Launches `kern` so that its set-up overlaps the tail of the previous kernel in the stream (it calls pdl_wait before
@@ -98,6 +136,10 @@ void launch_append_scalar(const AppendArgs& a, int dtype, int table_dtype, cudaS
 size_t attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len);
 bool launch_attention_split(const PagedArgs& a, int dtype, cudaStream_t s);
 void launch_attention_scalar(const PagedArgs& a, int dtype, cudaStream_t s);
+
+constexpr int kMaxExtend = 16384;  // sequences of one call: three counts of each lie in shared memory
+bool launch_extend(const ExtendArgs& a, cudaStream_t s);
+bool launch_sample(const SampleArgs& a, int dtype, cudaStream_t s);
 
 // Launch result of an entry point (and the strict-mode check), as every entry point reports it.
 int finish_launch(const char* fn, cudaStream_t s);

@@ -5,6 +5,7 @@
 #include <math_constants.h>
 
 #include "fq_device.cuh"
+#include "fq_epilogue.cuh"
 #include "fq_serving.h"
 
 namespace fq {
@@ -46,6 +47,9 @@ __global__ void __launch_bounds__(kThreads) matmul_scalar_kernel(const MatmulArg
       const float sc = __fmul_rn(a.a_scale[i * a.a_scale_stride + g], a.b_scale[j / kScaleBlock * a.b_scale_stride + g]);
       acc = __fmaf_rn(s, sc, acc);
     }
+    if (a.bias != nullptr) acc = __fadd_rn(acc, ld_any(dt, a.bias, j));
+    acc = activate(a.activation, acc);
+    if (a.residual != nullptr) acc = __fadd_rn(acc, ld_any(dt, a.residual, i * a.residual_stride + j));
     st_any(dt, a.out, i * a.out_stride + j, acc);
   }
 }
@@ -128,7 +132,10 @@ __global__ void __launch_bounds__(kThreads) attention_scalar_kernel(const PagedA
     o[i] = 0.f;
   }
   float m = -CUDART_MAX_NORMAL_F, l = 0.f;
-  for (int64_t t = warp; t < len; t += kWarps) {
+  // the visible tokens: [0, sunk) and [start, len)
+  const int64_t start = max(len - a.window, static_cast<int64_t>(0)), sunk = min(static_cast<int64_t>(a.sinks), start);
+  for (int64_t v = warp; v < len - start + sunk; v += kWarps) {
+    const int64_t t = v < sunk ? v : v - sunk + start;
     const int64_t at = t / c.page_size, off = t - at * c.page_size;
     const int64_t page = a.table[b * a.table_stride + at];
     if (page < 0 || page >= c.pages) continue;  // absent page: its tokens take no part

@@ -1,5 +1,6 @@
-"""Bindings of the FP8 serving operators (include/fq.h): the block-scaled FP8 matrix product, the QKV
-prologue that appends to a paged FP8 cache, and paged attention of one new token.
+"""Bindings of the serving operators (include/fq.h): the block-scaled FP8 matrix product (with an epilogue), the QKV
+prologue that appends to a paged FP8 cache, paged attention of one new token (of everything, or of a sliding window with
+sinks), the block tables and slot maps of a step, and the sampling of its tokens.
 
 A cache is four tensors: ``k_cache``, ``v_cache`` [pages, Hk, page_size, D] of e4m3 codes and
 ``k_scale``, ``v_scale`` [pages, Hk, page_size] fp32, one scale per row. Any strides that keep rows
@@ -44,14 +45,17 @@ def _load():
 
 
 def fp8_matmul(a: torch.Tensor, a_scale: torch.Tensor, b: torch.Tensor, b_scale: torch.Tensor,
-               out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
-    """out = dtype(a @ b.T) of block-scaled e4m3 operands.
+               out_dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+               activation: str | None = None, residual: torch.Tensor | None = None) -> torch.Tensor:
+    """out = dtype(activation(a @ b.T + bias) + residual) of block-scaled e4m3 operands.
 
     a: [M, K] codes with a_scale [M, ceil(K/128)] (what rmsnorm_rope_quant_groups(group_size=128) returns);
     b: [N, K] codes with b_scale [ceil(N/128), ceil(K/128)], one scale per 128 x 128 block of the weight.
-    Returns [M, N] bfloat16 or float16, every sum in fp32 and rounded once.
+    bias: [N] and residual: [M, N] (any row stride, 0 too; it may be ``out`` itself) of the output's type; activation:
+    None, "relu", "gelu" (erf), "gelu_tanh" or "silu".
+    Returns [M, N] bfloat16 or float16, every sum and the epilogue in fp32, rounded once.
     """
-    return (_native or _load()).fp8_matmul(a, a_scale, b, b_scale, out_dtype, out)
+    return (_native or _load()).fp8_matmul(a, a_scale, b, b_scale, out_dtype, out, bias, activation, residual)
 
 
 def qkv_norm_rope_append(qkv: torch.Tensor, wq: torch.Tensor, wk: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor,
@@ -79,7 +83,8 @@ def paged_attention(q: torch.Tensor, q_scale: torch.Tensor, k_cache: torch.Tenso
                     k_scale: torch.Tensor, v_scale: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
                     softmax_scale: float | None = None, out_dtype: torch.dtype = torch.bfloat16,
                     max_seq_len: int | None = None, want_lse: bool = False, out: torch.Tensor | None = None,
-                    lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+                    lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, window: int | None = None,
+                    sinks: int = 0):
     """Attention of one new token per sequence over the paged FP8 cache. Returns (out, lse or None).
 
     q: [B, Hq, D] codes (rows of a sequence contiguous, any stride between sequences) with q_scale
@@ -87,6 +92,39 @@ def paged_attention(q: torch.Tensor, q_scale: torch.Tensor, k_cache: torch.Tenso
     max_seq_len: an upper bound of the lengths known on the host (default: what the page table holds);
     longer sequences are cut to it. out: [B, Hq, D]; lse: fp32 [B, Hq]. A workspace that is passed
     (uint8) must not be in use by another call that may run at the same time.
+    window: only the last ``window`` tokens of a sequence take part, and the first ``sinks`` (None: all of them).
     """
     return (_native or _load()).paged_attention(q, q_scale, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens,
-                                                softmax_scale, out_dtype, max_seq_len, want_lse, out, lse, workspace)
+                                                softmax_scale, out_dtype, max_seq_len, want_lse, out, lse, workspace, window,
+                                                sinks)
+
+
+def paged_extend(page_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: torch.Tensor, free_pages: torch.Tensor,
+                 pool: torch.Tensor, page_size: int, max_tokens: int, slots: torch.Tensor | None = None,
+                 positions: torch.Tensor | None = None, starts: torch.Tensor | None = None,
+                 seq_lens_out: torch.Tensor | None = None, pool_out: torch.Tensor | None = None):
+    """Block tables and slot maps of a step: adds new_lens[b] tokens to each sequence of seq_lens[b], or ends it (< 0).
+
+    page_table: [B, max_pages], seq_lens and new_lens: [B], free_pages: [ring], a ring of the ids of free pages, pool:
+    [3] = its front, how many are free, (not read); all int32. New pages come from the ring's front and enter page_table;
+    those of sequences that end go behind its last. Sequences whose tokens fit neither the table, nor max_tokens, nor the
+    free pages are left as they are (include/fq.h has the rule).
+    Returns (slots int64 [max_tokens], positions int32 [max_tokens], starts int32 [B + 1], seq_lens_out, pool_out): what
+    qkv_norm_rope_append and paged_attention take, slots of -1 behind the last token. pool_out[2] counts the pages that
+    were asked for and not there. seq_lens_out and pool_out may be seq_lens and pool: a captured step then advances.
+    """
+    return (_native or _load()).paged_extend(page_table, seq_lens, new_lens, free_pages, pool, page_size, max_tokens, slots,
+                                             positions, starts, seq_lens_out, pool_out)
+
+
+def sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor | None = None, top_k: torch.Tensor | None = None,
+           top_p: torch.Tensor | None = None, min_p: torch.Tensor | None = None, want_logprob: bool = False,
+           token: torch.Tensor | None = None, logprob: torch.Tensor | None = None):
+    """The next token of each row of logits [B, V] (bfloat16 or float16), from uniform numbers u in [0, 1).
+
+    temperature, top_p, min_p: fp32 [B], top_k: int32 [B], each row its own; None leaves a step out. The cuts apply in the
+    order top-k, top-p, min-p to the tokens by falling logit (equal ones by rising index); u picks along that order.
+    temperature 0 takes the largest. Returns (token int64 [B], logprob fp32 [B] of the token among those kept, or None);
+    -1 for a row whose mask (-inf) leaves nothing.
+    """
+    return (_native or _load()).sample(logits, u, temperature, top_k, top_p, min_p, want_logprob, token, logprob)

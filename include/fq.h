@@ -262,9 +262,10 @@ int fq_rmsnorm_bwd_noalloc(const void* x, const void* w, const void* grad_y, voi
                            float* dw_f32, int64_t M, int64_t N, int dtype, float eps, cudaStream_t stream);
 
 /* ------------------------------------------------------------------------------------------------
- * FP8 serving operators: what reads the FP8 rows that the entry points above write. The tutorial
- * pages end at the prologue; these three carry it on: the projection in front of it, the prologue with
- * its K and V rows placed in a paged cache, and the attention of one new token over that cache.
+ * Serving operators: what reads the FP8 rows that the entry points above write. The tutorial
+ * pages end at the prologue; these carry it on: the projection in front of it (with an epilogue for the other
+ * projections of a block), the prologue with its K and V rows placed in a paged cache, the attention of one new token
+ * over that cache (whole, or a window of it), the block tables and slots of a step, and the sampling of its tokens.
  * ------------------------------------------------------------------------------------------------ */
 
 /*
@@ -282,6 +283,29 @@ int fq_rmsnorm_bwd_noalloc(const void* x, const void* w, const void* grad_y, voi
 int fq_fp8_matmul(const uint8_t* a, int64_t a_stride, const float* a_scale, int64_t a_scale_stride, const uint8_t* b,
                   int64_t b_stride, const float* b_scale, int64_t b_scale_stride, void* out, int64_t out_stride,
                   int64_t M, int64_t N, int64_t K, int dtype, cudaStream_t stream);
+
+/* Activations of fq_fp8_matmul_epilogue. */
+enum fq_activation {
+  FQ_ACT_NONE = 0,
+  FQ_ACT_RELU = 1,      /* max(y, 0) */
+  FQ_ACT_GELU = 2,      /* y * (1 + erf(y / sqrt(2))) / 2 */
+  FQ_ACT_GELU_TANH = 3, /* y * (1 + tanh(sqrt(2 / pi) * (y + 0.044715 y^3))) / 2 */
+  FQ_ACT_SILU = 4       /* y / (1 + exp(-y)) */
+};
+
+/*
+ * fq_fp8_matmul with bias, activation and residual in its epilogue:
+ *   out[i, j] = dtype( activation( P[i, j] + bias[j] ) + residual[i, j] )
+ * where P is fq_fp8_matmul's fp32 product before its rounding; every step in fp32, one rounding to dtype. bias: [N] dtype
+ * or null; residual: [M, N] dtype or null, rows residual_stride >= 0 elements apart (0: one row for all). The residual
+ * may be the output itself (the same pointer and stride: out += activation(...)); otherwise they must not overlap.
+ * activation: an fq_activation (else FQ_ERR_UNSUPPORTED). Without any of the three the result is fq_fp8_matmul's, bit for
+ * bit. Other arguments and errors as fq_fp8_matmul.
+ */
+int fq_fp8_matmul_epilogue(const uint8_t* a, int64_t a_stride, const float* a_scale, int64_t a_scale_stride,
+                           const uint8_t* b, int64_t b_stride, const float* b_scale, int64_t b_scale_stride, void* out,
+                           int64_t out_stride, const void* bias, int activation, const void* residual,
+                           int64_t residual_stride, int64_t M, int64_t N, int64_t K, int dtype, cudaStream_t stream);
 
 /*
  * Diagnostic, host only: the kernel that fq_fp8_matmul takes for aligned operands on a GPU of `sms` SMs (152 on GB300).
@@ -359,6 +383,70 @@ int fq_paged_attention(const uint8_t* q, int64_t q_stride, const float* q_scale,
                        const int32_t* seq_lens, void* out, float* lse, void* workspace, size_t workspace_bytes,
                        int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t max_pages, int64_t max_seq_len,
                        float softmax_scale, int dtype, cudaStream_t stream);
+
+/*
+ * fq_paged_attention of a sliding window with sinks: of a sequence of len_b tokens only those with
+ *   j < sinks   or   j >= len_b - window
+ * take part (window >= 1, sinks >= 0; a window of at least max_seq_len sees every token, and the call is then
+ * fq_paged_attention's, bit for bit). Pages in between are not read; their table entries may be anything. Other
+ * arguments, workspace and errors as fq_paged_attention.
+ */
+int fq_paged_attention_window(const uint8_t* q, int64_t q_stride, const float* q_scale, int64_t q_scale_stride,
+                              const fq_paged_cache* cache, const int32_t* page_table, int64_t table_stride,
+                              const int32_t* seq_lens, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                              int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t max_pages, int64_t max_seq_len,
+                              int64_t window, int64_t sinks, float softmax_scale, int dtype, cudaStream_t stream);
+
+/*
+ * Block tables and slot maps of one step, from the requests' lengths: what fq_qkv_norm_rope_append and
+ * fq_paged_attention take, built on the device. B sequences; sequence b holds seq_lens[b] tokens (a negative length
+ * counts as 0) in pages page_table[b*table_stride + 0..ceil(len/page_size)-1], and this step
+ *   new_lens[b] >= 0: adds that many tokens to it;   new_lens[b] < 0: ends it and returns its pages.
+ * Free pages wait in a ring of `ring` ids: free_pages[(pool[0] + i) % ring], i < pool[1]. For b in order:
+ *   - The tokens of sequence b are starts[b]..starts[b+1]-1 of the step's, starts being the running sum of the
+ *     positive new_lens. (starts: [B + 1]; sums above 2^31 - 1 stay there.)
+ *   - It is granted its tokens if they fit the table (ceil((len+new)/page_size) <= max_pages) and the step
+ *     (starts[b+1] <= max_tokens), and the pages it needs are left: those that it and the sequences before it need
+ *     (of the ones that fit) are pool[1] at most, or it needs none.
+ *   - Granted: its new pages, next from the ring's front, enter its row of the table; seq_lens_out[b] = len + new.
+ *     Not granted: row and length stay as they are. Ended: its pages (those below max_pages) go behind the ring's
+ *     last, to be given out from the next step on, in order; seq_lens_out[b] = 0; its row stays as it is.
+ *   - Token i of it is at position len + i: positions[starts[b] + i] (at most 2^31 - 1), slots[starts[b] + i] =
+ *     page * page_size + position % page_size, or -1 where it is not granted or that page's id is negative.
+ *   - Behind the last sequence's tokens, up to max_tokens: slot -1, position 0.
+ * pool_out: {ring's new front, free pages, pages that sequences which were not granted theirs had asked for}.
+ * pool[0] counts modulo `ring`, pool[1] within [0, ring]; pages returned to a full ring are dropped. pool[2] is not
+ * read. seq_lens_out and pool_out may be seq_lens and pool (a graph that is replayed then advances); otherwise outputs
+ * overlap nothing. slots: [max_tokens] int64; positions: [max_tokens] int32. table_stride >= max_pages.
+ * B <= 16384 (else FQ_ERR_UNSUPPORTED), ring >= 1, page_size >= 1, max_pages * page_size < 2^31. B = 0 and
+ * max_tokens = 0 are allowed.
+ */
+int fq_paged_extend(int32_t* page_table, int64_t table_stride, const int32_t* seq_lens, const int32_t* new_lens,
+                    int32_t* free_pages, int64_t ring, const int32_t* pool, int32_t* seq_lens_out, int32_t* pool_out,
+                    int64_t* slots, int32_t* positions, int32_t* starts, int64_t B, int64_t max_pages, int64_t page_size,
+                    int64_t max_tokens, cudaStream_t stream);
+
+/*
+ * The next token of each row of logits, from given uniform numbers. With x the row's V logits, T its temperature, and
+ * the row's tokens in the order of falling x (equal ones by rising index), w_i = exp((x_i - max x) / T):
+ *   top-k: the first top_k tokens of the order stay (top_k <= 0 or >= V: all);
+ *   top-p: of these, those before which the sum of w is below top_p times the sum over them all, and the first
+ *          (top_p >= 1: all);
+ *   min-p: of these, those with w >= min_p (and the first);
+ *   token: the first of these in the order up to and with which the sum of w exceeds u times the sum over these;
+ *   logprob = log(w of the token / that sum).
+ * A temperature that is not at least 2^-126 gives the first token of the order, logprob 0. u is cut to [0, 1 - 2^-24].
+ * A NaN counts as -inf. -inf takes no part; a row of nothing else gives token -1 and logprob -inf. Where +inf
+ * occurs, it alone counts. A NaN among the parameters switches its step off (temperature: as 0; u: as 0).
+ * Sums are exact sums of weights that are right to 2^-40 of themselves or 2^-62 of the largest, and the borders exact
+ * products of them, so that a result is that of 64-bit arithmetic but for borders met to about 2^-40 of the sum.
+ * logits: [B, V] dtype, rows `stride` >= 0 elements apart; u, temperature, top_p, min_p: [B] fp32, top_k: [B] int32; each
+ * of the last four may be null (T = 1, no cut). token: [B] int64; logprob: [B] fp32 or null. B >= 0 (0: no-op),
+ * 1 <= V < 2^31 - 1024. Any alignment and stride; the same call gives the same tokens on every GPU and run.
+ */
+int fq_sample(const void* logits, int64_t stride, const float* u, const float* temperature, const int32_t* top_k,
+              const float* top_p, const float* min_p, int64_t* token, float* logprob, int64_t B, int64_t V, int dtype,
+              cudaStream_t stream);
 
 #ifdef __cplusplus
 }

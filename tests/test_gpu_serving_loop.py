@@ -1,0 +1,470 @@
+"""GPU parity of the serving loop's operators against plain implementations (serving_loop_ref.py): block tables and slot
+maps, paged attention of a window with sinks, the FP8 product with an epilogue, sampling; and a run of them together."""
+import math
+import random
+
+import pytest
+import torch
+
+import fp8_quant_memory_gb300 as fq
+import serving_loop_ref as ref
+import serving_ref
+from guards import Guarded
+from test_gpu_serving import DT, attention_inputs, gen, matmul_inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _device_state(cuda_ok):
+    yield
+    torch.cuda.synchronize()
+    assert fq.device_status(clear=True) == 0
+
+
+def ints(v, t=torch.int32):
+    return torch.tensor(v, dtype=t, device="cuda")
+
+
+# ---------------------------------------------------------------------------------- block tables
+def make_step(B, W, page, ring, count, seed, ends=0.1, most=None):
+    """A consistent state: sequences with pages of their own, free ones in a ring, and what each sequence adds."""
+    r = random.Random(seed)
+    lens = [r.choice([0, 1, page, r.randrange(W * page + 1)]) for _ in range(B)]
+    new = [-1 if r.random() < ends else r.choice([0, 1, 1, 1, r.randrange(most or 2 * page + 2)]) for _ in range(B)]
+    owned = [ref.ceil(n, page) for n in lens]
+    ids = list(range(sum(owned) + count))
+    r.shuffle(ids)
+    table, at = [], 0
+    for n in owned:
+        table.append(ids[at:at + n] + [-1] * (W - n))
+        at += n
+    head = r.randrange(ring)
+    places = [-1] * ring
+    for i, id in enumerate(ids[at:]):
+        places[(head + i) % ring] = id
+    return table, lens, new, places, [head, count, 77]
+
+
+def check_extend(table, lens, new, ring, pool, page, T, in_place=False, pad=0):
+    want = ref.extend(table, lens, new, ring, pool, page, T)
+    B = len(lens)
+    W = len(table[0]) if B else 0
+    big = torch.full((B, W + pad), -5, dtype=torch.int32, device="cuda")
+    if B and W:
+        big[:, :W] = ints(table)
+    t, ln, nw, rg, pl = big[:, :W], ints(lens), ints(new), Guarded((len(ring),), torch.int32), ints(pool)
+    rg.t.copy_(ints(ring))
+    out = dict(slots=Guarded((T,), torch.int64, fill=9), positions=Guarded((T,), torch.int32, fill=9), starts=Guarded((B + 1,), torch.int32, fill=9))
+    given = {k: g.t for k, g in out.items()}
+    if in_place:
+        given.update(seq_lens_out=ln, pool_out=pl)
+    slots, positions, starts, lens_out, pool_out = fq.paged_extend(t, ln, nw, rg.t, pl, page, T, **given)
+    for g in [rg, *out.values()]:
+        g.check()
+    got = dict(slots=slots, positions=positions, starts=starts, seq_lens=lens_out, pool=pool_out, table=t, ring=rg.t)
+    for k, v in got.items():
+        assert v.tolist() == want[k], k
+    assert bool((big[:, W:] == -5).all())
+    if not in_place:
+        assert ln.tolist() == lens and pl.tolist() == pool
+    return want
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("B,W,page,T", [(1, 1, 1, 1), (1, 4, 16, 40), (3, 5, 7, 33), (17, 9, 16, 300), (64, 20, 64, 900), (100, 3, 1, 120),
+                                        (1000, 6, 24, 3000), (1024, 4, 8, 8192), (1025, 4, 8, 20000), (5000, 3, 16, 9000)])
+def test_extend(B, W, page, T, in_place):
+    state = make_step(B, W, page, ring=B * W + 5, count=B * W // 2 + 3, seed=B + T)
+    check_extend(*state, page, T, in_place=in_place)
+
+
+@pytest.mark.parametrize("count", [0, 1, 3, 10, 11, 12, 40])
+def test_extend_without_enough_pages(count):
+    """The first sequences get theirs, later ones that need none too, nothing else changes."""
+    want = check_extend(*make_step(60, 8, 4, ring=400, count=count, seed=count, ends=0.05, most=12), 4, 500)
+    assert (want["pool"][2] > 0) == (count < 40)
+
+
+@pytest.mark.parametrize("T", [0, 1, 10, 57])
+def test_extend_without_enough_places(T):
+    """Sequences whose tokens pass the step's last are not granted them; starts say so."""
+    want = check_extend(*make_step(50, 8, 4, ring=400, count=300, seed=T, most=12), 4, T, pad=3)
+    assert want["starts"][-1] > T
+
+
+def test_extend_table_too_narrow():
+    table, lens, new, ring, pool = make_step(40, 4, 8, ring=300, count=200, seed=3, most=40)
+    want = check_extend(table, lens, new, ring, pool, 8, 900)
+    assert any(m > 0 and o == n for n, m, o in zip(lens, new, want["seq_lens"]))
+
+
+def test_extend_ring_goes_round():
+    """Steps in a row in a ring of exactly as many places as pages; every page is somewhere once all along."""
+    r = random.Random(8)
+    page, B, W, pages = 4, 12, 10, 60
+    table, lens, ring, pool = [[-1] * W for _ in range(B)], [0] * B, list(range(pages)), [0, pages, 0]
+    for step in range(40):
+        new = [-1 if lens[b] and r.random() < 0.15 else r.choice([0, 1, 1, 5, 9]) for b in range(B)]
+        w = check_extend(table, lens, new, ring, pool, page, 200, in_place=step % 2 == 0)
+        table, lens, ring, pool = w["table"], w["seq_lens"], w["ring"], w["pool"]
+        held = [id for b in range(B) for id in table[b][:ref.ceil(lens[b], page)]]
+        free = [ring[(pool[0] + i) % pages] for i in range(pool[1])]
+        assert sorted(held + free) == list(range(pages))
+
+
+def test_extend_empty_and_odd_states():
+    check_extend([], [], [], [3, 4], [1, 2, 0], 16, 5)
+    check_extend([], [], [], [3], [0, 0, 0], 16, 0)
+    check_extend([[], []], [0, 0], [0, 1], [3], [0, 1, 0], 16, 4)  # a table without columns
+    check_extend([[1, 2], [-1, -1]], [-9, 0], [3, -2 ** 31], [5, 6, 7], [-1, 9, 0], 2, 4)  # a negative length, front and count out of range
+    check_extend([[-1, -1], [4, -1]], [2, 3], [1, 1], [5, 6, 7], [2, 3, 0], 2, 4)  # an absent page in the row
+    check_extend([[0, 1]], [4], [-1], [5, 6, 7], [1, 2, 0], 2, 4)  # two pages return, the ring has one place
+    big = 2 ** 31 - 1
+    check_extend([[0, 1], [2, 3]], [big, big], [big, big], [5, 6], [0, 2, 0], 3, 4)  # lengths and sums at the end of 32 bits
+    check_extend([[0, 1], [2, 3]], [big, 2], [-1, 1], [5, 6, 7, 8], [3, 1, 0], 3, 4)
+
+
+def test_extend_captured_step_advances():
+    table, lens, new, ring, pool = make_step(30, 12, 4, ring=400, count=200, seed=4, ends=0.0, most=3)
+    lens = [min(n, 8) for n in lens]
+    t, ln, nw, rg, pl = ints(table), ints(lens), ints(new), ints(ring), ints(pool)
+    side = torch.cuda.Stream()
+    keep = [x.clone() for x in (t, ln, rg, pl)]
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        fq.paged_extend(t, ln, nw, rg, pl, 4, 64, seq_lens_out=ln, pool_out=pl)
+    torch.cuda.current_stream().wait_stream(side)
+    for x, y in zip((t, ln, rg, pl), keep):
+        x.copy_(y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = fq.paged_extend(t, ln, nw, rg, pl, 4, 64, seq_lens_out=ln, pool_out=pl)
+    for step in range(4):
+        if step == 2:
+            new = [-1 if b % 3 == 0 else 2 for b in range(30)]
+            nw.copy_(ints(new))
+        graph.replay()
+        w = ref.extend(table, lens, new, ring, pool, 4, 64)
+        assert out[0].tolist() == w["slots"] and ln.tolist() == w["seq_lens"] and t.tolist() == w["table"] and rg.tolist() == w["ring"]
+        table, lens, ring, pool = w["table"], w["seq_lens"], w["ring"], w["pool"]
+        assert pl.tolist() == pool
+
+
+# -------------------------------------------------------------------------------------- attention
+def check_window(x, window, sinks, scale=None, max_len=None, dt="bf16"):
+    B, Hq, D = x[0].shape
+    out, lse = Guarded((B, Hq, D), DT[dt], fill=math.nan), Guarded((B, Hq), torch.float32, fill=math.nan)
+    fq.paged_attention(*x, softmax_scale=scale, max_seq_len=max_len, window=window, sinks=sinks, out=out.t, lse=lse.t)
+    out.check()
+    lse.check()
+    seen = ref.windowed(*x, window, sinks, max_len)
+    serving_ref.assert_attention(out.t, lse.t, *seen, D ** -0.5 if scale is None else scale)
+
+
+WINDOWS = [(1, 0), (1, 1), (2, 5), (15, 0), (16, 16), (17, 3), (100, 0), (100, 64), (128, 128), (129, 1), (300, 7), (1000, 200), (10 ** 9, 3)]
+LENS = [0, 1, 2, 15, 16, 17, 33, 100, 128, 129, 255, 256, 300, 511, 777, 1300, 2111]
+
+
+@pytest.mark.parametrize("window,sinks", WINDOWS)
+@pytest.mark.parametrize("Hq,Hk,D,page,dt", [(8, 2, 128, 16, "bf16"), (4, 4, 64, 24, "fp16"), (32, 2, 256, 32, "bf16"), (6, 1, 192, 8, "fp16"),
+                                             (5, 1, 96, 7, "bf16"), (4, 2, 100, 16, "bf16"), (16, 2, 64, 128, "bf16")])
+def test_window(window, sinks, Hq, Hk, D, page, dt):
+    check_window(attention_inputs(LENS, Hq, Hk, D, page, seed=window % 1000 + sinks), window, sinks, dt=dt)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (50, 4), (2000, 0), (4096, 64), (4097, 129)])
+def test_window_of_a_long_sequence(window, sinks):
+    check_window(attention_inputs([20011], 16, 2, 128, 16, seed=sinks), window, sinks)
+    check_window(attention_inputs([20011, 5], 4, 2, 64, 12, seed=sinks), window, sinks)
+
+
+def test_window_that_sees_everything_is_the_whole_attention():
+    x = attention_inputs([1000, 20, 0, 333], 8, 2, 128, 16, seed=3)
+    whole = fq.paged_attention(*x, want_lse=True)
+    most = x[6].shape[1] * 16
+    for window, sinks in ((most, 0), (most + 5, 9), (2 ** 62, 2 ** 62)):
+        got = fq.paged_attention(*x, want_lse=True, window=window, sinks=sinks)
+        assert torch.equal(whole[0], got[0]) and torch.equal(whole[1], got[1])
+
+
+@pytest.mark.parametrize("window,sinks", [(10, 2), (40, 0), (5, 33), (200, 17)])
+def test_window_lengths_are_cut(window, sinks):
+    x = attention_inputs([300, 280, 31], 8, 2, 128, 16, seed=63)
+    check_window(x, window, sinks, max_len=200)
+    check_window(x, window, sinks, max_len=0)
+    x[7] = torch.tensor([10 ** 9, 2 ** 31 - 1, -4], dtype=torch.int32, device="cuda")
+    check_window(x, window, sinks)
+
+
+@pytest.mark.parametrize("page,D", [(16, 128), (24, 64), (5, 100)])
+@pytest.mark.parametrize("offset", [0, 5])
+def test_window_absent_and_unread_pages(offset, page, D):
+    """Absent pages inside the window and among the sinks, a row whose window has none left; pages in between may be
+    anything: their ids are out of range or name a page of NaN."""
+    x = attention_inputs([600, 580, 60, 900], 8, 2, D, page, seed=64, offset=offset)
+    table, window, sinks = x[6], 200, 2 * page + 1
+    table[0, 1], table[0, (600 - 90) // page], table[1, 0] = -1, 10 ** 6, x[2].shape[0]
+    table[2, :] = -7
+    nan = int(table[3, 11])
+    x[2][nan], x[3][nan], x[4][nan], x[5][nan] = 0x7F, 0x7F, math.nan, math.nan
+    for b, n in ((0, 600), (1, 580), (3, 900)):
+        table[b, sinks // page + 1:(n - window) // page] = nan if b == 3 else 2 ** 31 - 1
+    check_window(x, window, sinks)
+    table[0, (600 - 7) // page:] = -1
+    check_window(x, 7, 0)
+
+
+def test_window_masks_inside_boxes():
+    """NaN rows right before the window's first token and behind the last sink change nothing."""
+    x = attention_inputs([700], 8, 2, 128, 16, seed=9)
+    clean = fq.paged_attention(*x, window=333, sinks=21, want_lse=True)
+    for j in (21, 22, 31, 365, 366, 352):
+        page = int(x[6][0, j // 16])
+        x[2][page, :, j % 16], x[3][page, :, j % 16] = 0x7F, 0x7F
+        x[4][page, :, j % 16], x[5][page, :, j % 16] = math.nan, math.inf
+    got = fq.paged_attention(*x, window=333, sinks=21, want_lse=True)
+    assert torch.equal(clean[0], got[0]) and torch.equal(clean[1], got[1])
+
+
+def test_window_repeats_bit_for_bit_and_replays():
+    x = attention_inputs([5000, 20, 1300, 0, 2222], 32, 8, 128, 64, seed=10)
+    first = fq.paged_attention(*x, window=1000, sinks=4, want_lse=True)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        again = fq.paged_attention(*x, window=1000, sinks=4, want_lse=True)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    with torch.cuda.graph(graph):
+        out, lse = fq.paged_attention(*x, window=1000, sinks=4, want_lse=True)
+    graph.replay()
+    assert torch.equal(first[0], out) and torch.equal(first[1], lse)
+    x[7].copy_(torch.tensor([17, 5100, 900, 1001, 1004], dtype=torch.int32))
+    x[6].clamp_(min=0)
+    graph.replay()
+    want = fq.paged_attention(*x, window=1000, sinks=4, want_lse=True)
+    assert torch.equal(want[0], out) and torch.equal(want[1], lse)
+
+
+# ----------------------------------------------------------------------------------------- linear
+def linear_inputs(M, N, K, seed, dt, which):
+    a, sa, b, sb = matmul_inputs(M, N, K, seed=seed)
+    sa.mul_(2.0 ** -5 * K ** -0.5 / float(sa.mean() * sb.mean() * 2 ** 6))  # outputs of a few units
+    g = gen(seed + 1)
+    bias = torch.randn(N, generator=g).to(DT[dt]).cuda() if "b" in which else None
+    res = (2 * torch.randn(M, N, generator=g)).to(DT[dt]).cuda() if "r" in which else None
+    return (a, sa, b, sb), bias, res
+
+
+LINEAR = [
+    (1, 1, 1, "bf16", "br", "silu"), (1, 129, 16, "fp16", "b", "gelu"), (3, 257, 130, "bf16", "br", "gelu_tanh"), (1, 4096, 8192, "bf16", "br", "silu"),
+    (8, 128, 256, "fp16", "r", None), (16, 384, 4096, "bf16", "b", "relu"), (31, 100, 144, "fp16", "br", "gelu"), (33, 127, 384, "bf16", "br", "silu"),
+    (64, 1024, 512, "bf16", "br", "gelu"), (64, 4100, 6928, "bf16", "br", "gelu_tanh"), (65, 300, 640, "fp16", "", "silu"), (128, 128, 128, "bf16", "br", None),
+    (129, 129, 129, "fp16", "br", "gelu_tanh"), (333, 1111, 1968, "fp16", "br", "gelu"), (300, 2049, 128, "bf16", "br", "relu"), (512, 1000, 16, "bf16", "b", "gelu"),
+    (1025, 513, 784, "fp16", "br", "silu"), (1536, 1280, 256, "bf16", "r", "gelu_tanh"), (2500, 2296, 1040, "bf16", "br", "silu"),
+    (2500, 2303, 528, "fp16", "br", "gelu"), (300, 4096, 96, "bf16", "br", "relu"), (2048, 1, 64, "bf16", "br", "silu"),
+]
+
+
+@pytest.mark.parametrize("M,N,K,dt,which,act", LINEAR)
+def test_linear(M, N, K, dt, which, act):
+    x, bias, res = linear_inputs(M, N, K, M + N, dt, which)
+    out = Guarded((M, N), DT[dt], fill=math.nan)
+    got = fq.fp8_matmul(*x, out=out.t, bias=bias, activation=act, residual=res)
+    out.check()
+    ref.assert_epilogue(got, *x, bias, act, res)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 256, 512), (40, 520, 512), (64, 1000, 4096), (200, 300, 256), (2400, 2304, 256), (2400, 2305, 128)])
+def test_linear_in_place_strided_and_broadcast(M, N, K):
+    """The residual is the output; rows of both further apart; one residual row for all; misaligned pointers."""
+    x, bias, res = linear_inputs(M, N, K, 7, "bf16", "br")
+    buf = torch.full((M, N + 9), 7.0, dtype=torch.bfloat16, device="cuda")
+    buf[:, :N] = res
+    got = fq.fp8_matmul(*x, out=buf[:, :N], bias=bias, activation="silu", residual=buf[:, :N])
+    ref.assert_epilogue(got, *x, bias, "silu", res)
+    assert bool((buf[:, N:] == 7.0).all())
+    same = fq.fp8_matmul(*x, bias=bias, activation="silu", residual=res)
+    assert torch.equal(same, got)
+    one = fq.fp8_matmul(*x, bias=bias, residual=res[:1].expand(M, N))
+    ref.assert_epilogue(one, *x, bias, None, res[:1].expand(M, N))
+    odd = torch.zeros(N + 1, dtype=torch.bfloat16, device="cuda")
+    odd[1:] = bias
+    shifted = torch.zeros(M * N + 1, dtype=torch.bfloat16, device="cuda")
+    shifted[1:] = res.flatten()
+    assert torch.equal(fq.fp8_matmul(*x, bias=odd[1:], activation="silu", residual=shifted[1:].view(M, N)), got)
+
+
+@pytest.mark.parametrize("M", [1, 100, 600])
+@pytest.mark.parametrize("act", [None, "relu", "gelu", "gelu_tanh", "silu"])
+def test_linear_ends_of_the_range(M, act):
+    """Infinite and NaN biases, sums far out on both sides."""
+    x, _, _ = linear_inputs(M, 264, 256, 6, "bf16", "")
+    bias = torch.zeros(264, dtype=torch.bfloat16, device="cuda")
+    bias[:8] = torch.tensor([1e4, -1e4, 1e30, -1e30, -90.0, 3e38, -3e38, -60.0])
+    out = fq.fp8_matmul(*x, bias=bias, activation=act)
+    ref.assert_epilogue(out, *x, bias, act, None)
+    bias[8:10] = torch.tensor([math.inf, math.nan])
+    out = fq.fp8_matmul(*x, bias=bias, activation=act)
+    assert bool((out[:, 8] == math.inf).all()) and bool(out[:, 9].isnan().all())
+    assert not bool(out[:, :8].isnan().any()) and not bool(out[:, 10:].isnan().any())
+
+
+# ---------------------------------------------------------------------------------------- sampling
+def check_sample(x, u, heat=None, k=None, top_p=None, min_p=None, exact=True):
+    """x: [B, V] on the GPU; lists of settings. Rows whose borders are met to 2^-38 may take a neighbour."""
+    B = x.shape[0]
+    given = {n: None if v is None else torch.tensor(v, dtype=t, device="cuda")
+             for n, v, t in (("temperature", heat, torch.float32), ("top_k", k, torch.int32), ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32))}
+    us = torch.tensor(u, dtype=torch.float32, device="cuda")
+    token, logprob = Guarded((B,), torch.int64, fill=-9), Guarded((B,), torch.float32, fill=math.nan)
+    fq.sample(x, us, **given, token=token.t, logprob=logprob.t)
+    token.check()
+    logprob.check()
+    rows = {n: [d] * B if g is None else g.double().tolist() for (n, g), d in zip(given.items(), (1.0, 0, 1.0, 0.0))}
+    close = 0
+    for b in range(B):
+        t, lp, margin = ref.sample(x[b].cpu().double(), us[b].double().item(), rows["temperature"][b], int(rows["top_k"][b]), rows["top_p"][b],
+                                   rows["min_p"][b])
+        if margin < 2.0 ** -38:
+            close += 1
+            continue
+        assert int(token.t[b]) == t, (b, int(token.t[b]), t, margin)
+        got = float(logprob.t[b])
+        assert got == lp or abs(got - lp) <= 2.0 ** -20 * abs(lp) + 2.0 ** -22, (b, got, lp)
+    assert close <= (B // 20 if exact else B)
+    bare, none = fq.sample(x, us, **given)
+    assert none is None and torch.equal(bare, token.t)
+
+
+def logits(B, V, dt, seed, spread=3.0):
+    return (spread * torch.randn(B, V, generator=gen(seed))).to(DT[dt]).cuda()
+
+
+def settings(B, seed):
+    r = random.Random(seed)
+    return dict(u=[r.random() for _ in range(B)], heat=[r.choice([0.0, 0.3, 0.7, 1.0, 1.0, 1.5, 4.0]) for _ in range(B)],
+                k=[r.choice([0, -1, 1, 2, 5, 50, 1000, 10 ** 6]) for _ in range(B)], top_p=[r.choice([0.0, 0.1, 0.5, 0.9, 0.99, 1.0, 2.0]) for _ in range(B)],
+                min_p=[r.choice([0.0, 0.0, 0.01, 0.2, 1.0, 3.0]) for _ in range(B)])
+
+
+VOCABULARIES = [1, 2, 7, 8, 9, 15, 17, 31, 64, 100, 255, 1000, 4099, 8192, 32000, 50001, 65535, 65537, 151936, 200003]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("V", VOCABULARIES)
+def test_sample(V, dt):
+    B = 40 if V < 10000 else 24
+    check_sample(logits(B, V, dt, V), **settings(B, V))
+
+
+@pytest.mark.parametrize("kind", ["heat", "k", "top_p", "min_p", "none"])
+@pytest.mark.parametrize("B", [1, 2, 5, 30, 160, 400])
+def test_sample_each_setting_alone(B, kind):
+    s = settings(B, B)
+    check_sample(logits(B, 3001, "bf16", B), s["u"], **({} if kind == "none" else {kind: s[kind]}))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_sample_ties(dt):
+    """Rows of few distinct values, of one, of both zeros: the lowest index comes first."""
+    B = 60
+    x = logits(B, 5003, dt, 5, spread=1.0).round()
+    x[40:50] = 2.5
+    x[50:] = torch.where(torch.rand(10, 5003, generator=gen(1)) < 0.5, -0.0, 0.0).cuda()
+    check_sample(x, **settings(B, 5))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_sample_masks_infinities_and_nan(dt):
+    B, V = 48, 2003
+    x = logits(B, V, dt, 6)
+    low = torch.finfo(DT[dt]).min
+    g = gen(7)
+    hide = (torch.rand(B, V, generator=g) < 0.98).cuda()
+    x[:8] = x[:8].masked_fill(hide[:8], -math.inf)
+    x[8:16] = x[8:16].masked_fill(hide[8:16], low)
+    x[16:24] = x[16:24].masked_fill(hide[16:24], math.nan)
+    x[24] = -math.inf
+    x[25] = math.nan
+    x[26, ::2], x[26, 1::2] = -math.inf, -math.nan
+    x[27] = low
+    x[28] = -math.inf
+    x[28, V - 1] = low
+    x[29, 3], x[29, 700] = math.inf, math.inf
+    x[30] = math.inf
+    x[31, 0], x[31, 1:] = 1.0, -math.inf
+    x[32:] *= 100.0
+    check_sample(x, **settings(B, 7))
+
+
+@pytest.mark.parametrize("dt,heat", [("bf16", 1e38), ("bf16", 3e38), ("bf16", math.inf), ("bf16", 1e-30), ("bf16", 1.2e-38), ("bf16", 1e20), ("fp16", 2000.0), ("fp16", 3e4),
+                                     ("fp16", 1e-6), ("fp16", math.inf)])
+def test_sample_all_magnitudes(dt, heat):
+    """Values of every exponent and both signs, at temperatures that keep them all (two rounds of bins), or few."""
+    V = 60000
+    raw = torch.randint(0, 65536, (12, V), generator=gen(9), dtype=torch.int64)
+    top = 0x7F80 if dt == "bf16" else 0x7C00
+    raw = torch.where((raw & 0x7FFF) >= top, raw & 0x8000, raw)
+    x = (raw - 65536 * (raw >= 32768).long()).to(torch.int16).view(DT[dt]).cuda()
+    s = settings(12, 3)
+    s["heat"] = [heat] * 12
+    check_sample(x, **s)
+
+
+def test_sample_border_numbers():
+    """u at 0, just below 1, outside and NaN; settings that are NaN switch their step off."""
+    x = logits(9, 777, "bf16", 11)
+    nan = math.nan
+    check_sample(x[:6], [0.0, 1 - 2.0 ** -24, 1.0, 7.0, -3.0, nan])
+    s = dict(u=[0.3, 0.6, 0.9])
+    u = torch.tensor(s["u"], device="cuda")
+    three = lambda v: torch.tensor([v] * 3, device="cuda")
+    plain = fq.sample(x[:3], u)[0]
+    assert torch.equal(fq.sample(x[:3], u, top_p=three(nan), min_p=three(nan))[0], plain)
+    assert torch.equal(fq.sample(x[:3], u, temperature=three(nan))[0], x[:3].float().argmax(1))
+    assert torch.equal(fq.sample(x[:3], u, temperature=three(-1.0))[0], x[:3].float().argmax(1))
+
+
+def test_sample_strided_and_misaligned_rows():
+    big = logits(10, 5000, "bf16", 12)
+    for view in (big[:, 1:4001], big[:, 3:4], big[::2, 7:3006], big[:1].expand(6, 5000), big[:, :4000]):
+        u = torch.rand(view.shape[0], generator=gen(2)).cuda()
+        k = torch.full((view.shape[0],), 40, dtype=torch.int32, device="cuda")
+        assert torch.equal(fq.sample(view, u, top_k=k)[0], fq.sample(view.contiguous(), u, top_k=k)[0])
+        assert torch.equal(fq.sample(view, u)[0], fq.sample(view.contiguous(), u)[0])
+
+
+def test_sample_rows_beyond_32_bits():
+    x = torch.full((40000, 1 << 17), -4.0, dtype=torch.bfloat16, device="cuda")  # 10.5 GB
+    x[39999, 100001] = 20.0
+    token = fq.sample(x[39990:], torch.full((10,), 0.5, device="cuda"))[0]
+    assert int(token[9]) == 100001
+    token = fq.sample(x, torch.full((40000,), 0.5, device="cuda"), temperature=torch.zeros(40000, device="cuda"))[0]
+    assert int(token[39999]) == 100001 and int(token[39998]) == 0
+
+
+def test_sample_many_equal_values_count_beyond_16_bits():
+    x = torch.full((3, 300000), 1.0, dtype=torch.bfloat16, device="cuda")
+    x[1, 200000:] = 1.0078125
+    x[2, ::2] = 1.0078125
+    check_sample(x, [0.999, 0.7, 0.75], top_p=[0.9, 1.0, 0.8])
+
+
+def test_sample_empty_and_replayed():
+    assert fq.sample(torch.zeros(0, 7, dtype=torch.bfloat16, device="cuda"), torch.zeros(0, device="cuda"))[0].shape == (0,)
+    x, u = logits(9, 3000, "bf16", 13), torch.rand(9, generator=gen(3)).cuda()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        fq.sample(x, u, want_logprob=True)
+    torch.cuda.current_stream().wait_stream(side)
+    with torch.cuda.graph(graph):
+        out = fq.sample(x, u, want_logprob=True)
+    for seed in (14, 15):
+        x.copy_(logits(9, 3000, "bf16", seed))
+        u.copy_(torch.rand(9, generator=gen(seed)))
+        graph.replay()
+        want = fq.sample(x, u, want_logprob=True)
+        assert torch.equal(want[0], out[0]) and torch.equal(want[1], out[1])
