@@ -24,6 +24,7 @@
 #include <cmath>
 
 #include "fq_device.cuh"
+#include "fq_epilogue.cuh"
 #include "fq_serving.h"
 #include "fq_tcgen05.cuh"
 #include "fq_tensormap.h"
@@ -46,6 +47,12 @@ struct MmArgs {
   // wide: whole tiles, column ranges that each of the others is cut into, pieces of work in all; whether out has
   // a tensor map
   int32_t whole, parts, pieces, tma_store;
+  // fused epilogue (kernels with kFused): out = dtype(activation(product + bias) + residual)
+  const void* bias;      // nullable
+  const void* residual;  // nullable
+  int64_t residual_stride;
+  int32_t activation;
+  int32_t bias_vec, residual_vec;  // wide: may be read 16 bytes at a time
 };
 
 __device__ __forceinline__ uint32_t pack_out(int dtype, float2 v) {
@@ -55,6 +62,20 @@ __device__ __forceinline__ uint32_t pack_out(int dtype, float2 v) {
 __device__ __forceinline__ void store_out(int dtype, void* out, int64_t i, float v) {
   if (dtype == DT_BF16) Elem<__nv_bfloat16>::store1(out, i, v);
   else Elem<__half>::store1(out, i, v);
+}
+
+__device__ __forceinline__ float load_in(int dtype, const void* p, int64_t i) {
+  return dtype == DT_BF16 ? Elem<__nv_bfloat16>::load1(p, i) : Elem<__half>::load1(p, i);
+}
+
+__device__ __forceinline__ float2 unpack_in(int dtype, uint32_t v) {
+  return dtype == DT_BF16 ? Elem<__nv_bfloat16>::unpack(v) : Elem<__half>::unpack(v);
+}
+
+// Four at a time and not inlined: the kernels' outputs lie in registers, so that every loop over them is unrolled, and
+// erfc 128 times over is 60 KB of instructions that each launch fetches anew.
+__device__ __noinline__ float4 activate4(int act, float4 v) {
+  return make_float4(activate(act, v.x), activate(act, v.y), activate(act, v.z), activate(act, v.w));
 }
 
 // ================================================================================= narrow
@@ -93,7 +114,49 @@ struct NarrowShared {
   uint32_t tmem;
 };
 
-template <int NT, int SPLIT, int G>
+// The fused epilogue of a thread's N outputs, rows col0.. of column `row`, and their stores; r: their residuals, two in a word.
+template <int N>
+__device__ __forceinline__ void narrow_finish(const MmArgs& p, int col0, int row, float (&v)[N], const uint32_t (&r)[N / 2]) {
+  if (p.bias != nullptr && row < p.N) {
+    const float bias = load_in(p.dtype, p.bias, row);
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = __fadd_rn(v[j], bias);
+  }
+  if (p.activation != FQ_ACT_NONE) {
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+      const float4 y = activate4(p.activation, make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+      v[j] = y.x;
+      v[j + 1] = y.y;
+      v[j + 2] = y.z;
+      v[j + 3] = y.w;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < N; j += 2) {
+    const float2 x = p.residual != nullptr ? unpack_in(p.dtype, r[j / 2]) : make_float2(0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (col0 + j + e < p.M && row < p.N)
+        store_out(p.dtype, p.out, static_cast<int64_t>(col0 + j + e) * p.out_stride + row,
+                  p.residual != nullptr ? __fadd_rn(v[j + e], e == 0 ? x.x : x.y) : v[j + e]);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void narrow_residual(const MmArgs& p, int col0, int row, uint32_t (&r)[N / 2]) {
+  const uint16_t* from = static_cast<const uint16_t*>(p.residual);
+#pragma unroll
+  for (int j = 0; j < N; j += 2) {
+    r[j / 2] = 0;
+    if (from != nullptr && row < p.N) {
+      if (col0 + j < p.M) r[j / 2] = from[static_cast<int64_t>(col0 + j) * p.residual_stride + row];
+      if (col0 + j + 1 < p.M) r[j / 2] |= static_cast<uint32_t>(from[static_cast<int64_t>(col0 + j + 1) * p.residual_stride + row]) << 16;
+    }
+  }
+}
+
+template <int NT, int SPLIT, int G, bool kFused>
 __global__ void __launch_bounds__(kNarrowThreads<G>, 1)
     matmul_narrow_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
                          const __grid_constant__ MmArgs p) {
@@ -201,6 +264,13 @@ __global__ void __launch_bounds__(kNarrowThreads<G>, 1)
         next[i] = j < NT && t0 + j < p.M ? __ldg(p.sa + static_cast<int64_t>(t0 + j) * p.sa_stride + k) * b : 0.f;
       }
     };
+    // The residuals of the outputs that this thread will finish are on their way during the products, as far as there
+    // are registers for it.
+    constexpr int kOwn = NT / SPLIT;
+    constexpr bool kEarly = kFused && kOwn <= 64;
+    uint32_t residual[kFused ? kOwn / 2 : 1];
+    if constexpr (kEarly)
+      if (group == 0) narrow_residual<kOwn>(p, t0 + kOwn * rank, n0 + 32 * quarter + lane, residual);
     const int first = kb0 + group;
     if (first < kb1) fetch(first);
     int b = group, turn = 0;
@@ -269,12 +339,17 @@ __global__ void __launch_bounds__(kNarrowThreads<G>, 1)
       // its shared memory, and it adds them in rank order.
       const int row = 32 * quarter + lane;
       auto value = [&](int j) { return j & 1 ? acc[j / 2].y : acc[j / 2].x; };
-      if constexpr (SPLIT == 1) {
+      if constexpr (kFused && !kEarly) narrow_residual<kOwn>(p, t0 + kOwn * rank, n0 + row, residual);
+      if constexpr (SPLIT == 1 && kFused) {
+        float v[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) v[j] = value(j);
+        narrow_finish<NT>(p, t0, n0 + row, v, residual);
+      } else if constexpr (SPLIT == 1) {
 #pragma unroll
         for (int j = 0; j < NT; ++j)
           if (t0 + j < p.M && n0 + row < p.N) store_out(p.dtype, p.out, static_cast<int64_t>(t0 + j) * p.out_stride + n0 + row, value(j));
       } else {
-        constexpr int kOwn = NT / SPLIT;
         cluster_wait();
 #pragma unroll
         for (int r = 0; r < SPLIT; ++r)
@@ -289,14 +364,17 @@ __global__ void __launch_bounds__(kNarrowThreads<G>, 1)
 #pragma unroll
         for (int r = 0; r < SPLIT; ++r)
           if (r == rank) {
+            float own[kFused ? kOwn : 1];
 #pragma unroll
             for (int j = 0; j < kOwn; ++j) {
               float v = 0.f;
 #pragma unroll
               for (int q = 0; q < SPLIT; ++q) v += q == r ? value(kOwn * r + j) : sm.part[kOwn * (q < r ? q : q - 1) + j][row];
               const int col = t0 + kOwn * r + j;
-              if (col < p.M && n0 + row < p.N) store_out(p.dtype, p.out, static_cast<int64_t>(col) * p.out_stride + n0 + row, v);
+              if constexpr (kFused) own[j] = v;
+              else if (col < p.M && n0 + row < p.N) store_out(p.dtype, p.out, static_cast<int64_t>(col) * p.out_stride + n0 + row, v);
             }
+            if constexpr (kFused) narrow_finish<kOwn>(p, t0 + kOwn * r, n0 + row, own, residual);
           }
       }
     }
@@ -311,7 +389,7 @@ __global__ void __launch_bounds__(kNarrowThreads<G>, 1)
   if (warp == kProducts) tmem_free<1>(tmem, C::kCols);
 }
 
-template <int NT>
+template <int NT, bool kFused>
 bool launch_narrow(const MatmulArgs& a, MmArgs p, const MatmulPlan& plan, cudaStream_t s) {
   CUtensorMap wmap, amap;
   const uint64_t wd[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.N)}, ws[1] = {static_cast<uint64_t>(a.b_stride)};
@@ -323,11 +401,15 @@ bool launch_narrow(const MatmulArgs& a, MmArgs p, const MatmulPlan& plan, cudaSt
   p.tiles_n = static_cast<int32_t>((a.N + 127) / 128);
   p.tiles_m = static_cast<int32_t>((a.M + NT - 1) / NT);
   const int split = plan.split;
-  auto kern = split == 1 ? matmul_narrow_kernel<NT, 1, 1> : split == 2 ? matmul_narrow_kernel<NT, 2, 1> : matmul_narrow_kernel<NT, 4, 1>;
+  auto kern = split == 1   ? matmul_narrow_kernel<NT, 1, 1, kFused>
+              : split == 2 ? matmul_narrow_kernel<NT, 2, 1, kFused>
+                           : matmul_narrow_kernel<NT, 4, 1, kFused>;
   int threads = kNarrowThreads<1>;
   if constexpr (NT == 64) {
     if (plan.groups == 2) {
-      kern = split == 1 ? matmul_narrow_kernel<NT, 1, 2> : split == 2 ? matmul_narrow_kernel<NT, 2, 2> : matmul_narrow_kernel<NT, 4, 2>;
+      kern = split == 1   ? matmul_narrow_kernel<NT, 1, 2, kFused>
+             : split == 2 ? matmul_narrow_kernel<NT, 2, 2, kFused>
+                          : matmul_narrow_kernel<NT, 4, 2, kFused>;
       threads = kNarrowThreads<2>;
     }
   }
@@ -425,9 +507,34 @@ __device__ __forceinline__ bool wide_accumulate(const MmArgs& p, WideShared& sm,
   return true;
 }
 
+// 64 columns of the warp's outputs out of its staging rows: by a TMA box, or row by row with neighbouring lanes on
+// neighbouring columns where the output has no tensor map (rows that are not whole 16-byte pieces).
+__device__ __forceinline__ void send_staged(const MmArgs& p, const CUtensorMap* omap, unsigned char* stage, int row0, int col) {
+  const int lane = threadIdx.x & 31;
+  if (p.tma_store) {
+    fence_async_shared();
+    __syncwarp();
+    if (lane == 0) {
+      if (row0 < p.M && col < p.N) tma_store_2d(omap, col, row0, stage);
+      bulk_commit();
+    }
+  } else {
+    __syncwarp();
+    const int rows = min(32, p.M - row0);
+    uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(row0) * p.out_stride + col;
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r, out += p.out_stride)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int x = lane + 32 * h;
+        if (col + x < p.N) out[x] = *reinterpret_cast<const uint16_t*>(stage + r * 128 + (((x >> 3) ^ (r & 7)) << 4) + 2 * (x & 7));
+      }
+    __syncwarp();
+  }
+}
+
 // The warp's outputs from (row0, col0), 64 columns at a time through staging rows of 128 bytes (16-byte pieces
-// swizzled): by a TMA box, or row by row with neighbouring lanes on neighbouring columns where the output has no
-// tensor map (rows that are not whole 16-byte pieces).
+// swizzled).
 template <int kChunks>
 __device__ __forceinline__ void wide_store(const MmArgs& p, const CUtensorMap* omap, unsigned char* stage, int row0, int col0,
                                            const float2 (&acc)[16 * kChunks]) {
@@ -442,30 +549,120 @@ __device__ __forceinline__ void wide_store(const MmArgs& p, const CUtensorMap* o
       *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
           make_uint4(pack_out(p.dtype, v[0]), pack_out(p.dtype, v[1]), pack_out(p.dtype, v[2]), pack_out(p.dtype, v[3]));
     }
-    const int col = col0 + 64 * c;
-    if (p.tma_store) {
-      fence_async_shared();
-      __syncwarp();
-      if (lane == 0) {
-        if (row0 < p.M && col < p.N) tma_store_2d(omap, col, row0, stage);
-        bulk_commit();
-      }
-    } else {
-      __syncwarp();
-      const int rows = min(32, p.M - row0);
-      uint16_t* out = static_cast<uint16_t*>(p.out) + static_cast<int64_t>(row0) * p.out_stride + col;
-#pragma unroll 1
-      for (int r = 0; r < rows; ++r, out += p.out_stride)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int x = lane + 32 * h;
-          if (col + x < p.N) out[x] = *reinterpret_cast<const uint16_t*>(stage + r * 128 + (((x >> 3) ^ (r & 7)) << 4) + 2 * (x & 7));
-        }
-      __syncwarp();
-    }
+    send_staged(p, omap, stage, row0, col0 + 64 * c);
   }
 }
 
+// 64 columns from `col` of the warp's residual rows, into registers: piece (lane % 8) of row 4i + lane / 8 in to[i], or, where
+// they cannot be read in pieces or end inside, by copy_residual.
+__device__ __forceinline__ bool residual_in_pieces(const MmArgs& p, int col) { return p.residual_vec != 0 && col + 64 <= p.N; }
+
+__device__ __forceinline__ const uint16_t* residual_at(const MmArgs& p, int row, int col) {
+  return static_cast<const uint16_t*>(p.residual) + static_cast<int64_t>(row) * p.residual_stride + col;
+}
+
+// The same columns into the staging rows, as wide_store lays them out.
+__device__ __forceinline__ void copy_residual(const MmArgs& p, unsigned char* stage, int row0, int col) {
+  const int lane = threadIdx.x & 31, rows = min(32, p.M - row0);
+  if (residual_in_pieces(p, col)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3), e = lane & 7;
+      if (r < rows)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(stage + r * 128 + ((e ^ (r & 7)) << 4))),
+                     "l"(residual_at(p, row0 + r, col + 8 * e))
+                     : "memory");
+    }
+    return;
+  }
+#pragma unroll 4
+  for (int r = 0; r < rows; ++r)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int x = lane + 32 * h;
+      if (col + x < p.N) *reinterpret_cast<uint16_t*>(stage + r * 128 + (((x >> 3) ^ (r & 7)) << 4) + 2 * (x & 7)) = *residual_at(p, row0 + r, col + x);
+    }
+}
+
+// Starts the copy of the first 64 columns' residuals, long before wide_store_fused takes them.
+__device__ __forceinline__ void wide_residual(const MmArgs& p, unsigned char* stage, int row0, int col0) {
+  if (p.residual == nullptr) return;
+  if ((threadIdx.x & 31) == 0) bulk_wait_read();  // the last box has left the staging rows
+  __syncwarp();
+  copy_residual(p, stage, row0, col0);
+}
+
+// wide_store with the fused epilogue: residuals come through the staging rows, whose pieces each lane replaces by its
+// outputs. Those of the second 64 columns wait in registers while the first are worked on.
+template <int kChunks>
+__device__ __forceinline__ void wide_store_fused(const MmArgs& p, const CUtensorMap* omap, unsigned char* stage, int row0, int col0,
+                                                 const float2 (&acc)[16 * kChunks]) {
+  const int lane = threadIdx.x & 31, rows = min(32, p.M - row0);
+  const bool ahead = kChunks == 4 && p.residual != nullptr && residual_in_pieces(p, col0 + 64);
+  uint4 next[kChunks == 4 ? 8 : 1];
+  if (ahead) {
+#pragma unroll
+    for (int i = 0; i < (kChunks == 4 ? 8 : 1); ++i) {
+      const int r = 4 * i + (lane >> 3);
+      if (r < rows) next[i] = *reinterpret_cast<const uint4*>(residual_at(p, row0 + r, col0 + 64 + 8 * (lane & 7)));
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < kChunks / 2; ++c) {
+    const int col = col0 + 64 * c;
+    if (c > 0 || p.residual == nullptr) {
+      if (lane == 0) bulk_wait_read();
+      __syncwarp();
+    }
+    if (c > 0 && ahead) {
+#pragma unroll
+      for (int i = 0; i < (kChunks == 4 ? 8 : 1); ++i) {
+        const int r = 4 * i + (lane >> 3);
+        if (r < rows) *reinterpret_cast<uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) = next[i];
+      }
+    } else if (c > 0 && p.residual != nullptr) {
+      copy_residual(p, stage, row0, col);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2* v = &acc[32 * c + 4 * e];
+      float4 lo = make_float4(v[0].x, v[0].y, v[1].x, v[1].y), hi = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+      if (p.bias != nullptr) {
+        const int from = col + 8 * e;
+        uint32_t b[4] = {0u, 0u, 0u, 0u};
+        if (p.bias_vec != 0 && from + 8 <= p.N) {
+          const uint4 w = ld_cached16(static_cast<const uint16_t*>(p.bias) + from);
+          b[0] = w.x, b[1] = w.y, b[2] = w.z, b[3] = w.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (from + i < p.N) b[i / 2] |= static_cast<uint32_t>(static_cast<const uint16_t*>(p.bias)[from + i]) << (16 * (i & 1));
+        }
+        const float2 b0 = unpack_in(p.dtype, b[0]), b1 = unpack_in(p.dtype, b[1]), b2 = unpack_in(p.dtype, b[2]), b3 = unpack_in(p.dtype, b[3]);
+        lo = make_float4(__fadd_rn(lo.x, b0.x), __fadd_rn(lo.y, b0.y), __fadd_rn(lo.z, b1.x), __fadd_rn(lo.w, b1.y));
+        hi = make_float4(__fadd_rn(hi.x, b2.x), __fadd_rn(hi.y, b2.y), __fadd_rn(hi.z, b3.x), __fadd_rn(hi.w, b3.y));
+      }
+      if (p.activation != FQ_ACT_NONE) {
+        lo = activate4(p.activation, lo);
+        hi = activate4(p.activation, hi);
+      }
+      uint4* at = reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4));
+      if (p.residual != nullptr) {
+        const uint4 w = *at;
+        const float2 r0 = unpack_in(p.dtype, w.x), r1 = unpack_in(p.dtype, w.y), r2 = unpack_in(p.dtype, w.z), r3 = unpack_in(p.dtype, w.w);
+        lo = make_float4(__fadd_rn(lo.x, r0.x), __fadd_rn(lo.y, r0.y), __fadd_rn(lo.z, r1.x), __fadd_rn(lo.w, r1.y));
+        hi = make_float4(__fadd_rn(hi.x, r2.x), __fadd_rn(hi.y, r2.y), __fadd_rn(hi.z, r3.x), __fadd_rn(hi.w, r3.y));
+      }
+      *at = make_uint4(pack_out(p.dtype, make_float2(lo.x, lo.y)), pack_out(p.dtype, make_float2(lo.z, lo.w)),
+                       pack_out(p.dtype, make_float2(hi.x, hi.y)), pack_out(p.dtype, make_float2(hi.z, hi.w)));
+    }
+    send_staged(p, omap, stage, row0, col);
+  }
+}
+
+template <bool kFused>
 __global__ void __launch_bounds__(kWideThreads, 1)
     matmul_wide_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
                        const __grid_constant__ CUtensorMap omap, const __grid_constant__ MmArgs p) {
@@ -581,18 +778,28 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const float* sa = p.sa + static_cast<int64_t>(min(row0 + lane, p.M - 1)) * p.sa_stride;
       // The columns start at a multiple of their number, so they lie in one scale block.
       const float* sb = p.sb + static_cast<int64_t>(min(col0, p.N - 1) / kScaleBlock) * p.sb_stride;
+      if (kFused && !none) wide_residual(p, stage, row0, col0);
       if (both) {
         float2 acc[64];
         ok = wide_accumulate<4>(p, sm, sa, sb, from, free0, free1, b, phase, acc);
-        if (ok) wide_store<4>(p, &omap, stage, row0, col0, acc);
+        if constexpr (kFused) {
+          if (ok) wide_store_fused<4>(p, &omap, stage, row0, col0, acc);
+        } else {
+          if (ok) wide_store<4>(p, &omap, stage, row0, col0, acc);
+        }
       } else {
         // Of a piece of 64 columns the second half has none: it reads what is there and keeps the barriers going.
         float2 acc[32];
         ok = wide_accumulate<2>(p, sm, sa, sb, from, free0, free1, b, phase, acc);
-        if (ok && !none) wide_store<2>(p, &omap, stage, row0, col0, acc);
+        if constexpr (kFused) {
+          if (ok && !none) wide_store_fused<2>(p, &omap, stage, row0, col0, acc);
+        } else {
+          if (ok && !none) wide_store<2>(p, &omap, stage, row0, col0, acc);
+        }
       }
       if (!ok) flag_failure(p.status);
     }
+    if (kFused) asm volatile("cp.async.wait_all;" ::: "memory");  // of a piece whose products never came
     if (lane == 0) bulk_wait_all();
   }
   __syncwarp();
@@ -601,6 +808,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   if (warp == 1) tmem_free<2>(tmem, 512);
 }
 
+template <bool kFused>
 bool launch_wide(const MatmulArgs& a, MmArgs p, const MatmulPlan& plan, cudaStream_t s) {
   CUtensorMap amap, wmap, omap{};
   const uint64_t ad[2] = {static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.M)}, as[1] = {static_cast<uint64_t>(a.a_stride)};
@@ -627,10 +835,21 @@ bool launch_wide(const MatmulArgs& a, MmArgs p, const MatmulPlan& plan, cudaStre
   p.pieces = static_cast<int32_t>(p.whole + rest * p.parts);
   constexpr size_t smem = sizeof(WideShared) + 1024;
   static_assert(smem <= 227 * 1024, "the ring and the staging rows fit the SM");
-  if (!ensure_dynamic_smem(reinterpret_cast<const void*>(matmul_wide_kernel), smem)) return false;
-  launch_overlapped(matmul_wide_kernel, dim3(static_cast<unsigned>(2 * (p.pieces < pairs ? p.pieces : pairs))), kWideThreads, smem, 2, s,
+  if (!ensure_dynamic_smem(reinterpret_cast<const void*>(matmul_wide_kernel<kFused>), smem)) return false;
+  launch_overlapped(matmul_wide_kernel<kFused>, dim3(static_cast<unsigned>(2 * (p.pieces < pairs ? p.pieces : pairs))), kWideThreads, smem, 2, s,
                     amap, wmap, omap, p);
   return true;
+}
+
+template <bool kFused>
+bool launch_planned(const MatmulArgs& a, const MmArgs& p, const MatmulPlan& plan, cudaStream_t s) {
+  switch (plan.rows) {
+    case 16: return launch_narrow<16, kFused>(a, p, plan, s);
+    case 32: return launch_narrow<32, kFused>(a, p, plan, s);
+    case 64: return launch_narrow<64, kFused>(a, p, plan, s);
+    case 128: return launch_narrow<128, kFused>(a, p, plan, s);
+    default: return launch_wide<kFused>(a, p, plan, s);
+  }
 }
 
 }  // namespace
@@ -689,13 +908,14 @@ bool launch_matmul_tc(const MatmulArgs& a, int dtype, cudaStream_t s) {
   if (b.M == 1) b.a_stride = (b.K + 15) / 16 * 16;
   if (b.N == 1) b.b_stride = (b.K + 15) / 16 * 16;
   const MatmulPlan plan = matmul_plan(a.M, a.N, a.K, sm_count());
-  switch (plan.rows) {
-    case 16: return launch_narrow<16>(b, p, plan, s);
-    case 32: return launch_narrow<32>(b, p, plan, s);
-    case 64: return launch_narrow<64>(b, p, plan, s);
-    case 128: return launch_narrow<128>(b, p, plan, s);
-    default: return launch_wide(b, p, plan, s);
-  }
+  if (!a.fused()) return launch_planned<false>(b, p, plan, s);
+  p.bias = a.bias;
+  p.residual = a.residual;
+  p.residual_stride = a.residual_stride;
+  p.activation = a.activation;
+  p.bias_vec = reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
+  p.residual_vec = reinterpret_cast<uintptr_t>(a.residual) % 16 == 0 && (a.M == 1 || a.residual_stride % 8 == 0);
+  return launch_planned<true>(b, p, plan, s);
 }
 
 }  // namespace fq

@@ -129,7 +129,7 @@ int matmul(const char* fn, const uint8_t* a, int64_t a_stride, const float* a_sc
   const bool tc = aligned(a, 16) && aligned(b, 16) && (M == 1 || (a_stride % 16 == 0 && a_stride >= K)) &&
                   (N == 1 || (b_stride % 16 == 0 && b_stride >= K));
   fq::drop_stale_error();
-  if (!(tc && !m.fused() && fq::launch_matmul_tc(m, dtype, stream))) fq::launch_matmul_scalar(m, dtype, stream);
+  if (!(tc && fq::launch_matmul_tc(m, dtype, stream))) fq::launch_matmul_scalar(m, dtype, stream);
   return fq::finish_launch(fn, stream);
 }
 

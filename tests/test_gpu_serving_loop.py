@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import fp8_quant_memory_gb300 as fq
+import matmul_cases
 import serving_loop_ref as ref
 import serving_ref
 from guards import Guarded
@@ -294,6 +295,37 @@ def test_linear_in_place_strided_and_broadcast(M, N, K):
     shifted = torch.zeros(M * N + 1, dtype=torch.bfloat16, device="cuda")
     shifted[1:] = res.flatten()
     assert torch.equal(fq.fp8_matmul(*x, bias=odd[1:], activation="silu", residual=shifted[1:].view(M, N)), got)
+
+
+@pytest.mark.parametrize("aligned", [True, False])
+@pytest.mark.parametrize("want, size", [*matmul_cases.NARROW.items(), *matmul_cases.WIDE.items(), *matmul_cases.WIDE_MORE], ids=str)
+def test_linear_every_kernel(want, size, aligned):
+    """Each kernel and variant of the product; bias, residual and output in whole 16-byte pieces or not."""
+    M, N, K = size
+    dt, act = ("bf16", "silu") if aligned else ("fp16", "gelu")
+    N = N // 8 * 8 if aligned and want[0] == 256 else N
+    if torch.cuda.get_device_properties(0).multi_processor_count == matmul_cases.SMS:
+        assert matmul_cases.plan(M, N, K) == want
+    x, bias, res = linear_inputs(M, N, K, 21, dt, "br")
+    stride = (N + 15) // 8 * 8 if aligned else N + 3
+    buf = torch.full((2, M, stride), 7.0, dtype=DT[dt], device="cuda")
+    buf[1, :, :N] = res
+    out, res = buf[0, :, :N], buf[1, :, :N]
+    fq.fp8_matmul(*x, out=out, bias=bias, activation=act, residual=res)
+    ref.assert_epilogue(out, *x, bias, act, res)
+    assert bool((buf[:, :, N:] == 7.0).all())
+    assert torch.equal(fq.fp8_matmul(*x, out=res, bias=bias, activation=act, residual=res), out)
+    assert bool((buf[:, :, N:] == 7.0).all())
+
+
+@pytest.mark.parametrize("M", [5, 64, 150, 2400])
+def test_linear_without_an_epilogue_is_the_product(M):
+    x, _, _ = linear_inputs(M, 2304, 512, 5, "bf16", "")
+    plain = fq.fp8_matmul(*x)
+    zero = torch.zeros(2304, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(fq.fp8_matmul(*x, bias=zero), plain)
+    relu = fq.fp8_matmul(*x, activation="relu")
+    assert torch.equal(relu, plain.clamp(min=0))
 
 
 @pytest.mark.parametrize("M", [1, 100, 600])
