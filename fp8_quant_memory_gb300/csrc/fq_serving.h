@@ -127,6 +127,7 @@ MatmulPlan matmul_plan(int64_t M, int64_t N, int64_t K, int sms);
 
 // tcgen05 kernels: 16-byte aligned operands and strides. False (nothing launched) otherwise.
 bool launch_matmul_tc(const MatmulArgs& a, int dtype, cudaStream_t s);
+bool launch_matmul_fused(const MatmulArgs& a, const MatmulPlan& plan, int dtype, cudaStream_t s);  // its part with an epilogue
 void launch_matmul_scalar(const MatmulArgs& a, int dtype, cudaStream_t s);
 
 bool launch_append_vector(const AppendArgs& a, int dtype, int table_dtype, cudaStream_t s);
