@@ -136,6 +136,7 @@ void launch_append_scalar(const AppendArgs& a, int dtype, int table_dtype, cudaS
 // Partial results of split sequences: what launch_attention_split needs in its workspace.
 size_t attention_workspace_bytes(int64_t B, int64_t Hq, int64_t Hk, int64_t D, int64_t max_len);
 bool launch_attention_split(const PagedArgs& a, int dtype, cudaStream_t s);
+bool launch_attention_window(const PagedArgs& a, int dtype, cudaStream_t s);  // its part with a window
 void launch_attention_scalar(const PagedArgs& a, int dtype, cudaStream_t s);
 
 constexpr int kMaxExtend = 16384;  // sequences of one call: three counts of each lie in shared memory

@@ -189,7 +189,7 @@ int attention(const char* fn, const uint8_t* q, int64_t q_stride, const float* q
   const bool vec = D % 16 == 0 && aligned(q, 16) && (B == 1 || q_stride % 16 == 0) && cache_vec16(p.cache, Hk) &&
                    aligned(out, 16);
   fq::drop_stale_error();
-  if (!(vec && p.window >= p.max_len && fq::launch_attention_split(p, dtype, stream))) fq::launch_attention_scalar(p, dtype, stream);
+  if (!(vec && fq::launch_attention_split(p, dtype, stream))) fq::launch_attention_scalar(p, dtype, stream);
   return fq::finish_launch(fn, stream);
 }
 
