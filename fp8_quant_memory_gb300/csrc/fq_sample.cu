@@ -22,8 +22,14 @@ using u128 = unsigned __int128;
 
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 49152;  // 192 KB; values further below the largest take a second round
-constexpr int kOne = 62;      // weights are integers, 2^62 the largest
+constexpr int kBins = 49152;          // 192 KB; values further below the largest take a second round
+constexpr int kGroups = kBins / 32;   // a warp's bins at a time
+constexpr int kPer = 2;               // groups of a thread in the sums over them
+static_assert(kPer * kThreads >= kGroups, "every group has a thread");
+constexpr int kChunk = (kGroups + kWarps - 1) / kWarps;  // groups of a warp
+constexpr int kFew = 256;             // threads whose part of the row is looked at again
+constexpr int kListed = 700;          // tokens that are listed where few are counted
+constexpr int kOne = 62;              // weights are integers, 2^62 the largest
 
 // ------------------------------------------------------------------------------------- weights
 // 2^(-j / 1024) as a sum of two floats, j in [0, 1024].
@@ -58,10 +64,27 @@ constexpr PowerTable make_powers() {
 __device__ const PowerTable kPowers = make_powers();
 
 // What a row's weights depend on: its largest value, and log2(e) / T / unit as two floats. Values are taken in halves
-// (unit 1/2) from a temperature of 1 on, so that the difference of any two is finite.
+// (unit 1/2) from a temperature of 1 on, so that the difference of any two is finite, and in smaller units at temperatures
+// whose reciprocal leaves fp32's normal range.
 struct Heat {
   float top, unit, hi, lo;
 };
+
+// hi = L / t rounded, lo what it lacks: the remainder L - hi * t is exact.
+__device__ __forceinline__ Heat heat_of(float top, float temperature) {
+  constexpr float kL = 1.44269502162933349609f, kLLo = 1.92596299112661746e-8f;  // log2(e)
+  Heat h;
+  h.top = top;
+  h.unit = temperature >= 1.8446744e19f ? 1.3552527e-20f : temperature >= 1.f ? 0.5f : 1.f;  // 2^64: 2^-66
+  const float t = temperature * h.unit;
+  if (t < INFINITY) {
+    h.hi = __fdiv_rn(kL, t);
+    h.lo = __fdiv_rn(fmaf(-h.hi, t, kL) + kLLo, t);
+  } else {
+    h.hi = h.lo = 0.f;
+  }
+  return h;
+}
 
 // 2^62 * exp((x - top) / T), x <= top, to 2^-41 of itself or 1.
 //
@@ -95,6 +118,18 @@ __device__ __forceinline__ uint64_t weight_of(const Heat& h, float x) {
 
 __device__ __forceinline__ float to_float(u128 v) {
   return fmaf(__ull2float_rn(static_cast<uint64_t>(v >> 64)), 18446744073709551616.f, __ull2float_rn(static_cast<uint64_t>(v)));
+}
+
+// floor(n / d) of a quotient below 2^31: float estimates of what is left, each 2^-21 of the last at most, or one unit.
+__device__ __forceinline__ int64_t quotient(u128 n, uint64_t d) {
+  const float inv = __fdividef(1.f, to_float(d));
+  int64_t q = static_cast<int64_t>(to_float(n) * inv);
+  for (;;) {
+    const __int128 left = static_cast<__int128>(n) - static_cast<__int128>(d) * q;
+    if (left >= 0 && left < static_cast<__int128>(d)) return q;
+    const int64_t part = max(static_cast<int64_t>(to_float(left < 0 ? -left : left) * inv), static_cast<int64_t>(1));
+    q += left < 0 ? -part : part;
+  }
 }
 
 __device__ __forceinline__ u128 lesser(u128 a, u128 b) { return a < b ? a : b; }
@@ -152,24 +187,48 @@ __device__ __forceinline__ uint32_t key_from<__half>(float x) {
   return two_keys(raw) & 0xffffu;
 }
 
-// A row as 16-byte vectors: vector v holds elements 8v - skip .. 8v - skip + 7, those outside the row as NaN.
+// A row as 16-byte vectors: vector v holds elements 8v - skip .. 8v - skip + 7. Vectors [first, last) are whole; there may
+// be one before and one behind, whose places outside the row are NaN.
 struct Row {
   const uint16_t* x;
-  int32_t V, skip, vectors;
+  int32_t V, skip, vectors, first, last;
 
-  __device__ __forceinline__ uint4 operator()(int32_t v) const {
-    const int64_t from = 8 * static_cast<int64_t>(v) - skip;
-    if (from >= 0 && from + 8 <= V) return __ldg(reinterpret_cast<const uint4*>(x + from));
-    uint32_t w[4];
+  __device__ __forceinline__ Row(const uint16_t* from, int32_t n) : x(from), V(n) {
+    skip = static_cast<int32_t>((reinterpret_cast<uintptr_t>(x) & 15u) / 2);
+    vectors = static_cast<int32_t>((static_cast<int64_t>(V) + skip + 7) / 8);
+    first = skip > 0 ? 1 : 0;
+    last = max(first, static_cast<int32_t>((static_cast<int64_t>(V) + skip) / 8));
+  }
+  __device__ __forceinline__ uint4 whole(int32_t v) const {
+    return __ldg(reinterpret_cast<const uint4*>(x + (8 * static_cast<int64_t>(v) - skip)));
+  }
+  __device__ __forceinline__ uint4 part(int32_t v) const {
+    uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t a = from + 2 * i;
-      const uint32_t lo = a >= 0 && a < V ? x[a] : 0xffffu, hi = a + 1 >= 0 && a + 1 < V ? x[a + 1] : 0xffffu;
-      w[i] = lo | (hi << 16);
+    for (int i = 0; i < 8; ++i) {
+      const int64_t a = 8 * static_cast<int64_t>(v) - skip + i;
+      if (a >= 0 && a < V) w[i / 2] = (i & 1) ? (w[i / 2] & 0xffffu) | (static_cast<uint32_t>(x[a]) << 16) : (w[i / 2] & 0xffff0000u) | x[a];
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
+
+// f(vector, its number) for vectors from + lane, from + lane + step, ... below `to`; four loads on their way at a time.
+template <typename F>
+__device__ __forceinline__ void each_vector(const Row& row, int32_t from, int32_t to, int32_t step, F f) {
+  if (from < row.first && from < to) f(row.part(from), from);
+  int32_t v = from < row.first ? from + step : from;
+  const int32_t end = min(to, row.last);
+  for (; v + 3 * static_cast<int64_t>(step) < end; v += 4 * step) {
+    uint4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = row.whole(v + i * step);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f(x[i], v + i * step);
+  }
+  for (; v < end; v += step) f(row.whole(v), v);
+  if (v < to && v >= row.last) f(row.part(v), v);  // v == last: there is one vector behind
+}
 
 template <typename F>
 __device__ __forceinline__ void each_key(const uint4& v, F f) {
@@ -187,6 +246,11 @@ __device__ __forceinline__ u128 shfl_up(u128 v, int o) {
   const uint64_t lo = __shfl_up_sync(0xffffffffu, static_cast<uint64_t>(v), o);
   const uint64_t hi = __shfl_up_sync(0xffffffffu, static_cast<uint64_t>(v >> 64), o);
   return (static_cast<u128>(hi) << 64) | lo;
+}
+
+__device__ __forceinline__ u128 broadcast(u128 v, int lane) {
+  return (static_cast<u128>(__shfl_sync(0xffffffffu, static_cast<uint64_t>(v >> 64), lane)) << 64) |
+         __shfl_sync(0xffffffffu, static_cast<uint64_t>(v), lane);
 }
 
 template <typename N>
@@ -218,14 +282,21 @@ __device__ __forceinline__ N block_scan(N v, N* part, N* total) {
 
 struct Shared {
   uint32_t bin[kBins];
+  // of a group of 32 bins: tokens before it (x, by its number), and the number of the n-th that has any (y, by n)
+  uint2 group[kGroups];
+  u128 part[kChunk];   // sums of a warp's groups
   u128 wide[kWarps];
+  uint64_t scan[kWarps];
   uint32_t narrow[kWarps];
-  // the thread's bins in which a border lies
-  u128 before;
-  int32_t rank, first;
-  // found there
-  u128 sum;
-  int32_t key, nth;
+  uint2 listed[kListed];  // index, key
+  uint16_t ids[kFew];
+  int32_t list_size, id_count;
+  // the border to find and what was found, by one thread for all
+  u128 border, kept;
+  uint32_t key;
+  int32_t nth;
+  float logprob;
+  int32_t index;
 };
 
 struct Cuts {
@@ -234,225 +305,402 @@ struct Cuts {
   uint64_t min_weight;
 };
 
-// The first bin of [first, first + n) up to and with which the running sum, `before` and `rank` tokens ahead of it, is
-// above `border`; one warp. Returns the bin, the sum before it and its weight.
+// The warp's sum of v < 2^108, whole in every lane: limbs of 27 bits, whose sums over 32 lanes fit 32 bits.
+__device__ __forceinline__ u128 warp_sum(u128 v) {
+  u128 sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    sum += static_cast<u128>(__reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> (27 * i)) & 0x7ffffffu)) << (27 * i);
+  return sum;
+}
+
+// This lane's tokens of a group (`count` in its bin, `rank` before the group) that are among the first top_k.
+__device__ __forceinline__ uint32_t among_first(uint32_t count, uint32_t rank, uint32_t top_k) {
+  if (rank >= top_k) return 0;
+  const uint32_t ahead = warp_scan(count) - count, left = top_k - rank;
+  return ahead >= left ? 0u : min(count, left - ahead);
+}
+
+// The counts of a round, bins 0 .. bins - 1 for keys first_key - bin, and their sums: over groups of 32 bins, of which
+// those that hold any tokens are shared out among the warps in order.
 template <typename T>
-__device__ __forceinline__ int find_bin(const Shared& sm, const Cuts& c, uint32_t top, int first, int n, u128 before, uint32_t rank,
-                                        u128 border, u128* sum_before, uint64_t* weight) {
-  const int lane = threadIdx.x & 31;
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    const int i = first + i0 + lane;
-    const uint32_t count = i0 + lane < n ? sm.bin[i] : 0u;
-    const uint32_t ahead = rank + warp_scan(count) - count;
-    const uint32_t in = ahead >= c.top_k ? 0u : min(count, c.top_k - ahead);
-    const uint64_t w = in != 0u ? weight_of(c.heat, value_of<T>(top - i)) : 0;
-    const u128 incl = before + warp_scan(static_cast<u128>(w) * in);
-    const uint32_t hit = __ballot_sync(0xffffffffu, incl > border);
-    if (hit != 0u) {
-      const int l = __ffs(hit) - 1;
-      const u128 from = incl - static_cast<u128>(w) * in;
-      *sum_before = (static_cast<u128>(__shfl_sync(0xffffffffu, static_cast<uint64_t>(from >> 64), l)) << 64) |
-                    __shfl_sync(0xffffffffu, static_cast<uint64_t>(from), l);
-      *weight = __shfl_sync(0xffffffffu, w, l);
-      return first + i0 + l;
-    }
-    before = (static_cast<u128>(__shfl_sync(0xffffffffu, static_cast<uint64_t>(incl >> 64), 31)) << 64) |
-             __shfl_sync(0xffffffffu, static_cast<uint64_t>(incl), 31);
-    rank += __shfl_sync(0xffffffffu, warp_scan(count), 31);
+struct Round {
+  uint32_t first_key;
+  int bins;
+  int32_t filled;       // groups with tokens
+  u128 before;          // sum before the lane-th warp's groups, and of them
+  u128 sum;
+
+  __device__ __forceinline__ int32_t begin(int warp) const { return filled * warp / kWarps; }
+
+  // This lane's tokens and their weight, of the n-th filled group.
+  __device__ __forceinline__ uint32_t tokens(const Shared& sm, const Cuts& c, int n, int* bin, uint64_t* w) const {
+    const uint32_t g = sm.group[n].y;
+    *bin = 32 * static_cast<int>(g) + (threadIdx.x & 31);
+    uint32_t count = sm.bin[*bin];
+    if (c.top_k != 0xffffffffu) count = among_first(count, sm.group[g].x, c.top_k);
+    *w = count != 0u ? weight_of(c.heat, value_of<T>(first_key - *bin)) : 0;
+    return count;
   }
-  return -1;
+
+  // Adds the round's tokens, weights, and weights of at least min_weight to the three sums.
+  __device__ __forceinline__ void add_up(Shared& sm, const Cuts& c, uint32_t& ranks, u128& total, u128& above) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, groups = (bins + 31) / 32;
+#pragma unroll 4
+    for (int g = warp; g < groups; g += kWarps) {
+      const uint32_t n = __reduce_add_sync(0xffffffffu, sm.bin[32 * g + lane]);
+      if (lane == 0) sm.group[g].x = n;
+    }
+    __syncthreads();
+    // tokens in the low half, filled groups in the high half
+    uint64_t size[kPer], mine = 0, all;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int g = kPer * threadIdx.x + i;
+      const uint32_t n = g < groups ? sm.group[g].x : 0u;
+      size[i] = n == 0u ? 0 : (1ull << 32) + n;
+      mine += size[i];
+    }
+    uint64_t at = block_scan(mine, sm.scan, &all);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int g = kPer * threadIdx.x + i;
+      if (size[i] != 0) {
+        sm.group[g].x = ranks + static_cast<uint32_t>(at);
+        sm.group[at >> 32].y = g;
+      }
+      at += size[i];
+    }
+    filled = static_cast<int32_t>(all >> 32);
+    ranks += static_cast<uint32_t>(all);
+    __syncthreads();
+    u128 mine_sum = 0, mine_above = 0;
+    for (int n = begin(warp); n < begin(warp + 1); ++n) {
+      int bin;
+      uint64_t w;
+      const uint32_t count = tokens(sm, c, n, &bin, &w);
+      const u128 part = static_cast<u128>(w) * count;
+      mine_sum += part;
+      if (w >= c.min_weight) mine_above += part;
+    }
+    mine_sum = warp_sum(mine_sum);
+    __syncthreads();
+    if (lane == 0) sm.wide[warp] = mine_sum;
+    __syncthreads();
+    sum = sm.wide[lane];
+    before = total + warp_scan(sum) - sum;
+    total += warp_sum(sum);
+    if (c.min_weight > 0) {
+      mine_above = warp_sum(mine_above);
+      __syncthreads();
+      if (lane == 0) sm.wide[warp] = mine_above;
+      __syncthreads();
+      above += warp_sum(sm.wide[lane]);
+    }
+  }
+
+  // Whether the running sum passes sm.border in this round; one thread then has called found(bin, its weight, the sum
+  // before it).
+  template <typename F>
+  __device__ __forceinline__ bool find(Shared& sm, const Cuts& c, F found) const {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const u128 border = sm.border;
+    const uint32_t in = __ballot_sync(0xffffffffu, before <= border && border < before + sum);
+    if (in == 0u) return false;
+    const int who = __ffs(in) - 1, first = begin(who), n = begin(who + 1) - first;
+    u128 upto = broadcast(before, who);
+    int at = first;
+    if (n > 1) {
+      // the sums of that warp's groups, one to a warp
+      for (int i = warp; i < n; i += kWarps) {
+        int bin;
+        uint64_t w;
+        const uint32_t count = tokens(sm, c, first + i, &bin, &w);
+        const u128 s = warp_sum(static_cast<u128>(w) * count);
+        if (lane == 0) sm.part[i] = s;
+      }
+      __syncthreads();
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const u128 s = i0 + lane < n ? sm.part[i0 + lane] : 0, incl = upto + warp_scan(s);
+        const uint32_t hit = __ballot_sync(0xffffffffu, incl > border);
+        if (hit != 0u) {
+          const int l = __ffs(hit) - 1;
+          at = first + i0 + l;
+          upto = broadcast(incl - s, l);
+          break;
+        }
+        upto = broadcast(incl, 31);
+      }
+    }
+    __syncthreads();  // every thread has read the border: found() may set the next one
+    if (warp == 0) {
+      int bin;
+      uint64_t w;
+      const uint32_t count = tokens(sm, c, at, &bin, &w);
+      const u128 part = static_cast<u128>(w) * count, incl = upto + warp_scan(part);
+      const uint32_t hit = __ballot_sync(0xffffffffu, incl > border);
+      if (lane == __ffs(hit) - 1) found(bin, w, incl - part);
+    }
+    __syncthreads();
+    return true;
+  }
+};
+
+// f(vector, its number) for the vectors of the threads for which `mine` is true (n of them, at most kFew), spread over all
+// threads. To be called by every thread.
+template <typename F>
+__device__ __forceinline__ void each_of_few(Shared& sm, const Row& row, bool mine, int n, F f) {
+  const int tid = threadIdx.x;
+  const uint32_t in = __ballot_sync(0xffffffffu, mine);
+  int at = 0;
+  if ((tid & 31) == 0 && in != 0u) at = atomicAdd(&sm.id_count, __popc(in));
+  at = __shfl_sync(0xffffffffu, at, 0) + __popc(in & ((1u << (tid & 31)) - 1u));
+  if (mine) sm.ids[at] = static_cast<uint16_t>(tid);
+  __syncthreads();
+  const int rounds = (row.vectors + kThreads - 1) / kThreads;
+  for (int32_t j = tid; j < n * rounds; j += kThreads) {  // 256 * 2^18 at most
+    const int32_t i = j / n, v = sm.ids[j - i * n] + kThreads * i;
+    if (v < row.vectors) f(v >= row.first && v < row.last ? row.whole(v) : row.part(v), v);
+  }
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
   pdl_wait();
-  for (int32_t b = blockIdx.x; b < a.B; b += gridDim.x) {
-    Row row;
-    row.x = a.logits + b * a.stride;
-    row.V = a.V;
-    row.skip = static_cast<int32_t>((reinterpret_cast<uintptr_t>(row.x) & 15u) / 2);
-    row.vectors = static_cast<int32_t>((static_cast<int64_t>(a.V) + row.skip + 7) / 8);
-    const float temperature = a.temperature == nullptr ? 1.f : a.temperature[b];
-    const int32_t k = a.top_k == nullptr ? 0 : a.top_k[b];
-    const float top_p = a.top_p == nullptr ? 1.f : a.top_p[b], min_p = a.min_p == nullptr ? 0.f : a.min_p[b];
+  const int32_t b = blockIdx.x;
+  const Row row(a.logits + b * a.stride, a.V);
+  const float temperature = a.temperature == nullptr ? 1.f : a.temperature[b];
+  const int32_t k = a.top_k == nullptr ? 0 : a.top_k[b];
+  const float top_p = a.top_p == nullptr ? 1.f : a.top_p[b], min_p = a.min_p == nullptr ? 0.f : a.min_p[b],
+              u = a.u[b];
 
-    // ------------------------------------------------------------------- the largest value
-    uint32_t top = 0;
-    for (int32_t v = threadIdx.x; v < row.vectors; v += kThreads)
-      each_key(row(v), [&](uint32_t s, int) {
-        if (s > Keys<T>::kFloor && s <= Keys<T>::kTop) top = max(top, s);
+  // ------------------------------------------------------------------- the largest value
+  uint32_t two = 0, own;  // of this thread's vectors tid, tid + 1024, ...
+  each_vector(row, tid, row.vectors, kThreads, [&](const uint4& v, int32_t) {
+    two = __vmaxu2(two, __vmaxu2(__vmaxu2(two_keys(v.x), two_keys(v.y)), __vmaxu2(two_keys(v.z), two_keys(v.w))));
+  });
+  own = max(two & 0xffffu, two >> 16);
+  if (own > Keys<T>::kTop) {  // NaN among them
+    own = 0;
+    each_vector(row, tid, row.vectors, kThreads, [&](const uint4& v, int32_t) {
+      each_key(v, [&](uint32_t s, int) {
+        if (s <= Keys<T>::kTop) own = max(own, s);
       });
-    top = __reduce_max_sync(0xffffffffu, top);
-    __syncthreads();  // the last row's readers are through
-    if (lane == 0) sm.narrow[warp] = top;
-    __syncthreads();
-    top = __reduce_max_sync(0xffffffffu, sm.narrow[lane]);
-    if (top == kMinusZero) top = kZero;
-    if (top == 0u) {  // nothing is left of the row
-      if (threadIdx.x == 0) {
-        a.token[b] = -1;
-        if (a.logprob != nullptr) a.logprob[b] = -INFINITY;
-      }
-      continue;
+    });
+  }
+  if (own == kMinusZero) own = kZero;
+  uint32_t top = __reduce_max_sync(0xffffffffu, own);
+  if (lane == 0) sm.narrow[warp] = top;
+  if (tid == 0) {
+    sm.list_size = 0;
+    sm.id_count = 0;
+    sm.index = 0x7fffffff;
+  }
+  __syncthreads();
+  top = __reduce_max_sync(0xffffffffu, sm.narrow[lane]);
+  if (top <= Keys<T>::kFloor) {  // nothing is left of the row
+    if (tid == 0) {
+      a.token[b] = -1;
+      if (a.logprob != nullptr) a.logprob[b] = -INFINITY;
     }
+    return;
+  }
 
-    uint32_t key = top;
-    int32_t nth = 0;
-    float logprob = 0.f;
-    if (temperature >= 1.17549435e-38f && k != 1) {
-      Cuts c;
-      c.heat.top = value_of<T>(top);
-      c.heat.unit = temperature >= 1.f ? 0.5f : 1.f;
-      const double heat = 1.4426950408889634074 / (static_cast<double>(temperature) * c.heat.unit);
-      c.heat.hi = static_cast<float>(heat);
-      c.heat.lo = static_cast<float>(heat - static_cast<double>(c.heat.hi));
-      c.top_k = k <= 0 ? 0xffffffffu : static_cast<uint32_t>(k);
-      c.min_weight = min_p > 0.f ? static_cast<uint64_t>(share_of(fminf(min_p, 1.f), static_cast<u128>(1) << kOne, true)) : 0;
-      // Weights below exp(-45) of the largest are 0 in units of 2^-62.
-      const float least = c.heat.top - 45.f * temperature;
-      uint32_t floor_key = Keys<T>::kFloor + 1;
-      if (least == least) floor_key = max(floor_key, key_from<T>(least));
-      const int bins = static_cast<int>(top - floor_key) + 1, rounds = (bins + kBins - 1) / kBins;
-
-      u128 sum_before = 0, sum_mine = 0, border = 0, kept = 0;
-      uint32_t rank_before = 0;
-      int from = 0, per = 0, base = 0;
-      // Round r: bins kBins * r ... Their counts, and this thread's bins [from, from + per) with the tokens and the sum
-      // before them.
-      auto count = [&](int r, uint32_t& rank_carry, u128& sum_carry, u128& floor_sum) {
-        base = kBins * r;
-        __syncthreads();  // the last round's readers are through
-        const int here = min(kBins, bins - base);
-        for (int i = threadIdx.x; i < here; i += kThreads) sm.bin[i] = 0u;
+  uint32_t key = top;
+  int32_t nth = 0;
+  float logprob = 0.f;
+  bool few = false;  // the tokens that count are listed
+  if (temperature >= 1.17549435e-38f && k != 1) {
+    Cuts c;
+    c.heat = heat_of(value_of<T>(top), temperature);
+    c.top_k = k <= 0 ? 0xffffffffu : static_cast<uint32_t>(k);
+    c.min_weight = min_p > 0.f ? static_cast<uint64_t>(share_of(fminf(min_p, 1.f), static_cast<u128>(1) << kOne, true)) : 0;
+    // Which keys count at all. Weights below exp(-45) of the largest are 0 in units of 2^-62; those below min_p matter to
+    // the sum that top_p is a part of, but without top_p to nothing.
+    float reach = 45.f;
+    if (min_p > 0.f && !(top_p < 1.f)) reach = fminf(reach, -logf(fminf(min_p, 1.f)) * 1.001f + 1e-5f);
+    const float least = c.heat.top - reach * temperature;
+    uint32_t floor_key = Keys<T>::kFloor + 1;
+    if (least == least) floor_key = max(floor_key, key_from<T>(least));
+    if (c.top_k <= kThreads) {
+      // At least k tokens are as large as the k-th largest of the threads' own largest, so none below it counts. It is
+      // looked for in the first bins, else by bisection.
+      constexpr int kNear = kPer * kThreads;
+      reinterpret_cast<uint2*>(sm.bin)[tid] = make_uint2(0u, 0u);
+      __syncthreads();
+      if (top - own < kNear) atomicAdd(&sm.bin[top - own], 1u);
+      __syncthreads();
+      const uint2 n = reinterpret_cast<const uint2*>(sm.bin)[tid];
+      uint32_t all, upto = block_scan(n.x + n.y, sm.narrow, &all);
+      if (all >= c.top_k) {
+        if (upto < c.top_k && upto + n.x + n.y >= c.top_k) sm.key = top - (kPer * tid + (upto + n.x >= c.top_k ? 0 : 1));
         __syncthreads();
-        const uint32_t first_key = top - base;
-        for (int32_t v = threadIdx.x; v < row.vectors; v += kThreads)
-          each_key(row(v), [&](uint32_t s, int) {
+        floor_key = max(floor_key, sm.key);
+      } else {
+        uint32_t lo = 0, hi = 0x10000;  // count(own >= lo) >= k > count(own >= hi)
+        while (hi - lo > 1) {
+          const uint32_t mid = (lo + hi) / 2;
+          if (static_cast<uint32_t>(__syncthreads_count(own >= mid)) >= c.top_k) lo = mid;
+          else hi = mid;
+        }
+        floor_key = max(floor_key, lo);
+      }
+    }
+    if (floor_key == kZero) floor_key = kMinusZero;
+    const int bins = static_cast<int>(top - floor_key) + 1, rounds = (bins + kBins - 1) / kBins;
+    const int counted = __syncthreads_count(own >= floor_key);
+    few = counted <= kFew && rounds == 1;
+
+    Round<T> round;
+    auto count = [&](int r) {
+      round.first_key = top - kBins * r;
+      round.bins = min(kBins, bins - kBins * r);
+      __syncthreads();  // the last round's readers are through
+      for (int i = tid; i < (round.bins + 31) / 32 * 8; i += kThreads) reinterpret_cast<uint4*>(sm.bin)[i] = make_uint4(0u, 0u, 0u, 0u);
+      __syncthreads();
+      const uint32_t first_key = round.first_key, n = static_cast<uint32_t>(round.bins);
+      if (few) {
+        each_of_few(sm, row, own >= floor_key, counted, [&](const uint4& v, int32_t at) {
+          each_key(v, [&](uint32_t s, int i) {
             if (s == kMinusZero) s = kZero;
-            const uint32_t i = first_key - s;  // larger keys (NaN, and the last round's) wrap around
-            if (i < static_cast<uint32_t>(here)) atomicAdd(&sm.bin[i], 1u);
+            if (first_key - s >= n) return;  // larger keys (NaN) wrap around
+            atomicAdd(&sm.bin[first_key - s], 1u);
+            const int place = atomicAdd(&sm.list_size, 1);
+            if (place < kListed) sm.listed[place] = make_uint2(static_cast<uint32_t>(8 * at - row.skip + i), s);
           });
-        __syncthreads();
-        per = ((here + kThreads - 1) / kThreads) | 1;  // odd: the threads' bins are in different banks
-        from = min(here, static_cast<int>(threadIdx.x) * per);
-        const int to = min(here, from + per);
-        uint32_t mine = 0, all;
-        for (int i = from; i < to; ++i) mine += sm.bin[i];
-        const uint32_t rank = rank_carry + block_scan(mine, sm.narrow, &all);
-        rank_carry += all;
-        rank_before = rank;
-        u128 sum = 0, above = 0;
-        uint32_t ahead = rank;
-        for (int i = from; i < to && ahead < c.top_k; ++i) {
-          const uint32_t n = sm.bin[i];
-          if (n == 0u) continue;
-          const uint64_t w = weight_of(c.heat, value_of<T>(first_key - i));
-          const u128 add = static_cast<u128>(w) * min(n, c.top_k - ahead);
-          sum += add;
-          if (w >= c.min_weight) above += add;
-          ahead += n;
-        }
-        u128 total;
-        sum_mine = sum;
-        sum_before = sum_carry + block_scan(sum, sm.wide, &total);
-        sum_carry += total;
-        u128 total_above;
-        block_scan(above, sm.wide, &total_above);
-        floor_sum += total_above;
-      };
-      // The bin of the round in which the running sum passes `border`, if it does; every thread.
-      auto search = [&](u128 border_at, bool crossing, uint64_t* w, u128* ahead, int* bin) {
-        __syncthreads();
-        if (threadIdx.x == 0) sm.first = -1;
-        __syncthreads();
-        if (crossing) {
-          sm.first = from;
-          sm.before = sum_before;
-          sm.rank = static_cast<int32_t>(rank_before);
-        }
-        __syncthreads();
-        if (sm.first < 0) return false;
-        const int here = min(kBins, bins - base);
-        *bin = find_bin<T>(sm, c, top - base, sm.first, min(per, here - sm.first), sm.before, static_cast<uint32_t>(sm.rank),
-                           border_at, ahead, w);
-        return *bin >= 0;
-      };
-      auto redo = [&](int r, uint32_t& rank_carry, u128& sum_carry) {
-        u128 unused = 0;
-        if (rounds > 1) count(r, rank_carry, sum_carry, unused);
-      };
-      uint32_t ranks = 0;
-      u128 total = 0, above = 0;
-      for (int r = 0; r < rounds; ++r) count(r, ranks, total, above);
-      kept = lesser(total, above);
-      if (top_p < 1.f) {
-        // The first running sum that reaches the border: tokens before which it is below are kept.
-        u128 reach = share_of(fmaxf(top_p, 0.f), total, true);
-        if (reach == 0) reach = 1;
-        uint32_t rc = 0;
-        u128 sc = 0;
-        for (int r = 0; r < rounds; ++r) {
-          redo(r, rc, sc);
-          uint64_t w;
-          u128 ahead;
-          int bin;
-          if (search(reach - 1, sum_before < reach && sum_before + sum_mine >= reach, &w, &ahead, &bin)) {
-            const u128 n = (reach - ahead + w - 1) / w;
-            kept = lesser(kept, ahead + n * w);
-            break;
-          }
-        }
+        });
+      } else if (own >= floor_key) {
+        each_vector(row, tid, row.vectors, kThreads, [&](const uint4& v, int32_t) {
+          each_key(v, [&](uint32_t s, int) {
+            if (s == kMinusZero) s = kZero;
+            if (first_key - s < n) atomicAdd(&sm.bin[first_key - s], 1u);
+          });
+        });
       }
-      const float u = a.u[b];
-      border = share_of(u > 0.f ? fminf(u, 0.999999940395355225f) : 0.f, kept, false);
+      __syncthreads();
+    };
+    uint32_t ranks = 0;
+    u128 total = 0, above = 0;
+    for (int r = 0; r < rounds; ++r) {
+      count(r);
+      round.add_up(sm, c, ranks, total, above);
+    }
+    // Again, round by round, where one does not hold them all; true once f is.
+    auto again = [&](auto f) {
       uint32_t rc = 0;
-      u128 sc = 0;
+      u128 sc = 0, unused = 0;
       for (int r = 0; r < rounds; ++r) {
-        redo(r, rc, sc);
-        uint64_t w;
-        u128 ahead;
-        int bin;
-        if (search(border, sum_before <= border && sum_before + sum_mine > border, &w, &ahead, &bin)) {
-          key = top - base - bin;
-          nth = static_cast<int32_t>((border - ahead) / w);
-          const float whole = to_float(kept), rest = to_float(kept - w);
-          logprob = rest < 0.5f * whole ? log1pf(-rest / whole) : logf(to_float(w) / whole);
-          break;
+        if (rounds > 1) {
+          count(r);
+          round.add_up(sm, c, rc, sc, unused);
         }
+        if (f()) return;
+      }
+    };
+    // Borders and what lies at them: 128-bit arithmetic, by one thread.
+    auto aim = [&] {
+      sm.border = share_of(u > 0.f ? fminf(u, 0.999999940395355225f) : 0.f, sm.kept, false);
+    };
+    if (tid == 0) {
+      sm.kept = c.min_weight > 0 ? lesser(total, above) : total;
+      if (top_p < 1.f) {
+        // Tokens before which the running sum is below the border are kept: up to the first sum that reaches it.
+        const u128 goal = share_of(fmaxf(top_p, 0.f), total, true);
+        sm.border = goal > 0 ? goal - 1 : 0;
+      } else {
+        aim();
       }
     }
+    __syncthreads();
+    if (top_p < 1.f)
+      again([&] {
+        return round.find(sm, c, [&](int, uint64_t w, u128 ahead) {
+          sm.kept = lesser(sm.kept, ahead + static_cast<u128>(quotient(sm.border - ahead, w) + 1) * w);
+          aim();
+        });
+      });
+    again([&] {
+      return round.find(sm, c, [&](int bin, uint64_t w, u128 ahead) {
+        sm.key = round.first_key - bin;
+        sm.nth = static_cast<int32_t>(quotient(sm.border - ahead, w));
+        const float whole = to_float(sm.kept), rest = to_float(sm.kept - w);
+        sm.logprob = rest < 0.5f * whole ? log1pf(-rest / whole) : logf(to_float(w) / whole);
+      });
+    });
+    key = sm.key;
+    nth = sm.nth;
+    logprob = sm.logprob;
+    few = few && sm.list_size <= kListed;
+  }
 
-    // ------------------------------------------------------- the nth element of that value
-    // Each warp takes an equal run of vectors: how many it has, then the run with the nth.
-    const uint32_t twin = key == kZero ? kMinusZero : key;
-    const int32_t run = (row.vectors + kWarps - 1) / kWarps, v0 = min(row.vectors, warp * run), v1 = min(row.vectors, v0 + run);
-    uint32_t mine = 0;
-    for (int32_t v = v0 + lane; v < v1; v += 32) each_key(row(v), [&](uint32_t s, int) { mine += s == key || s == twin; });
-    mine = __reduce_add_sync(0xffffffffu, mine);
-    __syncthreads();
-    if (lane == 0) sm.narrow[warp] = mine;
-    __syncthreads();
-    const uint32_t upto = warp_scan(sm.narrow[lane]), all_before = __shfl_sync(0xffffffffu, upto - sm.narrow[lane], warp);
-    if (all_before <= static_cast<uint32_t>(nth) && static_cast<uint32_t>(nth) < all_before + mine) {
-      uint32_t left = nth - all_before;
-      for (int32_t v = v0; v < v1; v += 32) {
-        uint32_t bits = 0;  // of this lane's eight
-        if (v + lane < v1) each_key(row(v + lane), [&](uint32_t s, int i) { bits |= static_cast<uint32_t>(s == key || s == twin) << i; });
-        const uint32_t has = __popc(bits), incl = warp_scan(has), all = __shfl_sync(0xffffffffu, incl, 31);
-        if (left < all) {
-          if (incl - has <= left && left < incl) {
-            for (uint32_t n = left - (incl - has); n > 0; --n) bits &= bits - 1;
-            a.token[b] = 8 * static_cast<int64_t>(v + lane) - row.skip + (__ffs(bits) - 1);
-            if (a.logprob != nullptr) a.logprob[b] = logprob;
-          }
-          break;
-        }
-        left -= all;
+  // ------------------------------------------------------- the nth element of that value
+  const uint32_t twin = key == kZero ? kMinusZero : key;
+  if (few) {
+    const int n = sm.list_size;
+    const uint2 me = tid < n ? sm.listed[tid] : make_uint2(0u, 0u);
+    if (tid < n && me.y == key) {
+      int32_t ahead = 0;
+      for (int i = 0; i < n; ++i) ahead += sm.listed[i].y == key && sm.listed[i].x < me.x;
+      if (ahead == nth) {
+        a.token[b] = me.x;
+        if (a.logprob != nullptr) a.logprob[b] = logprob;
       }
+    }
+    return;
+  }
+  if (key == top && nth == 0) {
+    // The least index of those threads that have it, if they are few.
+    const int n = __syncthreads_count(own == top);
+    if (n <= kFew) {
+      __syncthreads();
+      if (tid == 0) sm.id_count = 0;
+      __syncthreads();
+      each_of_few(sm, row, own == top, n, [&](const uint4& v, int32_t at) {
+        int32_t least = 0x7fffffff;
+        each_key(v, [&](uint32_t s, int i) {
+          if (s == key || s == twin) least = min(least, 8 * at - row.skip + i);
+        });
+        if (least != 0x7fffffff) atomicMin(&sm.index, least);
+      });
+      __syncthreads();
+      if (tid == 0) {
+        a.token[b] = sm.index;
+        if (a.logprob != nullptr) a.logprob[b] = logprob;
+      }
+      return;
+    }
+  }
+  // Each warp takes an equal run of vectors: how many it has, then the run with the nth.
+  const int32_t run = (row.vectors + kWarps - 1) / kWarps, v0 = min(row.vectors, warp * run), v1 = min(row.vectors, v0 + run);
+  uint32_t mine = 0;
+  each_vector(row, v0 + lane, v1, 32, [&](const uint4& v, int32_t) { each_key(v, [&](uint32_t s, int) { mine += s == key || s == twin; }); });
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  __syncthreads();
+  if (lane == 0) sm.narrow[warp] = mine;
+  __syncthreads();
+  const uint32_t upto = warp_scan(sm.narrow[lane]), all_before = __shfl_sync(0xffffffffu, upto - sm.narrow[lane], warp);
+  if (all_before <= static_cast<uint32_t>(nth) && static_cast<uint32_t>(nth) < all_before + mine) {
+    uint32_t left = nth - all_before;
+    for (int32_t v = v0; v < v1; v += 32) {
+      uint32_t bits = 0;  // of this lane's eight
+      if (v + lane < v1) {
+        const bool whole = v + lane >= row.first && v + lane < row.last;
+        each_key(whole ? row.whole(v + lane) : row.part(v + lane), [&](uint32_t s, int i) { bits |= static_cast<uint32_t>(s == key || s == twin) << i; });
+      }
+      const uint32_t has = __popc(bits), incl = warp_scan(has), all = __shfl_sync(0xffffffffu, incl, 31);
+      if (left < all) {
+        if (incl - has <= left && left < incl) {
+          for (uint32_t n = left - (incl - has); n > 0; --n) bits &= bits - 1;
+          a.token[b] = 8 * static_cast<int64_t>(v + lane) - row.skip + (__ffs(bits) - 1);
+          if (a.logprob != nullptr) a.logprob[b] = logprob;
+        }
+        break;
+      }
+      left -= all;
     }
   }
 }
@@ -462,8 +710,7 @@ bool launch(const SampleArgs& a, cudaStream_t s) {
   constexpr size_t smem = sizeof(Shared);
   static_assert(smem <= 227 * 1024, "the bins fit the SM");
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(sample_kernel<T>), smem)) return false;
-  const int64_t rows = a.B, sms = sm_count();
-  launch_overlapped(sample_kernel<T>, dim3(static_cast<unsigned>(rows < sms ? rows : sms)), kThreads, smem, 1, s, a);
+  launch_overlapped(sample_kernel<T>, dim3(static_cast<unsigned>(a.B)), kThreads, smem, 1, s, a);
   return true;
 }
 
