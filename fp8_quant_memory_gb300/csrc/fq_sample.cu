@@ -28,7 +28,7 @@ constexpr int kPer = 2;               // groups of a thread in the sums over the
 static_assert(kPer * kThreads >= kGroups, "every group has a thread");
 constexpr int kChunk = (kGroups + kWarps - 1) / kWarps;  // groups of a warp
 constexpr int kFew = 256;             // threads whose part of the row is looked at again
-constexpr int kListed = 700;          // tokens that are listed where few are counted
+constexpr int kListed = 256;          // tokens that are sorted where few count
 constexpr int kOne = 62;              // weights are integers, 2^62 the largest
 
 // ------------------------------------------------------------------------------------- weights
@@ -61,20 +61,22 @@ constexpr PowerTable make_powers() {
   return t;
 }
 
-__device__ const PowerTable kPowers = make_powers();
+__device__ const PowerTable kPowers = make_powers();  // each block copies it to shared memory
 
 // What a row's weights depend on: its largest value, and log2(e) / T / unit as two floats. Values are taken in halves
 // (unit 1/2) from a temperature of 1 on, so that the difference of any two is finite, and in smaller units at temperatures
 // whose reciprocal leaves fp32's normal range.
 struct Heat {
   float top, unit, hi, lo;
+  const PowerTable* powers;
 };
 
 // hi = L / t rounded, lo what it lacks: the remainder L - hi * t is exact.
-__device__ __forceinline__ Heat heat_of(float top, float temperature) {
+__device__ __forceinline__ Heat heat_of(float top, float temperature, const PowerTable* powers) {
   constexpr float kL = 1.44269502162933349609f, kLLo = 1.92596299112661746e-8f;  // log2(e)
   Heat h;
   h.top = top;
+  h.powers = powers;
   h.unit = temperature >= 1.8446744e19f ? 1.3552527e-20f : temperature >= 1.f ? 0.5f : 1.f;  // 2^64: 2^-66
   const float t = temperature * h.unit;
   if (t < INFINITY) {
@@ -86,24 +88,18 @@ __device__ __forceinline__ Heat heat_of(float top, float temperature) {
   return h;
 }
 
-// 2^62 * exp((x - top) / T), x <= top, to 2^-41 of itself or 1.
+// 2^62 * 2^-((d + err) * log2(e) / T), d >= 0 and err its error, in the heat's unit, to 2^-41 of itself or 1.
 //
-// d = top - x is exact in two floats, y = d * log2(e) / T but for 2^-47 of it; with n = floor(y), y = n + j / 1024 + r, the
-// weight is 2^-n * table[j] * (1 + z + z^2 / 2 + z^3 / 6), z = -r ln 2, |z| < 2^-11.5, whose square fits one float.
-__device__ __forceinline__ uint64_t weight_of(const Heat& h, float x) {
-  if (x == h.top) return 1ull << kOne;
-  const float t = h.top * h.unit;
-  x *= h.unit;
-  const float d = __fsub_rn(t, x);
-  // the rounding of d (the sum of two floats and its error, by their six operations)
-  const float bx = __fsub_rn(t, d), err = __fadd_rn(__fsub_rn(t, __fadd_rn(d, bx)), __fsub_rn(bx, x));
+// y = (d + err) * log2(e) / T in two floats, to 2^-47 of it; with n = floor(y), y = n + j / 1024 + r, the weight is
+// 2^-n * table[j] * (1 + z + z^2 / 2 + z^3 / 6), z = -r ln 2, |z| < 2^-11.5, whose square fits one float.
+__device__ __forceinline__ uint64_t falling(const Heat& h, float d, float err) {
   const float p = __fmul_rn(d, h.hi);
   if (!(p < 126.f)) return 0;  // also where the largest is infinite
   const float e = fmaf(d, h.hi, -p) + (d * h.lo + err * h.hi);
-  const float n = floorf(p), f = __fsub_rn(p, n);              // exact
+  const float n = floorf(p), f = __fsub_rn(p, n);                     // exact
   const float j = rintf(f * 1024.f), r = fmaf(j, -0.0009765625f, f);  // exact, |r| <= 2^-11
   const int at = static_cast<int>(j);
-  const float th = __ldg(&kPowers.hi[at]), tl = __ldg(&kPowers.lo[at]);
+  const float th = h.powers->hi[at], tl = h.powers->lo[at];
   constexpr float kLn2 = 0.693147182464599609f, kLn2Lo = -1.90465429995776e-9f;
   const float z = __fmul_rn(r, -kLn2);
   const float zl = fmaf(r, -kLn2, -z) - fmaf(r, kLn2Lo, e * kLn2);
@@ -114,6 +110,15 @@ __device__ __forceinline__ uint64_t weight_of(const Heat& h, float x) {
   const float lo = sl + (al + fmaf(th, zl + q, fmaf(tl, z, tl)));
   const float scale = __int_as_float((127 + kOne - static_cast<int>(n)) << 23);
   return static_cast<uint64_t>(__float2ll_rn(s * scale) + __float2ll_rn(lo * scale));
+}
+
+// 2^62 * exp((x - top) / T), x <= top. top - x is exact as a float and its error (the six operations of an exact sum).
+__device__ __forceinline__ uint64_t weight_of(const Heat& h, float x) {
+  if (x == h.top) return 1ull << kOne;
+  const float t = h.top * h.unit;
+  x *= h.unit;
+  const float d = __fsub_rn(t, x), bx = __fsub_rn(t, d);
+  return falling(h, d, __fadd_rn(__fsub_rn(t, __fadd_rn(d, bx)), __fsub_rn(bx, x)));
 }
 
 __device__ __forceinline__ float to_float(u128 v) {
@@ -134,6 +139,12 @@ __device__ __forceinline__ int64_t quotient(u128 n, uint64_t d) {
 
 __device__ __forceinline__ u128 lesser(u128 a, u128 b) { return a < b ? a : b; }
 
+// log(w / kept), w <= kept.
+__device__ __forceinline__ float log_share(uint64_t w, u128 kept) {
+  const float whole = to_float(kept), rest = to_float(kept - w);
+  return rest < 0.5f * whole ? log1pf(-rest / whole) : logf(to_float(w) / whole);
+}
+
 // floor (or ceil) of v * total for v in [0, 1], total < 2^94.
 __device__ __forceinline__ u128 share_of(float v, u128 total, bool up) {
   if (v <= 0.f) return 0;
@@ -151,13 +162,16 @@ __device__ __forceinline__ u128 share_of(float v, u128 total, bool up) {
 // the NaNs are outside. -0 has a key of its own below that of 0 and counts as 0.
 template <typename T>
 struct Keys;
+// Step of a value to its neighbours: 2^(exponent - kBias) with the raw exponent field, 1 for those without one.
 template <>
 struct Keys<__nv_bfloat16> {
   static constexpr uint32_t kFloor = 0x007f, kTop = 0xff80;
+  static constexpr int kFraction = 7, kBias = 134;
 };
 template <>
 struct Keys<__half> {
   static constexpr uint32_t kFloor = 0x03ff, kTop = 0xfc00;
+  static constexpr int kFraction = 10, kBias = 25;
 };
 constexpr uint32_t kZero = 0x8000, kMinusZero = 0x7fff;
 
@@ -171,6 +185,13 @@ template <typename T>
 __device__ __forceinline__ float value_of(uint32_t key) {
   const uint32_t raw = key & 0x8000u ? key & 0x7fffu : ~key & 0xffffu;
   return Elem<T>::unpack(raw).x;
+}
+
+// The exponent field of a key's value, at least 1; the same for the 32 keys of a group, which differ in their last five bits.
+template <typename T>
+__device__ __forceinline__ int exponent_of(uint32_t key) {
+  const uint32_t raw = (key & 0x8000u ? key : ~key) & 0x7fffu;
+  return max(static_cast<int>(raw >> Keys<T>::kFraction), 1);
 }
 
 // The least key that x or a larger value may have.
@@ -213,21 +234,28 @@ struct Row {
   }
 };
 
-// f(vector, its number) for vectors from + lane, from + lane + step, ... below `to`; four loads on their way at a time.
-template <typename F>
+// f(vector, its number) for vectors from, from + step, ... below `to`; kAhead loads on their way at a time.
+template <int kAhead, typename F>
 __device__ __forceinline__ void each_vector(const Row& row, int32_t from, int32_t to, int32_t step, F f) {
   if (from < row.first && from < to) f(row.part(from), from);
   int32_t v = from < row.first ? from + step : from;
   const int32_t end = min(to, row.last);
-  for (; v + 3 * static_cast<int64_t>(step) < end; v += 4 * step) {
-    uint4 x[4];
+  for (; v + (kAhead - 1) * static_cast<int64_t>(step) < end; v += kAhead * step) {
+    uint4 x[kAhead];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = row.whole(v + i * step);
+    for (int i = 0; i < kAhead; ++i) x[i] = row.whole(v + i * step);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f(x[i], v + i * step);
+    for (int i = 0; i < kAhead; ++i) f(x[i], v + i * step);
   }
-  for (; v < end; v += step) f(row.whole(v), v);
-  if (v < to && v >= row.last) f(row.part(v), v);  // v == last: there is one vector behind
+  // the rest, in one go
+  uint4 x[kAhead - 1];
+#pragma unroll
+  for (int i = 0; i < kAhead - 1; ++i)
+    if (v + i * step < end) x[i] = row.whole(v + i * step);
+#pragma unroll
+  for (int i = 0; i < kAhead - 1; ++i)
+    if (v + i * step < end) f(x[i], v + i * step);
+  if (row.last < to && row.last >= from && (row.last - from) % step == 0 && row.last < row.vectors) f(row.part(row.last), row.last);
 }
 
 template <typename F>
@@ -282,13 +310,16 @@ __device__ __forceinline__ N block_scan(N v, N* part, N* total) {
 
 struct Shared {
   uint32_t bin[kBins];
+  PowerTable powers;
   // of a group of 32 bins: tokens before it (x, by its number), and the number of the n-th that has any (y, by n)
   uint2 group[kGroups];
   u128 part[kChunk];   // sums of a warp's groups
   u128 wide[kWarps];
   uint64_t scan[kWarps];
   uint32_t narrow[kWarps];
-  uint2 listed[kListed];  // index, key
+  // few tokens: key and complement of the index of each, and, in their order, that and the weight
+  uint64_t listed[kListed], sorted[kListed], weight[kListed];
+  uint32_t place[kListed];
   uint16_t ids[kFew];
   int32_t list_size, id_count;
   // the border to find and what was found, by one thread for all
@@ -301,6 +332,7 @@ struct Shared {
 
 struct Cuts {
   Heat heat;
+  uint32_t top;  // the largest key
   uint32_t top_k;
   uint64_t min_weight;
 };
@@ -323,6 +355,10 @@ __device__ __forceinline__ uint32_t among_first(uint32_t count, uint32_t rank, u
 
 // The counts of a round, bins 0 .. bins - 1 for keys first_key - bin, and their sums: over groups of 32 bins, of which
 // those that hold any tokens are shared out among the warps in order.
+//
+// first_key ends in five ones, so that a group's keys differ in their last five bits alone: its values are evenly spaced,
+// and their weights the group's first one times powers of one factor, which the groups of an exponent share. A weight then
+// costs a product of 62-bit integers; but for the first group, whose first values may be above the largest of the row.
 template <typename T>
 struct Round {
   uint32_t first_key;
@@ -333,14 +369,34 @@ struct Round {
 
   __device__ __forceinline__ int32_t begin(int warp) const { return filled * warp / kWarps; }
 
-  // This lane's tokens and their weight, of the n-th filled group.
-  __device__ __forceinline__ uint32_t tokens(const Shared& sm, const Cuts& c, int n, int* bin, uint64_t* w) const {
+  __device__ __forceinline__ uint32_t group_key(uint32_t g) const { return first_key - 32 * g; }
+
+  // This lane's tokens of group g, among the first top_k.
+  __device__ __forceinline__ uint32_t tokens(const Shared& sm, const Cuts& c, uint32_t g) const {
+    const uint32_t count = sm.bin[32 * g + (threadIdx.x & 31)];
+    return c.top_k != 0xffffffffu ? among_first(count, sm.group[g].x, c.top_k) : count;
+  }
+  // Weight of a group's first value, and of `lane` steps at an exponent in units of 2^-62.
+  __device__ __forceinline__ uint64_t first_weight(const Cuts& c, uint32_t g) const {
+    return g == 0 && first_key >= c.top ? 0 : weight_of(c.heat, value_of<T>(group_key(g)));
+  }
+  __device__ __forceinline__ uint64_t steps(const Cuts& c, int exponent) const {
+    return falling(c.heat, ldexpf(static_cast<float>(threadIdx.x & 31), exponent - Keys<T>::kBias) * c.heat.unit, 0.f);
+  }
+  __device__ __forceinline__ uint64_t weight(const Cuts& c, uint32_t g, uint64_t first, uint64_t step) const {
+    if (g == 0 && first_key >= c.top) {
+      const uint32_t key = first_key - (threadIdx.x & 31);
+      return key <= c.top ? weight_of(c.heat, value_of<T>(key)) : 0;
+    }
+    return static_cast<uint64_t>((static_cast<u128>(first) * step) >> kOne);
+  }
+
+  // This lane's tokens and their weight in the n-th filled group.
+  __device__ __forceinline__ uint32_t at(const Shared& sm, const Cuts& c, int n, int* bin, uint64_t* w) const {
     const uint32_t g = sm.group[n].y;
     *bin = 32 * static_cast<int>(g) + (threadIdx.x & 31);
-    uint32_t count = sm.bin[*bin];
-    if (c.top_k != 0xffffffffu) count = among_first(count, sm.group[g].x, c.top_k);
-    *w = count != 0u ? weight_of(c.heat, value_of<T>(first_key - *bin)) : 0;
-    return count;
+    *w = weight(c, g, first_weight(c, g), steps(c, exponent_of<T>(group_key(g))));
+    return tokens(sm, c, g);
   }
 
   // Adds the round's tokens, weights, and weights of at least min_weight to the three sums.
@@ -361,27 +417,40 @@ struct Round {
       size[i] = n == 0u ? 0 : (1ull << 32) + n;
       mine += size[i];
     }
-    uint64_t at = block_scan(mine, sm.scan, &all);
+    uint64_t place = block_scan(mine, sm.scan, &all);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int g = kPer * threadIdx.x + i;
       if (size[i] != 0) {
-        sm.group[g].x = ranks + static_cast<uint32_t>(at);
-        sm.group[at >> 32].y = g;
+        sm.group[g].x = ranks + static_cast<uint32_t>(place);
+        sm.group[place >> 32].y = g;
       }
-      at += size[i];
+      place += size[i];
     }
     filled = static_cast<int32_t>(all >> 32);
     ranks += static_cast<uint32_t>(all);
     __syncthreads();
     u128 mine_sum = 0, mine_above = 0;
-    for (int n = begin(warp); n < begin(warp + 1); ++n) {
-      int bin;
-      uint64_t w;
-      const uint32_t count = tokens(sm, c, n, &bin, &w);
-      const u128 part = static_cast<u128>(w) * count;
-      mine_sum += part;
-      if (w >= c.min_weight) mine_above += part;
+    int exponent = 0;
+    uint64_t step = 0;
+    for (int n0 = begin(warp); n0 < begin(warp + 1); n0 += 32) {
+      const int n = min(32, begin(warp + 1) - n0);
+      // each lane the first weight of a group
+      const uint32_t my_group = lane < n ? sm.group[n0 + lane].y : 0u;
+      const uint64_t my_first = lane < n ? first_weight(c, my_group) : 0;
+      for (int i = 0; i < n; ++i) {
+        const uint32_t g = __shfl_sync(0xffffffffu, my_group, i);
+        const uint64_t first = __shfl_sync(0xffffffffu, my_first, i);
+        const int e = exponent_of<T>(group_key(g));
+        if (e != exponent) {
+          exponent = e;
+          step = steps(c, e);
+        }
+        const uint64_t w = weight(c, g, first, step);
+        const u128 part = static_cast<u128>(w) * tokens(sm, c, g);
+        mine_sum += part;
+        if (w >= c.min_weight) mine_above += part;
+      }
     }
     mine_sum = warp_sum(mine_sum);
     __syncthreads();
@@ -409,13 +478,13 @@ struct Round {
     if (in == 0u) return false;
     const int who = __ffs(in) - 1, first = begin(who), n = begin(who + 1) - first;
     u128 upto = broadcast(before, who);
-    int at = first;
+    int n_at = first;
     if (n > 1) {
       // the sums of that warp's groups, one to a warp
       for (int i = warp; i < n; i += kWarps) {
         int bin;
         uint64_t w;
-        const uint32_t count = tokens(sm, c, first + i, &bin, &w);
+        const uint32_t count = at(sm, c, first + i, &bin, &w);
         const u128 s = warp_sum(static_cast<u128>(w) * count);
         if (lane == 0) sm.part[i] = s;
       }
@@ -425,7 +494,7 @@ struct Round {
         const uint32_t hit = __ballot_sync(0xffffffffu, incl > border);
         if (hit != 0u) {
           const int l = __ffs(hit) - 1;
-          at = first + i0 + l;
+          n_at = first + i0 + l;
           upto = broadcast(incl - s, l);
           break;
         }
@@ -436,7 +505,7 @@ struct Round {
     if (warp == 0) {
       int bin;
       uint64_t w;
-      const uint32_t count = tokens(sm, c, at, &bin, &w);
+      const uint32_t count = at(sm, c, n_at, &bin, &w);
       const u128 part = static_cast<u128>(w) * count, incl = upto + warp_scan(part);
       const uint32_t hit = __ballot_sync(0xffffffffu, incl > border);
       if (lane == __ffs(hit) - 1) found(bin, w, incl - part);
@@ -445,6 +514,76 @@ struct Round {
     return true;
   }
 };
+
+// The whole of the choice among n tokens that are listed, n <= kListed.
+template <typename T>
+__device__ __forceinline__ void sample_listed(Shared& sm, const Cuts& c, int n, float top_p, float u, int64_t* token, float* logprob) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  // Each token's place is the number of those ahead of it, counted by teams of threads that share the others.
+  int wide = 32;
+  while (wide < n) wide *= 2;
+  const int parts = kThreads / wide, me = tid & (wide - 1), part = tid / wide;
+  if (me < n) {
+    const uint64_t mine = sm.listed[me];
+    int ahead = 0;
+    for (int j = part; j < n; j += parts) ahead += sm.listed[j] > mine;
+    atomicAdd(&sm.place[me], ahead);
+  }
+  __syncthreads();
+  if (tid < n) {
+    const uint64_t mine = sm.listed[tid];
+    const uint32_t at = sm.place[tid];
+    sm.sorted[at] = mine;
+    sm.weight[at] = at < c.top_k ? weight_of(c.heat, value_of<T>(static_cast<uint32_t>(mine >> 32))) : 0;
+  }
+  __syncthreads();
+  if (tid >= 32) return;
+  // Each lane a run of the order.
+  constexpr int kRun = kListed / 32;
+  const int run = (n + 31) / 32, first = lane * run, last = min(first + run, n);
+  uint64_t w[kRun];
+  u128 mine = 0;
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) {
+    w[i] = i < run && first + i < last ? sm.weight[first + i] : 0;
+    mine += w[i];
+  }
+  const u128 upto = warp_scan(mine), total = broadcast(upto, 31), before = upto - mine;
+  u128 kept = total;
+  if (c.min_weight > 0) {
+    u128 above = 0;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i)
+      if (w[i] >= c.min_weight) above += w[i];
+    kept = warp_sum(above);
+  }
+  // The running sum up to and with the token that passes `border`; its place, weight.
+  int at = 0;
+  uint64_t weight = 0;
+  auto pass = [&](u128 border) {
+    const int who = __ffs(__ballot_sync(0xffffffffu, before <= border && border < upto)) - 1;
+    u128 sum = before;
+    int found = -1;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i)
+      if (found < 0) {
+        sum += w[i];
+        if (sum > border) found = i;
+      }
+    at = __shfl_sync(0xffffffffu, first + max(found, 0), who);
+    weight = sm.weight[at];
+    return broadcast(sum, who);
+  };
+  if (top_p < 1.f) {
+    const u128 goal = share_of(fmaxf(top_p, 0.f), total, true);
+    kept = lesser(kept, pass(goal > 0 ? goal - 1 : 0));
+  }
+  pass(share_of(u, kept, false));
+  if (lane == 0) {
+    *token = static_cast<int64_t>(~static_cast<uint32_t>(sm.sorted[at]));
+    if (logprob != nullptr) *logprob = log_share(weight, kept);
+  }
+}
 
 // f(vector, its number) for the vectors of the threads for which `mine` is true (n of them, at most kFew), spread over all
 // threads. To be called by every thread.
@@ -470,23 +609,25 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
   Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
+  for (int i = tid; i < static_cast<int>(sizeof(PowerTable) / 4); i += kThreads)
+    reinterpret_cast<float*>(&sm.powers)[i] = __ldg(reinterpret_cast<const float*>(&kPowers) + i);
   pdl_wait();
   const int32_t b = blockIdx.x;
   const Row row(a.logits + b * a.stride, a.V);
   const float temperature = a.temperature == nullptr ? 1.f : a.temperature[b];
   const int32_t k = a.top_k == nullptr ? 0 : a.top_k[b];
   const float top_p = a.top_p == nullptr ? 1.f : a.top_p[b], min_p = a.min_p == nullptr ? 0.f : a.min_p[b],
-              u = a.u[b];
+              given = a.u[b], u = given > 0.f ? fminf(given, 0.999999940395355225f) : 0.f;
 
   // ------------------------------------------------------------------- the largest value
   uint32_t two = 0, own;  // of this thread's vectors tid, tid + 1024, ...
-  each_vector(row, tid, row.vectors, kThreads, [&](const uint4& v, int32_t) {
+  each_vector<4>(row, tid, row.vectors, kThreads, [&](const uint4& v, int32_t) {
     two = __vmaxu2(two, __vmaxu2(__vmaxu2(two_keys(v.x), two_keys(v.y)), __vmaxu2(two_keys(v.z), two_keys(v.w))));
   });
   own = max(two & 0xffffu, two >> 16);
   if (own > Keys<T>::kTop) {  // NaN among them
     own = 0;
-    each_vector(row, tid, row.vectors, kThreads, [&](const uint4& v, int32_t) {
+    each_vector<4>(row, tid, row.vectors, kThreads, [&](const uint4& v, int32_t) {
       each_key(v, [&](uint32_t s, int) {
         if (s <= Keys<T>::kTop) own = max(own, s);
       });
@@ -513,10 +654,10 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
   uint32_t key = top;
   int32_t nth = 0;
   float logprob = 0.f;
-  bool few = false;  // the tokens that count are listed
   if (temperature >= 1.17549435e-38f && k != 1) {
     Cuts c;
-    c.heat = heat_of(value_of<T>(top), temperature);
+    c.heat = heat_of(value_of<T>(top), temperature, &sm.powers);
+    c.top = top;
     c.top_k = k <= 0 ? 0xffffffffu : static_cast<uint32_t>(k);
     c.min_weight = min_p > 0.f ? static_cast<uint64_t>(share_of(fminf(min_p, 1.f), static_cast<u128>(1) << kOne, true)) : 0;
     // Which keys count at all. Weights below exp(-45) of the largest are 0 in units of 2^-62; those below min_p matter to
@@ -551,37 +692,50 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
       }
     }
     if (floor_key == kZero) floor_key = kMinusZero;
-    const int bins = static_cast<int>(top - floor_key) + 1, rounds = (bins + kBins - 1) / kBins;
-    const int counted = __syncthreads_count(own >= floor_key);
-    few = counted <= kFew && rounds == 1;
+    const uint32_t first_bin = top | 31u;
+    const int bins = static_cast<int>(first_bin - floor_key) + 1, rounds = (bins + kBins - 1) / kBins;
+    const int looked_at = __syncthreads_count(own >= floor_key);
+    if (looked_at <= kFew) {
+      if (tid < kListed) sm.place[tid] = 0;
+      each_of_few(sm, row, own >= floor_key, looked_at, [&](const uint4& v, int32_t at) {
+        const uint32_t most = __vmaxu2(__vmaxu2(two_keys(v.x), two_keys(v.y)), __vmaxu2(two_keys(v.z), two_keys(v.w)));
+        if (max(most & 0xffffu, most >> 16) < floor_key) return;
+        each_key(v, [&](uint32_t s, int i) {
+          if (s == kMinusZero) s = kZero;
+          if (s < floor_key || s > top) return;  // above the largest: NaN
+          const int place = atomicAdd(&sm.list_size, 1);
+          if (place < kListed) sm.listed[place] = (static_cast<uint64_t>(s) << 32) | ~static_cast<uint32_t>(8 * at - row.skip + i);
+        });
+      });
+      __syncthreads();
+      if (sm.list_size <= kListed) {
+        sample_listed<T>(sm, c, sm.list_size, top_p, u, a.token + b, a.logprob == nullptr ? nullptr : a.logprob + b);
+        return;
+      }
+    }
 
     Round<T> round;
     auto count = [&](int r) {
-      round.first_key = top - kBins * r;
+      round.first_key = first_bin - kBins * r;
       round.bins = min(kBins, bins - kBins * r);
       __syncthreads();  // the last round's readers are through
       for (int i = tid; i < (round.bins + 31) / 32 * 8; i += kThreads) reinterpret_cast<uint4*>(sm.bin)[i] = make_uint4(0u, 0u, 0u, 0u);
       __syncthreads();
       const uint32_t first_key = round.first_key, n = static_cast<uint32_t>(round.bins);
-      if (few) {
-        each_of_few(sm, row, own >= floor_key, counted, [&](const uint4& v, int32_t at) {
-          each_key(v, [&](uint32_t s, int i) {
-            if (s == kMinusZero) s = kZero;
-            if (first_key - s >= n) return;  // larger keys (NaN) wrap around
-            atomicAdd(&sm.bin[first_key - s], 1u);
-            const int place = atomicAdd(&sm.list_size, 1);
-            if (place < kListed) sm.listed[place] = make_uint2(static_cast<uint32_t>(8 * at - row.skip + i), s);
-          });
-        });
-      } else if (own >= floor_key) {
-        each_vector(row, tid, row.vectors, kThreads, [&](const uint4& v, int32_t) {
+      if (own >= floor_key) {
+        each_vector<4>(row, tid, row.vectors, kThreads, [&](const uint4& v, int32_t) {
           each_key(v, [&](uint32_t s, int) {
             if (s == kMinusZero) s = kZero;
-            if (first_key - s < n) atomicAdd(&sm.bin[first_key - s], 1u);
+            if (first_key - s < n)  // keys of the rounds before wrap around
+              atomicAdd(&sm.bin[first_key - s], 1u);
           });
         });
       }
       __syncthreads();
+      if (r == 0 && first_bin > Keys<T>::kTop) {  // bins above the largest are those of NaN
+        if (tid < static_cast<int>(first_bin - top)) sm.bin[tid] = 0u;
+        __syncthreads();
+      }
     };
     uint32_t ranks = 0;
     u128 total = 0, above = 0;
@@ -603,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
     };
     // Borders and what lies at them: 128-bit arithmetic, by one thread.
     auto aim = [&] {
-      sm.border = share_of(u > 0.f ? fminf(u, 0.999999940395355225f) : 0.f, sm.kept, false);
+      sm.border = share_of(u, sm.kept, false);
     };
     if (tid == 0) {
       sm.kept = c.min_weight > 0 ? lesser(total, above) : total;
@@ -627,31 +781,23 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
       return round.find(sm, c, [&](int bin, uint64_t w, u128 ahead) {
         sm.key = round.first_key - bin;
         sm.nth = static_cast<int32_t>(quotient(sm.border - ahead, w));
-        const float whole = to_float(sm.kept), rest = to_float(sm.kept - w);
-        sm.logprob = rest < 0.5f * whole ? log1pf(-rest / whole) : logf(to_float(w) / whole);
+        sm.logprob = log_share(w, sm.kept);
       });
     });
     key = sm.key;
     nth = sm.nth;
     logprob = sm.logprob;
-    few = few && sm.list_size <= kListed;
   }
 
   // ------------------------------------------------------- the nth element of that value
   const uint32_t twin = key == kZero ? kMinusZero : key;
-  if (few) {
-    const int n = sm.list_size;
-    const uint2 me = tid < n ? sm.listed[tid] : make_uint2(0u, 0u);
-    if (tid < n && me.y == key) {
-      int32_t ahead = 0;
-      for (int i = 0; i < n; ++i) ahead += sm.listed[i].y == key && sm.listed[i].x < me.x;
-      if (ahead == nth) {
-        a.token[b] = me.x;
-        if (a.logprob != nullptr) a.logprob[b] = logprob;
-      }
-    }
-    return;
-  }
+  // Vectors without that value are passed by: the least of (x ^ value) over a vector's low and high halves is not 0.
+  // (The zeros of both signs differ in a bit that is left out.)
+  const uint32_t pair = (key & 0x8000u ? key & 0x7fffu : ~key & 0xffffu) * 0x10001u, bits_used = key == kZero ? 0x7fff7fffu : 0xffffffffu;
+  auto holds = [&](const uint4& v) {
+    const uint32_t x = __vminu2(__vminu2((v.x ^ pair) & bits_used, (v.y ^ pair) & bits_used), __vminu2((v.z ^ pair) & bits_used, (v.w ^ pair) & bits_used));
+    return (x & 0xffffu) == 0u || x < 0x10000u;
+  };
   if (key == top && nth == 0) {
     // The least index of those threads that have it, if they are few.
     const int n = __syncthreads_count(own == top);
@@ -677,7 +823,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
   // Each warp takes an equal run of vectors: how many it has, then the run with the nth.
   const int32_t run = (row.vectors + kWarps - 1) / kWarps, v0 = min(row.vectors, warp * run), v1 = min(row.vectors, v0 + run);
   uint32_t mine = 0;
-  each_vector(row, v0 + lane, v1, 32, [&](const uint4& v, int32_t) { each_key(v, [&](uint32_t s, int) { mine += s == key || s == twin; }); });
+  each_vector<4>(row, v0 + lane, v1, 32, [&](const uint4& v, int32_t) {
+    if (holds(v)) each_key(v, [&](uint32_t s, int) { mine += s == key || s == twin; });
+  });
   mine = __reduce_add_sync(0xffffffffu, mine);
   __syncthreads();
   if (lane == 0) sm.narrow[warp] = mine;
