@@ -346,6 +346,25 @@ __device__ __forceinline__ u128 warp_sum(u128 v) {
   return sum;
 }
 
+// A sum of weights times counts (together below 2^31), in two limbs: weights have 62 bits, and one instruction multiplies
+// 32 and adds 64.
+struct Sum {
+  uint64_t lo = 0, hi = 0;
+  __device__ __forceinline__ void add(uint64_t w, uint32_t count) {
+    lo += static_cast<uint64_t>(static_cast<uint32_t>(w) & 0x7fffffffu) * count;
+    hi += static_cast<uint64_t>(static_cast<uint32_t>(w >> 31)) * count;
+  }
+  __device__ __forceinline__ u128 whole() const { return (static_cast<u128>(hi) << 31) + lo; }
+};
+
+// a * b / 2^62 of numbers up to 2^62, rounded down but for 1; the low limbs' product is below that.
+__device__ __forceinline__ uint64_t product62(uint64_t a, uint64_t b) {
+  const uint32_t a0 = static_cast<uint32_t>(a) & 0x7fffffffu, a1 = static_cast<uint32_t>(a >> 31);
+  const uint32_t b0 = static_cast<uint32_t>(b) & 0x7fffffffu, b1 = static_cast<uint32_t>(b >> 31);
+  const uint64_t cross = static_cast<uint64_t>(a1) * b0 + static_cast<uint64_t>(a0) * b1;
+  return static_cast<uint64_t>(a1) * b1 + (cross >> 31);
+}
+
 // This lane's tokens of a group (`count` in its bin, `rank` before the group) that are among the first top_k.
 __device__ __forceinline__ uint32_t among_first(uint32_t count, uint32_t rank, uint32_t top_k) {
   if (rank >= top_k) return 0;
@@ -388,7 +407,7 @@ struct Round {
       const uint32_t key = first_key - (threadIdx.x & 31);
       return key <= c.top ? weight_of(c.heat, value_of<T>(key)) : 0;
     }
-    return static_cast<uint64_t>((static_cast<u128>(first) * step) >> kOne);
+    return product62(first, step);
   }
 
   // This lane's tokens and their weight in the n-th filled group.
@@ -402,18 +421,20 @@ struct Round {
   // Adds the round's tokens, weights, and weights of at least min_weight to the three sums.
   __device__ __forceinline__ void add_up(Shared& sm, const Cuts& c, uint32_t& ranks, u128& total, u128& above) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, groups = (bins + 31) / 32;
-#pragma unroll 4
-    for (int g = warp; g < groups; g += kWarps) {
-      const uint32_t n = __reduce_add_sync(0xffffffffu, sm.bin[32 * g + lane]);
-      if (lane == 0) sm.group[g].x = n;
-    }
-    __syncthreads();
     // tokens in the low half, filled groups in the high half
     uint64_t size[kPer], mine = 0, all;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int g = kPer * threadIdx.x + i;
-      const uint32_t n = g < groups ? sm.group[g].x : 0u;
+      uint32_t n = 0;
+      if (g < groups) {
+        const uint4* in = reinterpret_cast<const uint4*>(sm.bin + 32 * g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 v = in[(j + lane) & 7];  // eight lanes read different banks
+          n += v.x + v.y + v.z + v.w;
+        }
+      }
       size[i] = n == 0u ? 0 : (1ull << 32) + n;
       mine += size[i];
     }
@@ -430,7 +451,7 @@ struct Round {
     filled = static_cast<int32_t>(all >> 32);
     ranks += static_cast<uint32_t>(all);
     __syncthreads();
-    u128 mine_sum = 0, mine_above = 0;
+    Sum sums, sums_above;
     int exponent = 0;
     uint64_t step = 0;
     for (int n0 = begin(warp); n0 < begin(warp + 1); n0 += 32) {
@@ -447,12 +468,12 @@ struct Round {
           step = steps(c, e);
         }
         const uint64_t w = weight(c, g, first, step);
-        const u128 part = static_cast<u128>(w) * tokens(sm, c, g);
-        mine_sum += part;
-        if (w >= c.min_weight) mine_above += part;
+        const uint32_t count = tokens(sm, c, g);
+        sums.add(w, count);
+        if (c.min_weight > 0 && w >= c.min_weight) sums_above.add(w, count);
       }
     }
-    mine_sum = warp_sum(mine_sum);
+    const u128 mine_sum = warp_sum(sums.whole());
     __syncthreads();
     if (lane == 0) sm.wide[warp] = mine_sum;
     __syncthreads();
@@ -460,7 +481,7 @@ struct Round {
     before = total + warp_scan(sum) - sum;
     total += warp_sum(sum);
     if (c.min_weight > 0) {
-      mine_above = warp_sum(mine_above);
+      const u128 mine_above = warp_sum(sums_above.whole());
       __syncthreads();
       if (lane == 0) sm.wide[warp] = mine_above;
       __syncthreads();
@@ -603,8 +624,31 @@ __device__ __forceinline__ void each_of_few(Shared& sm, const Row& row, bool min
   }
 }
 
+// Whether every token of a row counts (no top-k that bounds them, nor a min-p alone): such a row takes about four times as
+// long as others.
+__device__ __forceinline__ bool is_long(const SampleArgs& a, int32_t b) {
+  const int32_t k = a.top_k == nullptr ? 0 : __ldg(a.top_k + b);
+  const float top_p = a.top_p == nullptr ? 1.f : __ldg(a.top_p + b), min_p = a.min_p == nullptr ? 0.f : __ldg(a.min_p + b);
+  return (k <= 0 || k > kThreads) && (a.temperature == nullptr || __ldg(a.temperature + b) > 0.f) && (top_p < 1.f || !(min_p > 0.f));
+}
+
+// The i-th row, the long ones first. For at most kThreads rows.
+__device__ __forceinline__ int32_t row_of(const SampleArgs& a, Shared& sm, int32_t i) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  const bool slow = tid < a.B && is_long(a, tid);
+  const uint32_t in = __ballot_sync(0xffffffffu, slow);
+  if (lane == 0) sm.narrow[tid >> 5] = __popc(in);
+  __syncthreads();
+  const uint32_t mine = sm.narrow[lane], upto = warp_scan(mine), all = __shfl_sync(0xffffffffu, upto, 31);
+  const int32_t ahead = __shfl_sync(0xffffffffu, upto - mine, tid >> 5) + __popc(in & ((1u << lane) - 1u));
+  const int32_t place = slow ? ahead : static_cast<int32_t>(all) + tid - ahead;
+  if (tid < a.B && place == i) sm.index = tid;
+  __syncthreads();
+  return sm.index;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a, bool ordered) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -612,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
   for (int i = tid; i < static_cast<int>(sizeof(PowerTable) / 4); i += kThreads)
     reinterpret_cast<float*>(&sm.powers)[i] = __ldg(reinterpret_cast<const float*>(&kPowers) + i);
   pdl_wait();
-  const int32_t b = blockIdx.x;
+  const int32_t b = ordered ? row_of(a, sm, blockIdx.x) : static_cast<int32_t>(blockIdx.x);
   const Row row(a.logits + b * a.stride, a.V);
   const float temperature = a.temperature == nullptr ? 1.f : a.temperature[b];
   const int32_t k = a.top_k == nullptr ? 0 : a.top_k[b];
@@ -635,6 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a)
   }
   if (own == kMinusZero) own = kZero;
   uint32_t top = __reduce_max_sync(0xffffffffu, own);
+  __syncthreads();
   if (lane == 0) sm.narrow[warp] = top;
   if (tid == 0) {
     sm.list_size = 0;
@@ -858,7 +903,9 @@ bool launch(const SampleArgs& a, cudaStream_t s) {
   constexpr size_t smem = sizeof(Shared);
   static_assert(smem <= 227 * 1024, "the bins fit the SM");
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(sample_kernel<T>), smem)) return false;
-  launch_overlapped(sample_kernel<T>, dim3(static_cast<unsigned>(a.B)), kThreads, smem, 1, s, a);
+  // More rows than SMs: the long ones go first, or the last of them is waited for.
+  const bool ordered = a.B > sm_count() && a.B <= kThreads;
+  launch_overlapped(sample_kernel<T>, dim3(static_cast<unsigned>(a.B)), kThreads, smem, 1, s, a, ordered);
   return true;
 }
 
