@@ -26,7 +26,9 @@ constexpr int kBins = 49152;          // 192 KB; values further below the larges
 constexpr int kGroups = kBins / 32;   // a warp's bins at a time
 constexpr int kPer = 2;               // groups of a thread in the sums over them
 static_assert(kPer * kThreads >= kGroups, "every group has a thread");
-constexpr int kChunk = (kGroups + kWarps - 1) / kWarps;  // groups of a warp
+constexpr int kBatches = kGroups / 32;  // of 32 groups, one to a lane; two of them to a warp at most
+static_assert(kBatches <= 2 * kWarps && kBatches > kWarps, "two batches a warp");
+constexpr int kExponents = 32;        // below the largest of a row, whose steps are in a table
 constexpr int kFew = 256;             // threads whose part of the row is looked at again
 constexpr int kListed = 256;          // tokens that are sorted where few count
 constexpr int kOne = 62;              // weights are integers, 2^62 the largest
@@ -313,13 +315,19 @@ struct Shared {
   PowerTable powers;
   // of a group of 32 bins: tokens before it (x, by its number), and the number of the n-th that has any (y, by n)
   uint2 group[kGroups];
-  u128 part[kChunk];   // sums of a warp's groups
+  u128 batch[kBatches];  // sums of 32 filled groups
   u128 wide[kWarps];
   uint64_t scan[kWarps];
   uint32_t narrow[kWarps];
-  // few tokens: key and complement of the index of each, and, in their order, that and the weight
-  uint64_t listed[kListed], sorted[kListed], weight[kListed];
-  uint32_t place[kListed];
+  union {
+    // few tokens: key and complement of the index of each, and, in their order, that and the weight
+    struct {
+      uint64_t listed[kListed], sorted[kListed], weight[kListed];
+      uint32_t place[kListed];
+    };
+    // else: what a value's weight loses in 0 to 31 steps of an exponent, in two limbs of 31 bits
+    uint2 steps[kExponents][32];
+  };
   uint16_t ids[kFew];
   int32_t list_size, id_count;
   // the border to find and what was found, by one thread for all
@@ -373,56 +381,92 @@ __device__ __forceinline__ uint32_t among_first(uint32_t count, uint32_t rank, u
 }
 
 // The counts of a round, bins 0 .. bins - 1 for keys first_key - bin, and their sums: over groups of 32 bins, of which
-// those that hold any tokens are shared out among the warps in order.
+// those that hold any tokens are shared out, in order, a group to a lane.
 //
 // first_key ends in five ones, so that a group's keys differ in their last five bits alone: its values are evenly spaced,
-// and their weights the group's first one times powers of one factor, which the groups of an exponent share. A weight then
-// costs a product of 62-bit integers; but for the first group, whose first values may be above the largest of the row.
+// and their weights the group's first one times powers of one factor, which the groups of an exponent share. A lane so adds
+// up counts times steps, two instructions a bin, and multiplies by the group's first weight once. (A weight for each bin by
+// itself took 90 instructions of each lane, 20 of the 29 thousand clocks of a row of 151936 fp16 logits.) Bins are taken
+// one by one where that does not do: in the first group, whose first values may be above the largest of the row, in one that
+// top-k or min-p cuts, and at exponents 2^-32 of the largest. A group's sum and the sum over its bins may differ in the last
+// of 62 bits of each.
 template <typename T>
 struct Round {
   uint32_t first_key;
   int bins;
+  int least;            // the lowest exponent in the table
   int32_t filled;       // groups with tokens
-  u128 before;          // sum before the lane-th warp's groups, and of them
-  u128 sum;
-
-  __device__ __forceinline__ int32_t begin(int warp) const { return filled * warp / kWarps; }
+  u128 before, mine[2];  // sum before the round, and of this lane's groups
 
   __device__ __forceinline__ uint32_t group_key(uint32_t g) const { return first_key - 32 * g; }
-
-  // This lane's tokens of group g, among the first top_k.
-  __device__ __forceinline__ uint32_t tokens(const Shared& sm, const Cuts& c, uint32_t g) const {
-    const uint32_t count = sm.bin[32 * g + (threadIdx.x & 31)];
-    return c.top_k != 0xffffffffu ? among_first(count, sm.group[g].x, c.top_k) : count;
+  __device__ __forceinline__ bool even(const Cuts& c, uint32_t g) const {
+    return group_key(g) <= c.top && exponent_of<T>(group_key(g)) >= least;
   }
-  // Weight of a group's first value, and of `lane` steps at an exponent in units of 2^-62.
-  __device__ __forceinline__ uint64_t first_weight(const Cuts& c, uint32_t g) const {
-    return g == 0 && first_key >= c.top ? 0 : weight_of(c.heat, value_of<T>(group_key(g)));
-  }
-  __device__ __forceinline__ uint64_t steps(const Cuts& c, int exponent) const {
-    return falling(c.heat, ldexpf(static_cast<float>(threadIdx.x & 31), exponent - Keys<T>::kBias) * c.heat.unit, 0.f);
-  }
-  __device__ __forceinline__ uint64_t weight(const Cuts& c, uint32_t g, uint64_t first, uint64_t step) const {
-    if (g == 0 && first_key >= c.top) {
-      const uint32_t key = first_key - (threadIdx.x & 31);
-      return key <= c.top ? weight_of(c.heat, value_of<T>(key)) : 0;
+  // Weight of bin `i` of a group with that first weight.
+  __device__ __forceinline__ uint64_t weight(const Shared& sm, const Cuts& c, uint32_t g, int i, uint64_t first) const {
+    if (even(c, g)) {
+      const uint2 step = sm.steps[exponent_of<T>(group_key(g)) - least][i];
+      return product62(first, (static_cast<uint64_t>(step.y) << 31) + step.x);
     }
-    return product62(first, step);
+    const uint32_t key = group_key(g) - i;
+    return key <= c.top ? weight_of(c.heat, value_of<T>(key)) : 0;
+  }
+  __device__ __forceinline__ uint64_t first_weight(const Cuts& c, uint32_t g) const {
+    return even(c, g) ? weight_of(c.heat, value_of<T>(group_key(g))) : 0;
   }
 
-  // This lane's tokens and their weight in the n-th filled group.
-  __device__ __forceinline__ uint32_t at(const Shared& sm, const Cuts& c, int n, int* bin, uint64_t* w) const {
-    const uint32_t g = sm.group[n].y;
-    *bin = 32 * static_cast<int>(g) + (threadIdx.x & 31);
-    *w = weight(c, g, first_weight(c, g), steps(c, exponent_of<T>(group_key(g))));
-    return tokens(sm, c, g);
+  // The sum of a group's weights, `rank` tokens before it, and that of the weights of at least min_weight; for a lane's
+  // group each, or, where a lane's is to be taken bin by bin, by the warp. To be called by whole warps.
+  __device__ __forceinline__ u128 sum_of(const Shared& sm, const Cuts& c, bool any, uint32_t g, uint32_t rank, u128* above) const {
+    const int lane = threadIdx.x & 31;
+    const uint32_t* count = sm.bin + 32 * g;
+    const uint64_t first = any ? first_weight(c, g) : 0;
+    any = any && rank < c.top_k;
+    bool apart = any && !even(c, g);
+    if (c.top_k != 0xffffffffu && any && !apart) {
+      uint32_t n = 0;
+      for (int i = 0; i < 32; ++i) n += count[(i + lane) & 31];
+      apart = n > c.top_k - rank;
+    }
+    const bool low = first < c.min_weight;  // none reaches min_weight
+    if (c.min_weight > 0 && any && !apart && !low) apart = weight(sm, c, g, 31, first) < c.min_weight;
+    u128 total = 0;
+    if (any && !apart) {
+      const uint2* step = sm.steps[exponent_of<T>(group_key(g)) - least];
+      Sum sum;
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) {
+        const int at = (i + lane) & 31;  // lanes read different banks
+        const uint32_t n = count[at];
+        const uint2 s = step[at];
+        sum.lo += static_cast<uint64_t>(s.x) * n;
+        sum.hi += static_cast<uint64_t>(s.y) * n;
+      }
+      // first * (hi * 2^31 + lo) / 2^62, in limbs of 31 bits of the first: 2^62 * 2^31 a product at most
+      const uint32_t f0 = static_cast<uint32_t>(first) & 0x7fffffffu, f1 = static_cast<uint32_t>(first >> 31);
+      const u128 whole = sum.whole();
+      total = (whole * f1 + ((whole * f0) >> 31)) >> 31;
+      if (!low) *above += total;
+    }
+    for (uint32_t todo = __ballot_sync(0xffffffffu, apart); todo != 0u; todo &= todo - 1) {
+      const int who = __ffs(todo) - 1;
+      const uint32_t its = __shfl_sync(0xffffffffu, g, who), ahead = __shfl_sync(0xffffffffu, rank, who);
+      const uint32_t held = sm.bin[32 * its + lane], n = c.top_k != 0xffffffffu ? among_first(held, ahead, c.top_k) : held;
+      const uint64_t w = n != 0u ? weight(sm, c, its, lane, first_weight(c, its)) : 0;
+      const u128 part = static_cast<u128>(w) * n, all = warp_sum(part), some = warp_sum(w >= c.min_weight ? part : 0);
+      if (lane == who) {
+        total = all;
+        *above += some;
+      }
+    }
+    return total;
   }
 
   // Adds the round's tokens, weights, and weights of at least min_weight to the three sums.
   __device__ __forceinline__ void add_up(Shared& sm, const Cuts& c, uint32_t& ranks, u128& total, u128& above) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, groups = (bins + 31) / 32;
     // tokens in the low half, filled groups in the high half
-    uint64_t size[kPer], mine = 0, all;
+    uint64_t size[kPer], own = 0, all;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int g = kPer * threadIdx.x + i;
@@ -436,9 +480,9 @@ struct Round {
         }
       }
       size[i] = n == 0u ? 0 : (1ull << 32) + n;
-      mine += size[i];
+      own += size[i];
     }
-    uint64_t place = block_scan(mine, sm.scan, &all);
+    uint64_t place = block_scan(own, sm.scan, &all);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int g = kPer * threadIdx.x + i;
@@ -450,86 +494,67 @@ struct Round {
     }
     filled = static_cast<int32_t>(all >> 32);
     ranks += static_cast<uint32_t>(all);
+    before = total;
     __syncthreads();
-    Sum sums, sums_above;
-    int exponent = 0;
-    uint64_t step = 0;
-    for (int n0 = begin(warp); n0 < begin(warp + 1); n0 += 32) {
-      const int n = min(32, begin(warp + 1) - n0);
-      // each lane the first weight of a group
-      const uint32_t my_group = lane < n ? sm.group[n0 + lane].y : 0u;
-      const uint64_t my_first = lane < n ? first_weight(c, my_group) : 0;
-      for (int i = 0; i < n; ++i) {
-        const uint32_t g = __shfl_sync(0xffffffffu, my_group, i);
-        const uint64_t first = __shfl_sync(0xffffffffu, my_first, i);
-        const int e = exponent_of<T>(group_key(g));
-        if (e != exponent) {
-          exponent = e;
-          step = steps(c, e);
-        }
-        const uint64_t w = weight(c, g, first, step);
-        const uint32_t count = tokens(sm, c, g);
-        sums.add(w, count);
-        if (c.min_weight > 0 && w >= c.min_weight) sums_above.add(w, count);
+    u128 own_above = 0;
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      const int batch = warp + kWarps * i, n = 32 * batch + lane;
+      if (batch >= kBatches) break;
+      if (32 * batch >= filled) {
+        if (lane == 0) sm.batch[batch] = 0;
+        continue;
       }
+      const uint32_t g = n < filled ? sm.group[n].y : 0u;
+      u128 sum = sum_of(sm, c, n < filled, g, sm.group[g].x, &own_above);
+      if (i == 0) mine[0] = sum;
+      else mine[1] = sum;
+      sum = warp_sum(sum);
+      if (lane == 0) sm.batch[batch] = sum;
     }
-    const u128 mine_sum = warp_sum(sums.whole());
     __syncthreads();
-    if (lane == 0) sm.wide[warp] = mine_sum;
-    __syncthreads();
-    sum = sm.wide[lane];
-    before = total + warp_scan(sum) - sum;
-    total += warp_sum(sum);
+    total += warp_sum(sm.batch[lane]) + warp_sum(lane + kWarps < kBatches ? sm.batch[lane + kWarps] : 0);
     if (c.min_weight > 0) {
-      const u128 mine_above = warp_sum(sums_above.whole());
-      __syncthreads();
-      if (lane == 0) sm.wide[warp] = mine_above;
+      own_above = warp_sum(own_above);
+      if (lane == 0) sm.wide[warp] = own_above;
       __syncthreads();
       above += warp_sum(sm.wide[lane]);
     }
   }
 
-  // Whether the running sum passes sm.border in this round; one thread then has called found(bin, its weight, the sum
-  // before it).
+  // Whether the running sum passes sm.border in this round; one thread then has called found(bin, its weight, its tokens, the
+  // sum before it).
   template <typename F>
   __device__ __forceinline__ bool find(Shared& sm, const Cuts& c, F found) const {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const u128 border = sm.border;
-    const uint32_t in = __ballot_sync(0xffffffffu, before <= border && border < before + sum);
-    if (in == 0u) return false;
-    const int who = __ffs(in) - 1, first = begin(who), n = begin(who + 1) - first;
-    u128 upto = broadcast(before, who);
-    int n_at = first;
-    if (n > 1) {
-      // the sums of that warp's groups, one to a warp
-      for (int i = warp; i < n; i += kWarps) {
-        int bin;
-        uint64_t w;
-        const uint32_t count = at(sm, c, first + i, &bin, &w);
-        const u128 s = warp_sum(static_cast<u128>(w) * count);
-        if (lane == 0) sm.part[i] = s;
-      }
-      __syncthreads();
-      for (int i0 = 0; i0 < n; i0 += 32) {
-        const u128 s = i0 + lane < n ? sm.part[i0 + lane] : 0, incl = upto + warp_scan(s);
-        const uint32_t hit = __ballot_sync(0xffffffffu, incl > border);
-        if (hit != 0u) {
-          const int l = __ffs(hit) - 1;
-          n_at = first + i0 + l;
-          upto = broadcast(incl - s, l);
-          break;
-        }
+    u128 upto = before;
+    int batch = -1;
+#pragma unroll 1
+    for (int i = 0; i < 2 && batch < 0; ++i) {
+      const u128 s = lane + kWarps * i < kBatches ? sm.batch[lane + kWarps * i] : 0, incl = upto + warp_scan(s);
+      const uint32_t hit = __ballot_sync(0xffffffffu, incl > border);
+      if (hit != 0u) {
+        batch = __ffs(hit) - 1 + kWarps * i;
+        upto = broadcast(incl - s, __ffs(hit) - 1);
+      } else {
         upto = broadcast(incl, 31);
       }
     }
+    if (batch < 0) return false;
     __syncthreads();  // every thread has read the border: found() may set the next one
-    if (warp == 0) {
-      int bin;
-      uint64_t w;
-      const uint32_t count = at(sm, c, n_at, &bin, &w);
-      const u128 part = static_cast<u128>(w) * count, incl = upto + warp_scan(part);
-      const uint32_t hit = __ballot_sync(0xffffffffu, incl > border);
-      if (lane == __ffs(hit) - 1) found(bin, w, incl - part);
+    if (warp == (batch & (kWarps - 1))) {
+      const u128 s = batch < kWarps ? mine[0] : mine[1], incl = upto + warp_scan(s);
+      const int who = __ffs(__ballot_sync(0xffffffffu, incl > border)) - 1;
+      upto = broadcast(incl - s, who);
+      const uint32_t g = sm.group[32 * batch + who].y;
+      const uint32_t held = sm.bin[32 * g + lane], count = c.top_k != 0xffffffffu ? among_first(held, sm.group[g].x, c.top_k) : held;
+      const uint64_t w = weight(sm, c, g, lane, first_weight(c, g));
+      const u128 part = static_cast<u128>(w) * count, to = upto + warp_scan(part);
+      // the last bin with tokens where the sum over the bins falls short of the group's
+      uint32_t hit = __ballot_sync(0xffffffffu, to > border);
+      if (hit == 0u) hit = 0x80000000u >> __clz(__ballot_sync(0xffffffffu, count > 0 && w > 0));
+      if (lane == __ffs(hit) - 1) found(32 * static_cast<int>(g) + lane, w, count, to - part);
     }
     __syncthreads();
     return true;
@@ -760,6 +785,14 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a,
     }
 
     Round<T> round;
+    {
+      // The table of steps, an exponent to a warp.
+      round.least = max(exponent_of<T>(top), exponent_of<T>(floor_key)) - (kExponents - 1);
+      __syncthreads();  // the list is over
+      const float step = ldexpf(static_cast<float>(lane), round.least + warp - Keys<T>::kBias) * c.heat.unit;
+      const uint64_t w = falling(c.heat, step, 0.f);
+      sm.steps[warp][lane] = make_uint2(static_cast<uint32_t>(w) & 0x7fffffffu, static_cast<uint32_t>(w >> 31));
+    }
     auto count = [&](int r) {
       round.first_key = first_bin - kBins * r;
       round.bins = min(kBins, bins - kBins * r);
@@ -817,15 +850,15 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a,
     __syncthreads();
     if (top_p < 1.f)
       again([&] {
-        return round.find(sm, c, [&](int, uint64_t w, u128 ahead) {
-          sm.kept = lesser(sm.kept, ahead + static_cast<u128>(quotient(sm.border - ahead, w) + 1) * w);
+        return round.find(sm, c, [&](int, uint64_t w, uint32_t n, u128 ahead) {
+          sm.kept = lesser(sm.kept, ahead + static_cast<u128>(min(quotient(sm.border - ahead, w) + 1, static_cast<int64_t>(n))) * w);
           aim();
         });
       });
     again([&] {
-      return round.find(sm, c, [&](int bin, uint64_t w, u128 ahead) {
+      return round.find(sm, c, [&](int bin, uint64_t w, uint32_t n, u128 ahead) {
         sm.key = round.first_key - bin;
-        sm.nth = static_cast<int32_t>(quotient(sm.border - ahead, w));
+        sm.nth = static_cast<int32_t>(min(quotient(sm.border - ahead, w), static_cast<int64_t>(n) - 1));
         sm.logprob = log_share(w, sm.kept);
       });
     });

@@ -445,6 +445,43 @@ def test_sample_all_magnitudes(dt, heat):
     check_sample(x, **s)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("B", [1, 2, 18, 20, 39, 77])
+@pytest.mark.parametrize("V", [8191, 8193, 16385, 33000, 70001])
+def test_sample_rows_cut_among_blocks(B, V, dt):
+    """One to 77 rows of lengths that one, two, four or eight blocks share, ties across their parts."""
+    x = logits(B, V, dt, V + B)
+    x[:, ::3] = x[:, ::3].round()
+    s = settings(B, V)
+    s["k"] = [r if r != 1000 else 3000 for r in s["k"]]
+    check_sample(x, **s)
+
+
+@pytest.mark.parametrize("V", [9000, 20000, 40000])
+def test_sample_blocks_without_tokens(V):
+    """Parts of a row that hold nothing, the largest alone, or NaN; the largest in several parts."""
+    B = 19
+    x = torch.full((B, V), -math.inf, dtype=torch.bfloat16, device="cuda")
+    y = logits(B, V, "bf16", V)
+    for b in range(B):
+        lo, hi = b * V // B, min(V, (b * V) // B + 300)
+        x[b, lo:hi] = y[b, lo:hi]
+    x[3], x[4], x[5, ::2] = -math.inf, math.nan, math.nan
+    x[6], x[6, [5, V // 2, V - 1]] = -math.inf, 3.0
+    x[7, [V - 1, V // 3]], x[8, 1] = math.inf, math.inf
+    x[9] = 0.0
+    check_sample(x, **settings(B, 1))
+    check_sample(x, u=[0.99 - b / 40 for b in range(B)], heat=[1.0] * B, top_p=[0.95] * B)
+
+
+@pytest.mark.parametrize("heat", [1e38, 3e38])
+def test_sample_two_rounds_cut_among_blocks(heat):
+    raw = torch.randint(0, 65536, (3, 40000), generator=gen(19), dtype=torch.int64)
+    raw = torch.where((raw & 0x7FFF) >= 0x7F80, raw & 0x8000, raw)
+    x = (raw - 65536 * (raw >= 32768).long()).to(torch.int16).view(torch.bfloat16).cuda()
+    check_sample(x, u=[0.1, 0.6, 0.999], heat=[heat] * 3, k=[0, 20000, 5000], top_p=[0.99, 1.0, 0.7], min_p=[0.0, 0.01, 0.0])
+
+
 def test_sample_border_numbers():
     """u at 0, just below 1, outside and NaN; settings that are NaN switch their step off."""
     x = logits(9, 777, "bf16", 11)
