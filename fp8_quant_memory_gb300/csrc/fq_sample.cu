@@ -358,10 +358,6 @@ __device__ __forceinline__ u128 warp_sum(u128 v) {
 // 32 and adds 64.
 struct Sum {
   uint64_t lo = 0, hi = 0;
-  __device__ __forceinline__ void add(uint64_t w, uint32_t count) {
-    lo += static_cast<uint64_t>(static_cast<uint32_t>(w) & 0x7fffffffu) * count;
-    hi += static_cast<uint64_t>(static_cast<uint32_t>(w >> 31)) * count;
-  }
   __device__ __forceinline__ u128 whole() const { return (static_cast<u128>(hi) << 31) + lo; }
 };
 
@@ -657,8 +653,8 @@ __device__ __forceinline__ bool is_long(const SampleArgs& a, int32_t b) {
   return (k <= 0 || k > kThreads) && (a.temperature == nullptr || __ldg(a.temperature + b) > 0.f) && (top_p < 1.f || !(min_p > 0.f));
 }
 
-// The i-th row, the long ones first. For at most kThreads rows.
-__device__ __forceinline__ int32_t row_of(const SampleArgs& a, Shared& sm, int32_t i) {
+// The i-th row and the then-th (-1: there is none), the long ones first. For at most kThreads rows.
+__device__ __forceinline__ int2 rows_of(const SampleArgs& a, Shared& sm, int32_t i, int32_t then) {
   const int tid = threadIdx.x, lane = tid & 31;
   const bool slow = tid < a.B && is_long(a, tid);
   const uint32_t in = __ballot_sync(0xffffffffu, slow);
@@ -667,13 +663,25 @@ __device__ __forceinline__ int32_t row_of(const SampleArgs& a, Shared& sm, int32
   const uint32_t mine = sm.narrow[lane], upto = warp_scan(mine), all = __shfl_sync(0xffffffffu, upto, 31);
   const int32_t ahead = __shfl_sync(0xffffffffu, upto - mine, tid >> 5) + __popc(in & ((1u << lane) - 1u));
   const int32_t place = slow ? ahead : static_cast<int32_t>(all) + tid - ahead;
-  if (tid < a.B && place == i) sm.index = tid;
+  if (tid == 0) sm.nth = -1;
   __syncthreads();
-  return sm.index;
+  if (tid < a.B && place == i) sm.index = tid;
+  if (tid < a.B && place == then) sm.nth = tid;
+  __syncthreads();
+  return make_int2(sm.index, sm.nth);
+}
+
+// Brings a row to the L2 cache; one warp.
+__device__ __forceinline__ void prefetch_row(const SampleArgs& a, int32_t b) {
+  constexpr uint32_t kPiece = 8192;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.logits + b * a.stride), from = (at + 15) & ~static_cast<uintptr_t>(15);
+  const uintptr_t to = (at + 2 * static_cast<uintptr_t>(a.V)) & ~static_cast<uintptr_t>(15);
+  for (uintptr_t p = from + kPiece * (threadIdx.x & 31); p < to; p += 32 * kPiece)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(static_cast<uint32_t>(to - p < kPiece ? to - p : kPiece)) : "memory");
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a, bool ordered) {
+__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a, bool ordered, int32_t ahead) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -681,7 +689,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a,
   for (int i = tid; i < static_cast<int>(sizeof(PowerTable) / 4); i += kThreads)
     reinterpret_cast<float*>(&sm.powers)[i] = __ldg(reinterpret_cast<const float*>(&kPowers) + i);
   pdl_wait();
-  const int32_t b = ordered ? row_of(a, sm, blockIdx.x) : static_cast<int32_t>(blockIdx.x);
+  int2 rows = make_int2(static_cast<int32_t>(blockIdx.x), static_cast<int64_t>(blockIdx.x) + ahead < a.B ? static_cast<int32_t>(blockIdx.x) + ahead : -1);
+  if (ordered) rows = rows_of(a, sm, rows.x, rows.y);
+  const int32_t b = rows.x;
   const Row row(a.logits + b * a.stride, a.V);
   const float temperature = a.temperature == nullptr ? 1.f : a.temperature[b];
   const int32_t k = a.top_k == nullptr ? 0 : a.top_k[b];
@@ -713,6 +723,8 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a,
   }
   __syncthreads();
   top = __reduce_max_sync(0xffffffffu, sm.narrow[lane]);
+  // The row of the block that follows on this SM, now that this one has been read.
+  if (ahead > 0 && rows.y >= 0 && warp == 0) prefetch_row(a, rows.y);
   if (top <= Keys<T>::kFloor) {  // nothing is left of the row
     if (tid == 0) {
       a.token[b] = -1;
@@ -800,8 +812,14 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a,
       for (int i = tid; i < (round.bins + 31) / 32 * 8; i += kThreads) reinterpret_cast<uint4*>(sm.bin)[i] = make_uint4(0u, 0u, 0u, 0u);
       __syncthreads();
       const uint32_t first_key = round.first_key, n = static_cast<uint32_t>(round.bins);
-      if (own >= floor_key) {
+      if (own >= floor_key && rounds == 1) {
         each_vector<4>(row, tid, row.vectors, kThreads, [&](const uint4& v, int32_t) {
+          each_key(v, [&](uint32_t s, int) {
+            if (first_key - s < n) atomicAdd(&sm.bin[first_key - s], 1u);
+          });
+        });
+      } else if (own >= floor_key) {
+        each_vector<2>(row, tid, row.vectors, kThreads, [&](const uint4& v, int32_t) {
           each_key(v, [&](uint32_t s, int) {
             if (s == kMinusZero) s = kZero;
             if (first_key - s < n)  // keys of the rounds before wrap around
@@ -810,6 +828,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a,
         });
       }
       __syncthreads();
+      if (rounds == 1 && first_key - kMinusZero < n) {  // in one round -0 is counted on its own
+        if (tid == 0) {
+          sm.bin[first_key - kZero] += sm.bin[first_key - kMinusZero];
+          sm.bin[first_key - kMinusZero] = 0;
+        }
+        __syncthreads();
+      }
       if (r == 0 && first_bin > Keys<T>::kTop) {  // bins above the largest are those of NaN
         if (tid < static_cast<int>(first_bin - top)) sm.bin[tid] = 0u;
         __syncthreads();
@@ -937,8 +962,9 @@ bool launch(const SampleArgs& a, cudaStream_t s) {
   static_assert(smem <= 227 * 1024, "the bins fit the SM");
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(sample_kernel<T>), smem)) return false;
   // More rows than SMs: the long ones go first, or the last of them is waited for.
-  const bool ordered = a.B > sm_count() && a.B <= kThreads;
-  launch_overlapped(sample_kernel<T>, dim3(static_cast<unsigned>(a.B)), kThreads, smem, 1, s, a, ordered);
+  const int sms = sm_count();
+  const bool ordered = a.B > sms && a.B <= kThreads;
+  launch_overlapped(sample_kernel<T>, dim3(static_cast<unsigned>(a.B)), kThreads, smem, 1, s, a, ordered, a.B > sms ? sms : 0);
   return true;
 }
 
