@@ -6,9 +6,9 @@
 // to the sequence whose sums enclose j. Tokens and returned pages find their sequence the same way.
 //
 // What bounds it: one launch and two dependent rounds of loads (lengths; table and ring entries), not bytes: a step of 64
-// tokens moves 3.6 KB, one of 65536 1 MB. One cluster does the whole step: every CTA sums all lengths itself (a few
-// per thread, in L2), then takes its share of the tokens and pages. Lengths and pool may be updated in place, so they are
-// written behind a barrier of the cluster, after every CTA has read them.
+// tokens moves 3.6 KB, one of 65536 1 MB. Every CTA sums all lengths itself (a few per thread), then takes its share of the
+// tokens and pages, so that none waits for another; only where lengths or pool are updated in place, the CTAs are one
+// cluster and write them behind its barrier, after every CTA has read them.
 #include "fq_serving.h"
 #include "fq_sync.cuh"
 #include "fq_tcgen05.cuh"
@@ -16,34 +16,48 @@
 namespace fq {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr uint32_t kRefused = 0x80000000u;  // flag in `need`'s sums
+constexpr int kSmall = 256;                  // tokens and sequences of a step that one small block takes
+constexpr uint32_t kRefused = 0x80000000u;  // flag in the sums of pages taken
 
 __device__ __forceinline__ int32_t cut(int64_t v) { return v > 0x7fffffffLL ? 0x7fffffff : static_cast<int32_t>(v); }
 
-// The block's exclusive sum of v over its threads, and the total.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scan, int64_t* total) {
+// The block's exclusive sums of kN numbers over its threads, and the totals.
+template <int kThreads, int kN>
+__device__ __forceinline__ void block_scan(int64_t (&v)[kN], int64_t (*scan)[kThreads / 32], int64_t (&total)[kN]) {
+  constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t incl = v;
+  int64_t incl[kN];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += u;
-  }
-  __syncthreads();
-  if (lane == 31) scan[warp] = incl;
-  __syncthreads();
-  int64_t w = scan[lane];  // kWarps == 32
+  for (int i = 0; i < kN; ++i) incl[i] = v[i];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, w, o);
-    if (lane >= o) w += u;
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, incl[i], o);
+      if (lane >= o) incl[i] += u;
+    }
+  __syncthreads();
+  if (lane == 31)
+#pragma unroll
+    for (int i = 0; i < kN; ++i) scan[i][warp] = incl[i];
+  __syncthreads();
+  int64_t w[kN];
+#pragma unroll
+  for (int i = 0; i < kN; ++i) w[i] = lane < kWarps ? scan[i][lane] : 0;
+#pragma unroll
+  for (int o = 1; o < kWarps; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int64_t u = __shfl_up_sync(0xffffffffu, w[i], o);
+      if (lane >= o) w[i] += u;
+    }
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    total[i] = __shfl_sync(0xffffffffu, w[i], kWarps - 1);
+    const int64_t before = __shfl_sync(0xffffffffu, w[i], warp == 0 ? 0 : warp - 1);
+    v[i] = (warp == 0 ? 0 : before) + incl[i] - v[i];
   }
-  *total = __shfl_sync(0xffffffffu, w, 31);
-  const int64_t before = warp == 0 ? 0 : __shfl_sync(0xffffffffu, w, warp - 1);
-  return before + incl - v;
 }
 
 // The last i in [0, n) with first[i] <= x; first[0] <= x.
@@ -59,35 +73,46 @@ __device__ __forceinline__ int32_t owner(const uint32_t* first, int32_t n, uint3
 
 // Lengths, pool, table and ring are read through L2: this call writes them, and a kernel that starts on the same SM
 // before this one ends must not find their old lines in L1.
-__device__ __forceinline__ int32_t held_tokens(const ExtendArgs& a, int32_t b) { return max(__ldcg(a.lens + b), 0); }
 
-// Pages of n < 2^31 tokens.
-__device__ __forceinline__ uint32_t pages_of(const ExtendArgs& a, int64_t n) {
-  return (static_cast<uint32_t>(n) + a.page_size - 1u) / static_cast<uint32_t>(a.page_size);
+// Page of position t < 2^31; pages of n < 2^31 tokens.
+__device__ __forceinline__ uint32_t page_of(const ExtendArgs& a, uint32_t t) {
+  return static_cast<uint32_t>((static_cast<uint64_t>(t) * a.page_magic) >> a.page_magic_shift);
 }
+__device__ __forceinline__ uint32_t pages_of(const ExtendArgs& a, int64_t n) { return n == 0 ? 0u : page_of(a, static_cast<uint32_t>(n) - 1u) + 1u; }
 
+// kRun: tokens that a thread takes at a time. A small step's block shares its warps out: half of them take tokens, a
+// quarter the pages taken, a quarter those returned, each of which is a chain of loads.
+template <int kThreads, int kRun, bool kSmallStep>
 __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a) {
   extern __shared__ uint32_t sums[];
   uint32_t* tokens = sums;             // [B + 1], running sums before each sequence
   uint32_t* taken = sums + a.B + 1;    // with kRefused where a sequence is not granted its tokens
   uint32_t* given = taken + a.B + 1;   // returned pages
-  __shared__ int64_t scan[kWarps];
-  const uint32_t ctas = cluster_size(), rank = cluster_rank();
+  uint32_t* lens = given + a.B + 1;    // tokens held
+  __shared__ int64_t scan[2][kThreads / 32];
+  const uint32_t ctas = gridDim.x, rank = blockIdx.x;
   const int32_t per = (a.B + kThreads - 1) / kThreads, b0 = min(a.B, static_cast<int32_t>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
   pdl_trigger();
   pdl_wait();
   const int64_t F = a.places;
-  int64_t front = __ldcg(a.pool) % F;
-  if (front < 0) front += F;
+  int64_t front = __ldcg(a.pool);
   const int64_t free_count = min(max(static_cast<int64_t>(__ldcg(a.pool + 1)), static_cast<int64_t>(0)), F);
-  auto place = [&](int64_t i) { return a.ring + (front + i < F ? front + i : front + i - F); };  // 0 <= i <= F
-
-  int64_t sum = 0, all_tokens, all_taken, all_given;
-  for (int32_t b = b0; b < b1; ++b) sum += max(__ldcg(a.added + b), 0);
-  int64_t at = block_scan(sum, scan, &all_tokens);
-  int64_t need = 0, back = 0;
+  int64_t sum[1] = {0}, all[2], all_tokens[1];
   for (int32_t b = b0; b < b1; ++b) {
-    const int32_t n = __ldcg(a.added + b), len = held_tokens(a, b);
+    const int32_t n = __ldcg(a.added + b);
+    lens[b] = max(__ldcg(a.lens + b), 0);
+    given[b] = n;  // for the moment
+    sum[0] += max(n, 0);
+  }
+  if (front < 0 || front >= F) {
+    front %= F;
+    if (front < 0) front += F;
+  }
+  auto place = [&](int64_t i) { return a.ring + (front + i < F ? front + i : front + i - F); };  // 0 <= i <= F
+  block_scan<kThreads>(sum, scan, all_tokens);
+  int64_t at = sum[0], need[2] = {0, 0};  // pages taken, returned
+  for (int32_t b = b0; b < b1; ++b) {
+    const int32_t n = static_cast<int32_t>(given[b]), len = static_cast<int32_t>(lens[b]);
     tokens[b] = cut(at);
     at += max(n, 0);
     const uint32_t held = pages_of(a, len);
@@ -95,10 +120,12 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
     const bool fits = n >= 0 && then <= static_cast<int64_t>(a.width) * a.page_size && at <= a.tokens;
     taken[b] = fits ? pages_of(a, then) - held : kRefused;
     given[b] = n < 0 ? min(held, static_cast<uint32_t>(a.width)) : 0u;
-    need += taken[b] & ~kRefused;
-    back += given[b];
+    need[0] += taken[b] & ~kRefused;
+    need[1] += given[b];
   }
-  int64_t off = block_scan(need, scan, &all_taken), off_back = block_scan(back, scan, &all_given);
+  block_scan<kThreads>(need, scan, all);
+  const int64_t all_taken = all[0], all_given = all[1];
+  int64_t off = need[0], off_back = need[1];
   for (int32_t b = b0; b < b1; ++b) {
     const uint32_t own = taken[b] & ~kRefused, returned = given[b];
     const bool granted = (taken[b] & kRefused) == 0u && (own == 0u || off + own <= free_count);
@@ -108,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
     off_back += returned;
   }
   if (threadIdx.x == 0) {
-    tokens[a.B] = cut(all_tokens);
+    tokens[a.B] = cut(all_tokens[0]);
     taken[a.B] = cut(all_taken);
     given[a.B] = cut(all_given);
   }
@@ -121,42 +148,107 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
   }
   const int64_t room = F - free_count, returned = min(all_given, room);
 
+  // This thread and how many there are for the tokens, the pages taken and those returned.
+  constexpr uint32_t kPart = kThreads / 4;
+  const uint32_t warps_of = kSmallStep ? threadIdx.x / kPart : 0u;
   const uint32_t first = threadIdx.x + kThreads * rank, step = kThreads * ctas;
-  for (int64_t t = first; t < a.tokens; t += step) {
-    int64_t slot = -1;
-    int32_t pos = 0;
-    if (t < all_tokens) {
-      const int32_t b = owner(tokens, a.B, ~0u, static_cast<uint32_t>(t));
-      const int32_t len = held_tokens(a, b);
-      pos = cut(len + (t - tokens[b]));
-      const uint32_t own = taken[b];
-      if ((own & kRefused) == 0u) {
-        const int32_t at_page = pos / a.page_size, held = static_cast<int32_t>(pages_of(a, len));
-        const int32_t id = at_page < held ? __ldcg(a.table + b * a.table_stride + at_page)
-                                          : __ldcg(place(static_cast<int64_t>(own) + (at_page - held)));
-        if (id >= 0) slot = static_cast<int64_t>(id) * a.page_size + (pos - at_page * a.page_size);
+  if (!kSmallStep || warps_of < 2) {
+    const uint32_t step_t = kSmallStep ? 2 * kPart : step;
+    const uint32_t live = static_cast<uint32_t>(min(all_tokens[0], static_cast<int64_t>(a.tokens)));
+    const uint32_t lane = threadIdx.x & 31;
+    // A warp takes 32 * kRun tokens in a row: their first and last sequence, then each token's between those.
+    for (uint32_t base = (first - lane) * kRun; base < live; base += step_t * kRun) {
+      int32_t b_first, b_last;
+      if constexpr (kRun > 1) {
+        // one search by each half of the warp
+        const int32_t found = owner(tokens, a.B, ~0u, lane < 16 ? base : min(base + 32 * kRun, live) - 1);
+        b_first = __shfl_sync(0xffffffffu, found, 0);
+        b_last = __shfl_sync(0xffffffffu, found, 31);
+      } else {
+        b_first = 0;
+        b_last = a.B - 1;
+      }
+      int32_t b[kRun], end[kRun];
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        b[i] = b_first;
+        end[i] = b_last + 1;
+      }
+      for (int32_t n = b_last - b_first; n > 0; n >>= 1) {  // owner(tokens, ..) of each, side by side
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+          const int32_t mid = (b[i] + end[i]) >> 1;
+          if (end[i] - b[i] > 1) {
+            if (tokens[mid] <= base + 32 * i + lane) b[i] = mid;
+            else end[i] = mid;
+          }
+        }
+      }
+      int32_t pos[kRun], id[kRun];
+      uint32_t in_page[kRun];
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        const uint32_t t = base + 32 * i + lane;
+        pos[i] = 0;
+        id[i] = -1;
+        in_page[i] = 0;
+        if (t >= live) continue;
+        const uint32_t len = lens[b[i]], own = taken[b[i]];
+        pos[i] = cut(static_cast<int64_t>(len) + (t - tokens[b[i]]));
+        if ((own & kRefused) != 0u) continue;
+        const uint32_t p = page_of(a, pos[i]), held = pages_of(a, len);
+        in_page[i] = pos[i] - p * a.page_size;
+        id[i] = __ldcg(p < held ? a.table + b[i] * a.table_stride + p : place(static_cast<int64_t>(own) + (p - held)));
+      }
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        const uint32_t t = base + 32 * i + lane;
+        if (t >= live) continue;
+        a.slots[t] = id[i] >= 0 ? static_cast<int64_t>(id[i]) * a.page_size + in_page[i] : -1;
+        a.positions[t] = pos[i];
       }
     }
-    a.slots[t] = slot;
-    a.positions[t] = pos;
+    for (uint32_t t = live + first; t < static_cast<uint32_t>(a.tokens); t += step_t) {
+      a.slots[t] = -1;
+      a.positions[t] = 0;
+    }
   }
-  for (int64_t j = first; j < last; j += step) {
-    const int32_t b = owner(taken, a.B, ~kRefused, static_cast<uint32_t>(j));
-    const int64_t held = pages_of(a, held_tokens(a, b));
-    a.table[b * a.table_stride + held + (j - (taken[b] & ~kRefused))] = __ldcg(place(j));
+  if (!kSmallStep || warps_of == 2) {
+    const uint32_t first_p = kSmallStep ? threadIdx.x - 2 * kPart : first, step_p = kSmallStep ? kPart : step;
+    for (int64_t j = first_p; j < last; j += step_p) {
+      const int32_t b = owner(taken, a.B, ~kRefused, static_cast<uint32_t>(j));
+      const int64_t held = pages_of(a, lens[b]);
+      a.table[b * a.table_stride + held + (j - (taken[b] & ~kRefused))] = __ldcg(place(j));
+    }
   }
-  for (int64_t j = first; j < returned; j += step) {
-    const int32_t b = owner(given, a.B, ~0u, static_cast<uint32_t>(j));
-    *place(free_count + j) = __ldcg(a.table + b * a.table_stride + (j - given[b]));
+  if (!kSmallStep || warps_of == 3) {
+    const uint32_t first_p = kSmallStep ? threadIdx.x - 3 * kPart : first, step_p = kSmallStep ? kPart : step;
+    constexpr int kAtOnce = 4;
+    for (int64_t j0 = first_p; j0 < returned; j0 += kAtOnce * static_cast<int64_t>(step_p)) {
+      int32_t id[kAtOnce];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int64_t j = j0 + i * static_cast<int64_t>(step_p);
+        if (j >= returned) continue;
+        const int32_t b = owner(given, a.B, ~0u, static_cast<uint32_t>(j));
+        id[i] = __ldcg(a.table + b * a.table_stride + (j - given[b]));
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int64_t j = j0 + i * static_cast<int64_t>(step_p);
+        if (j < returned) *place(free_count + j) = id[i];
+      }
+    }
   }
-  // Every CTA has read the lengths and the pool.
+  // In place: every CTA has read the lengths and the pool.
   __syncthreads();
-  if (ctas > 1) cluster_barrier();
+  if (a.in_place != 0 && ctas > 1) cluster_barrier();
   for (int32_t b = first; b <= a.B; b += step) {
     a.starts[b] = static_cast<int32_t>(tokens[b]);
     if (b == a.B) break;
-    const int32_t n = __ldcg(a.added + b), len = held_tokens(a, b);
-    a.lens_out[b] = (taken[b] & kRefused) == 0u ? len + n : n < 0 ? 0 : len;
+    // Tokens granted fit the step, so their sums are whole. One that ends gets 0: it holds returned pages, or had none.
+    const int32_t len = static_cast<int32_t>(lens[b]);
+    a.lens_out[b] = (taken[b] & kRefused) == 0u ? len + static_cast<int32_t>(tokens[b + 1] - tokens[b]) : __ldcg(a.added + b) < 0 ? 0 : len;
   }
   if (first == 0) {
     a.pool_out[0] = static_cast<int32_t>(place(last) - a.ring);
@@ -165,15 +257,34 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
   }
 }
 
+template <int kThreads, int kRun, bool kSmallStep>
+bool launch(const ExtendArgs& a, int64_t ctas, cudaStream_t s) {
+  auto kern = extend_kernel<kThreads, kRun, kSmallStep>;
+  const size_t smem = 4 * (static_cast<size_t>(a.B) + 1) * sizeof(uint32_t);
+  if (!ensure_dynamic_smem(reinterpret_cast<const void*>(kern), smem)) return false;
+  launch_overlapped(kern, dim3(static_cast<unsigned>(ctas)), kThreads, smem, a.in_place != 0 ? static_cast<unsigned>(ctas) : 1, s, a);
+  return true;
+}
+
 }  // namespace
 
-bool launch_extend(const ExtendArgs& a, cudaStream_t s) {
-  const size_t smem = 3 * (static_cast<size_t>(a.B) + 1) * sizeof(uint32_t);
-  if (!ensure_dynamic_smem(reinterpret_cast<const void*>(extend_kernel), smem)) return false;
-  unsigned cluster = 1;
-  while (cluster < kMaxCluster && static_cast<int64_t>(cluster) * kThreads < a.tokens) cluster *= 2;
-  launch_overlapped(extend_kernel, dim3(cluster), kThreads, smem, cluster, s, a);
-  return true;
+bool launch_extend(const ExtendArgs& given, cudaStream_t s) {
+  ExtendArgs a = given;
+  int lg = 0;
+  while ((1LL << lg) < a.page_size) ++lg;
+  a.page_magic_shift = 31 + lg;
+  a.page_magic = static_cast<uint32_t>(((1ull << a.page_magic_shift) + a.page_size - 1) / a.page_size);
+  a.in_place = a.lens_out == a.lens || a.pool_out == a.pool;
+  if (a.tokens <= kSmall && a.B <= kSmall) return launch<2 * kSmall, 1, true>(a, 1, s);
+  // A CTA for each 1024 tokens, up to one for each SM or, where lengths or pool are written over, up to a cluster; their
+  // threads take several tokens at a time where there are more. 65536 tokens: 8.0 us, in place 15.
+  const int64_t want = (static_cast<int64_t>(a.tokens) + 1023) / 1024, most = a.in_place != 0 ? kMaxCluster : sm_count();
+  int64_t ctas = 1;
+  if (a.in_place != 0)
+    while (ctas < most && ctas < want) ctas *= 2;
+  else
+    ctas = want < 1 ? 1 : want < most ? want : most;
+  return want > ctas ? launch<1024, 8, false>(a, ctas, s) : launch<1024, 1, false>(a, ctas, s);
 }
 
 }  // namespace fq

@@ -80,6 +80,9 @@ struct ExtendArgs {
   int32_t* positions;
   int32_t* starts;
   int32_t B, width, page_size, tokens, places;  // places: the ring's
+  uint32_t page_magic;  // t / page_size = (t * page_magic) >> page_magic_shift for t < 2^31
+  int32_t page_magic_shift;
+  int32_t in_place;  // lens_out is lens, or pool_out pool
 };
 
 struct SampleArgs {
@@ -139,7 +142,7 @@ bool launch_attention_split(const PagedArgs& a, int dtype, cudaStream_t s);
 bool launch_attention_window(const PagedArgs& a, int dtype, cudaStream_t s);  // its part with a window
 void launch_attention_scalar(const PagedArgs& a, int dtype, cudaStream_t s);
 
-constexpr int kMaxExtend = 16384;  // sequences of one call: three counts of each lie in shared memory
+constexpr int kMaxExtend = 12288;  // sequences of one call: four numbers of each lie in shared memory
 bool launch_extend(const ExtendArgs& a, cudaStream_t s);
 bool launch_sample(const SampleArgs& a, int dtype, cudaStream_t s);
 

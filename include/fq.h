@@ -418,7 +418,7 @@ int fq_paged_attention_window(const uint8_t* q, int64_t q_stride, const float* q
  * pool[0] counts modulo `ring`, pool[1] within [0, ring]; pages returned to a full ring are dropped. pool[2] is not
  * read. seq_lens_out and pool_out may be seq_lens and pool (a graph that is replayed then advances); otherwise outputs
  * overlap nothing. slots: [max_tokens] int64; positions: [max_tokens] int32. table_stride >= max_pages.
- * B <= 16384 (else FQ_ERR_UNSUPPORTED), ring >= 1, page_size >= 1, max_pages * page_size < 2^31. B = 0 and
+ * B <= 12288 (else FQ_ERR_UNSUPPORTED), ring >= 1, page_size >= 1, max_pages * page_size < 2^31. B = 0 and
  * max_tokens = 0 are allowed.
  */
 int fq_paged_extend(int32_t* page_table, int64_t table_stride, const int32_t* seq_lens, const int32_t* new_lens,

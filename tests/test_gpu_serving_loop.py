@@ -74,7 +74,7 @@ def check_extend(table, lens, new, ring, pool, page, T, in_place=False, pad=0):
 
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("B,W,page,T", [(1, 1, 1, 1), (1, 4, 16, 40), (3, 5, 7, 33), (17, 9, 16, 300), (64, 20, 64, 900), (100, 3, 1, 120),
-                                        (1000, 6, 24, 3000), (1024, 4, 8, 8192), (1025, 4, 8, 20000), (5000, 3, 16, 9000)])
+                                        (1000, 6, 24, 3000), (1024, 4, 8, 8192), (1025, 4, 8, 20000), (5000, 3, 16, 9000), (12288, 2, 8, 20000), (257, 3, 4, 100), (255, 3, 4, 257)])
 def test_extend(B, W, page, T, in_place):
     state = make_step(B, W, page, ring=B * W + 5, count=B * W // 2 + 3, seed=B + T)
     check_extend(*state, page, T, in_place=in_place)

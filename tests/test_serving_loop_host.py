@@ -55,7 +55,7 @@ EXTEND = dict(table=P16, table_stride=9, lens=P16, new=P16, ring=P16, F=100, poo
     (dict(lens_out=None), INVALID), (dict(pool_out=None), INVALID), (dict(slots=None), INVALID), (dict(positions=None), INVALID),
     (dict(starts=None), INVALID), (dict(B=-1), INVALID), (dict(W=-1), INVALID), (dict(page=0), INVALID), (dict(T=-1), INVALID), (dict(F=0), INVALID),
     (dict(table_stride=8), INVALID), (dict(table_stride=1 << 41), INVALID), (dict(T=1 << 31), INVALID), (dict(F=1 << 31), INVALID),
-    (dict(W=1 << 20, table_stride=1 << 20, page=1 << 12), INVALID), (dict(B=16385), UNSUPPORTED), (dict(slots=P16 + 4), INVALID),
+    (dict(W=1 << 20, table_stride=1 << 20, page=1 << 12), INVALID), (dict(B=12289), UNSUPPORTED), (dict(slots=P16 + 4), INVALID),
     (dict(lens=P16 + 2), INVALID), (dict(table=P16 + 1), INVALID)], ids=str)
 def test_extend_refusals(lib, over, code):  # noqa: F811
     rc, msg = call(lib, "fq_paged_extend", EXTEND, over)
