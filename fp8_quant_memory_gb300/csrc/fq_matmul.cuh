@@ -474,11 +474,13 @@ constexpr int kPlain = -1;  // no fused epilogue
 
 constexpr int kTileM = 256, kTileN = 256;  // outputs of a CTA pair
 constexpr int kWideStageBytes = 256 * kBK; // one CTA's half of the pair's operands
-constexpr int kWideStages = 6;
-
+// With a fused epilogue a stage less, for staging rows of all a warp's columns: their residuals arrive there during the
+// products (64 columns of them, the others loaded at the end, took 172 us where this takes 148: 4096 x 8192 x 4096, gelu_tanh).
+template <bool kFused>
 struct WideShared {
+  static constexpr int kWideStages = kFused ? 5 : 6;
   alignas(1024) unsigned char ring[kWideStages][kWideStageBytes];  // 128 rows of a, then 128 weight rows
-  alignas(1024) unsigned char out[8][32 * 128];                    // per epilogue warp: 32 rows x 64 columns
+  alignas(1024) unsigned char out[8][kFused ? 2 : 1][32 * 128];    // per epilogue warp: 32 rows x 64 columns
   alignas(8) uint64_t full[kWideStages];  // leader: both CTAs' operands have landed
   uint64_t empty[kWideStages];            // both: the products have read them
   uint64_t done[2];                       // both: a block's products are in tensor memory
@@ -511,8 +513,8 @@ __device__ __forceinline__ Tile tile_at(const MmArgs& p, int t) {
 
 // A warp's part of a piece: 32 rows x 32*kChunks columns over every block of k; `b` and `phase` are the next
 // accumulator buffer and its parity. False if a wait gave up.
-template <int kChunks>
-__device__ __forceinline__ bool wide_accumulate(const MmArgs& p, WideShared& sm, const float* sa, const float* sb, uint32_t from,
+template <int kChunks, typename Sm>
+__device__ __forceinline__ bool wide_accumulate(const MmArgs& p, Sm& sm, const float* sa, const float* sb, uint32_t from,
                                                 uint32_t free0, uint32_t free1, int& b, uint32_t& phase,
                                                 float2 (&acc)[16 * kChunks]) {
   const int lane = threadIdx.x & 31;
@@ -598,18 +600,14 @@ __device__ __forceinline__ void wide_store(const MmArgs& p, const CUtensorMap* o
   }
 }
 
-// 64 columns from `col` of the warp's residual rows, into registers: piece (lane % 8) of row 4i + lane / 8 in to[i], or, where
-// they cannot be read in pieces or end inside, by copy_residual.
-__device__ __forceinline__ bool residual_in_pieces(const MmArgs& p, int col) { return p.residual_vec != 0 && col + 64 <= p.N; }
-
 __device__ __forceinline__ const uint16_t* residual_at(const MmArgs& p, int row, int col) {
   return static_cast<const uint16_t*>(p.residual) + static_cast<int64_t>(row) * p.residual_stride + col;
 }
 
-// The same columns into the staging rows, as wide_store lays them out.
+// 64 columns from `col` of the warp's residual rows into staging rows, as wide_store lays them out.
 __device__ __forceinline__ void copy_residual(const MmArgs& p, unsigned char* stage, int row0, int col) {
   const int lane = threadIdx.x & 31, rows = min(32, p.M - row0);
-  if (residual_in_pieces(p, col)) {
+  if (p.residual_vec != 0 && col + 64 <= p.N) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int r = 4 * i + (lane >> 3), e = lane & 7;
@@ -629,15 +627,16 @@ __device__ __forceinline__ void copy_residual(const MmArgs& p, unsigned char* st
     }
 }
 
-// What a piece's epilogue needs, on its way from the piece's start: the residuals of the first 64 columns, to the staging
-// rows, and 4 columns' biases of each lane (-0 where there are none: y + -0 is y).
+// What a piece's epilogue needs, on its way from the piece's start: the residuals, to the staging rows, and 4 columns'
+// biases of each lane (-0 where there are none: y + -0 is y).
 template <int kChunks>
 __device__ __forceinline__ uint2 wide_prepare(const MmArgs& p, unsigned char* stage, int row0, int col0) {
   const int lane = threadIdx.x & 31, col = col0 + 4 * lane;
   if (p.residual != nullptr) {
-    if (lane == 0) bulk_wait_read();  // the last box has left the staging rows
+    if (lane == 0) bulk_wait_read();  // the last boxes have left the staging rows
     __syncwarp();
-    copy_residual(p, stage, row0, col0);
+#pragma unroll
+    for (int c = 0; c < kChunks / 2; ++c) copy_residual(p, stage + 4096 * c, row0, col0 + 64 * c);
   }
   uint2 b = make_uint2(0x80008000u, 0x80008000u);
   if (p.bias != nullptr && lane < 8 * kChunks) {
@@ -655,64 +654,50 @@ __device__ __forceinline__ uint2 wide_prepare(const MmArgs& p, unsigned char* st
 }
 
 // wide_store with the fused epilogue: residuals come through the staging rows, whose pieces each lane replaces by its
-// outputs. Those of the second 64 columns wait in registers while the first are worked on.
+// outputs.
 template <int kChunks, int kAct, typename T>
 __device__ __forceinline__ void wide_store_fused(const MmArgs& p, const CUtensorMap* omap, unsigned char* stage, int row0, int col0,
                                                  uint2 bias, const float2 (&acc)[16 * kChunks]) {
-  const int lane = threadIdx.x & 31, rows = min(32, p.M - row0);
-  const bool ahead = kChunks == 4 && p.residual != nullptr && residual_in_pieces(p, col0 + 64);
-  uint4 next[kChunks == 4 ? 8 : 1];
-  if (ahead) {
-#pragma unroll
-    for (int i = 0; i < (kChunks == 4 ? 8 : 1); ++i) {
-      const int r = 4 * i + (lane >> 3);
-      if (r < rows) next[i] = *reinterpret_cast<const uint4*>(residual_at(p, row0 + r, col0 + 64 + 8 * (lane & 7)));
-    }
+  const int lane = threadIdx.x & 31;
+  if (p.residual == nullptr) {
+    if (lane == 0) bulk_wait_read();
+  } else {
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
+  __syncwarp();
 #pragma unroll
   for (int c = 0; c < kChunks / 2; ++c) {
-    const int col = col0 + 64 * c;
-    if (c > 0 || p.residual == nullptr) {
-      if (lane == 0) bulk_wait_read();
-      __syncwarp();
-    }
-    if (p.residual != nullptr) {
-      if (c > 0 && ahead) {
 #pragma unroll
-        for (int i = 0; i < (kChunks == 4 ? 8 : 1); ++i) {
-          const int r = 4 * i + (lane >> 3);
-          if (r < rows) *reinterpret_cast<uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4)) = next[i];
+    for (int e0 = 0; e0 < 8; e0 += 4) {
+      uint4 res[4];  // before the stores of these four, which the compiler cannot tell apart from them
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        res[i] = p.residual != nullptr ? *reinterpret_cast<const uint4*>(stage + 4096 * c + lane * 128 + (((e0 + i) ^ (lane & 7)) << 4))
+                                       : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = e0 + i;
+        uint32_t packed[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float2* v = &acc[32 * c + 4 * e + 2 * h];
+          const int owner = 16 * c + 2 * e + h;  // the lane with these four columns' biases
+          const float2 s0 = add2(v[0], Elem<T>::unpack(__shfl_sync(0xffffffffu, bias.x, owner)));
+          const float2 s1 = add2(v[1], Elem<T>::unpack(__shfl_sync(0xffffffffu, bias.y, owner)));
+          float y[4] = {s0.x, s0.y, s1.x, s1.y};
+          activate4<kAct>(y);
+          float2 y0 = make_float2(y[0], y[1]), y1 = make_float2(y[2], y[3]);
+          if (p.residual != nullptr) {
+            y0 = add2(y0, Elem<T>::unpack(h == 0 ? res[i].x : res[i].z));
+            y1 = add2(y1, Elem<T>::unpack(h == 0 ? res[i].y : res[i].w));
+          }
+          packed[2 * h] = Elem<T>::pack(y0);
+          packed[2 * h + 1] = Elem<T>::pack(y1);
         }
-      } else if (c > 0) {
-        copy_residual(p, stage, row0, col);
+        *reinterpret_cast<uint4*>(stage + 4096 * c + lane * 128 + ((e ^ (lane & 7)) << 4)) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-      __syncwarp();
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      uint4* at = reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4));
-      const uint4 res = p.residual != nullptr ? *at : make_uint4(0u, 0u, 0u, 0u);
-      uint32_t packed[4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float2* v = &acc[32 * c + 4 * e + 2 * h];
-        const int owner = 16 * c + 2 * e + h;  // the lane with these four columns' biases
-        const float2 b0 = Elem<T>::unpack(__shfl_sync(0xffffffffu, bias.x, owner)), b1 = Elem<T>::unpack(__shfl_sync(0xffffffffu, bias.y, owner));
-        const float2 s0 = add2_rn(v[0], b0), s1 = add2_rn(v[1], b1);
-        float y[4] = {s0.x, s0.y, s1.x, s1.y};
-        activate4<kAct>(y);
-        float2 y0 = make_float2(y[0], y[1]), y1 = make_float2(y[2], y[3]);
-        if (p.residual != nullptr) {
-          y0 = add2_rn(y0, Elem<T>::unpack(h == 0 ? res.x : res.z));
-          y1 = add2_rn(y1, Elem<T>::unpack(h == 0 ? res.y : res.w));
-        }
-        packed[2 * h] = Elem<T>::pack(y0);
-        packed[2 * h + 1] = Elem<T>::pack(y1);
-      }
-      *at = make_uint4(packed[0], packed[1], packed[2], packed[3]);
-    }
-    send_staged(p, omap, stage, row0, col);
+    send_staged(p, omap, stage + 4096 * c, row0, col0 + 64 * c);
   }
 }
 
@@ -724,7 +709,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   constexpr bool kFused = kAct != kPlain;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   // The swizzle repeats every 1024 bytes: align to 1024 (the same offset in both CTAs).
-  WideShared& sm = *reinterpret_cast<WideShared*>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
+  using Sm = WideShared<kFused>;
+  constexpr int kWideStages = Sm::kWideStages;
+  Sm& sm = *reinterpret_cast<Sm*>(smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pairs = gridDim.x / 2, first = blockIdx.x / 2;
@@ -820,7 +807,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
     const int quarter = warp & 3, half = (warp - 4) >> 2;  // lanes 32*quarter.., which half of the columns
     const uint32_t lanes = tmem + (static_cast<uint32_t>(32 * quarter) << 16);
-    unsigned char* stage = sm.out[warp - 4];
+    unsigned char* stage = sm.out[warp - 4][0];
     const uint32_t free0 = in_cta(&sm.free_[0], 0), free1 = in_cta(&sm.free_[1], 0);
     int b = 0;
     uint32_t phase = 0;
@@ -891,7 +878,7 @@ bool launch_wide(const MatmulArgs& a, MmArgs p, const MatmulPlan& plan, cudaStre
   p.whole = static_cast<int32_t>(tiles - rest);
   p.parts = plan.parts;
   p.pieces = static_cast<int32_t>(p.whole + rest * p.parts);
-  constexpr size_t smem = sizeof(WideShared) + 1024;
+  constexpr size_t smem = sizeof(WideShared<kAct != kPlain>) + 1024;
   static_assert(smem <= 227 * 1024, "the ring and the staging rows fit the SM");
   if (!ensure_dynamic_smem(reinterpret_cast<const void*>(matmul_wide_kernel<kAct, T>), smem)) return false;
   launch_overlapped(matmul_wide_kernel<kAct, T>, dim3(static_cast<unsigned>(2 * (p.pieces < pairs ? p.pieces : pairs))), kWideThreads, smem, 2, s,
