@@ -163,27 +163,27 @@ __device__ __forceinline__ void narrow_finish(const MmArgs& p, int col0, int row
   const bool in_row = row < p.N;
   const float bias = p.bias != nullptr && in_row ? load_in(p.dtype, p.bias, row) : -0.f;  // y + -0 is y
   int64_t at = static_cast<int64_t>(col0) * p.out_stride + row;
+  constexpr int kGroup = N < 8 ? N : 8;
 #pragma unroll 1
-  for (int j = 0; j < N && col0 + j < p.M; j += 4) {
-    float v[4];
+  for (int j = 0; j < N && col0 + j < p.M; j += kGroup) {
+    float2 v[kGroup / 2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kGroup; ++i) {
       float x = 0.f;
 #pragma unroll
       for (int q = 0; q < SPLIT; ++q) x += q == mine ? sums[j + i][t] : part[N * (q < mine ? q : q - 1) + j + i][t];
-      v[i] = __fadd_rn(SPLIT == 1 ? sums[j + i][t] : x, bias);
+      const float y = __fadd_rn(SPLIT == 1 ? sums[j + i][t] : x, bias);
+      if (i & 1) v[i / 2].y = y;
+      else v[i / 2].x = y;
     }
-    activate4(p.activation, v);
+    activate_pairs(p.activation, v);
     if (p.residual != nullptr) {
-      const float2 a = unpack_in(p.dtype, words[j / 2][t]), b = unpack_in(p.dtype, words[j / 2 + 1][t]);
-      v[0] = __fadd_rn(v[0], a.x);
-      v[1] = __fadd_rn(v[1], a.y);
-      v[2] = __fadd_rn(v[2], b.x);
-      v[3] = __fadd_rn(v[3], b.y);
+#pragma unroll
+      for (int i = 0; i < kGroup / 2; ++i) v[i] = add2(v[i], unpack_in(p.dtype, words[j / 2 + i][t]));
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i, at += p.out_stride)
-      if (in_row && col0 + j + i < p.M) store_out(p.dtype, p.out, at, v[i]);
+    for (int i = 0; i < kGroup; ++i, at += p.out_stride)
+      if (in_row && col0 + j + i < p.M) store_out(p.dtype, p.out, at, i & 1 ? v[i / 2].y : v[i / 2].x);
   }
 }
 
@@ -475,7 +475,7 @@ constexpr int kPlain = -1;  // no fused epilogue
 constexpr int kTileM = 256, kTileN = 256;  // outputs of a CTA pair
 constexpr int kWideStageBytes = 256 * kBK; // one CTA's half of the pair's operands
 // With a fused epilogue a stage less, for staging rows of all a warp's columns: their residuals arrive there during the
-// products (64 columns of them, the others loaded at the end, took 172 us where this takes 148: 4096 x 8192 x 4096, gelu_tanh).
+// products (half of them loaded at the end took 147 us where this takes 135: 4096 x 8192 x 4096 with bias and residual).
 template <bool kFused>
 struct WideShared {
   static constexpr int kWideStages = kFused ? 5 : 6;
@@ -682,11 +682,8 @@ __device__ __forceinline__ void wide_store_fused(const MmArgs& p, const CUtensor
         for (int h = 0; h < 2; ++h) {
           const float2* v = &acc[32 * c + 4 * e + 2 * h];
           const int owner = 16 * c + 2 * e + h;  // the lane with these four columns' biases
-          const float2 s0 = add2(v[0], Elem<T>::unpack(__shfl_sync(0xffffffffu, bias.x, owner)));
-          const float2 s1 = add2(v[1], Elem<T>::unpack(__shfl_sync(0xffffffffu, bias.y, owner)));
-          float y[4] = {s0.x, s0.y, s1.x, s1.y};
-          activate4<kAct>(y);
-          float2 y0 = make_float2(y[0], y[1]), y1 = make_float2(y[2], y[3]);
+          float2 y0 = activate2<kAct>(add2(v[0], Elem<T>::unpack(__shfl_sync(0xffffffffu, bias.x, owner))));
+          float2 y1 = activate2<kAct>(add2(v[1], Elem<T>::unpack(__shfl_sync(0xffffffffu, bias.y, owner))));
           if (p.residual != nullptr) {
             y0 = add2(y0, Elem<T>::unpack(h == 0 ? res[i].x : res[i].z));
             y1 = add2(y1, Elem<T>::unpack(h == 0 ? res[i].y : res[i].w));

@@ -537,3 +537,158 @@ def test_sample_empty_and_replayed():
         graph.replay()
         want = fq.sample(x, u, want_logprob=True)
         assert torch.equal(want[0], out[0]) and torch.equal(want[1], out[1])
+
+
+# ------------------------------------------------------------------------------------- a serving loop
+class Loop:
+    """One block of a model with random weights, its cache, and the requests' state."""
+
+    def __init__(self, B=5, Hq=8, Hk=2, D=128, hidden=512, V=1003, page=16, seed=90):
+        g = gen(seed)
+        self.B, self.Hq, self.Hk, self.D, self.hidden, self.V, self.page, self.width, self.window, self.sinks = B, Hq, Hk, D, hidden, V, page, 6, 20, 3
+        pages = 40
+
+        def weight(n, k):
+            codes = serving_ref.finite_codes((n, k), g)
+            return codes.cuda(), (torch.rand(-(-n // 128), k // 128, generator=g) * 2e-4 + 1e-4).cuda()
+        self.w_qkv, self.w_out, self.w_logits = weight((Hq + 2 * Hk) * D, hidden), weight(hidden, Hq * D), weight(V, hidden)
+        self.b_qkv = (0.1 * torch.randn((Hq + 2 * Hk) * D, generator=g)).bfloat16().cuda()
+        self.w_in, self.w_mid, self.w_last = ((1 + 0.1 * torch.randn(n, generator=g)).bfloat16().cuda() for n in (hidden, Hq * D, hidden))
+        self.wq, self.wk = ((1 + 0.1 * torch.randn(D, generator=g)).bfloat16().cuda() for _ in range(2))
+        self.embedding = torch.randn(V, hidden, generator=g).bfloat16().cuda()
+        angle = torch.arange(self.width * page)[:, None] * 1e4 ** (-torch.arange(D // 2) * 2.0 / D)
+        self.cos, self.sin = angle.cos().cuda(), angle.sin().cuda()
+        self.none = torch.zeros(0, device="cuda")
+        self.cache = [torch.zeros(pages, Hk, page, D, dtype=torch.uint8, device="cuda") for _ in range(2)] + \
+            [torch.ones(pages, Hk, page, device="cuda") for _ in range(2)]
+        self.table = torch.full((B, self.width), -1, dtype=torch.int32, device="cuda")
+        self.lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+        self.new = torch.ones(B, dtype=torch.int32, device="cuda")
+        self.ring = torch.randperm(pages, generator=g).int().cuda()
+        self.pool = ints([3, pages, 0])
+        self.u = torch.rand(B, generator=g).cuda()
+        self.heat, self.k = torch.full((B,), 0.7, device="cuda"), ints([50] * B)
+        self.top_p = torch.full((B,), 0.9, device="cuda")
+
+    def quantise(self, x, w):
+        tables = torch.empty(x.shape[0], 0, dtype=torch.bfloat16, device="cuda")
+        return fq.rmsnorm_rope_quant_groups(x, w, tables, tables, 128, want_y=False)[1:]
+
+    def step(self, ids, max_tokens, seen=None):
+        """ids: [max_tokens] token ids, the sequences' new ones in order; returns the next token of each sequence."""
+        B, Hq, D = self.B, self.Hq, self.D
+        before = [t.clone() for t in (self.table, self.lens, self.ring, self.pool)]
+        slots, pos, starts, _, _ = fq.paged_extend(self.table, self.lens, self.new, self.ring, self.pool, self.page, max_tokens,
+                                                   seq_lens_out=self.lens, pool_out=self.pool)
+        x = self.embedding[ids]
+        a = self.quantise(x, self.w_in)
+        qkv = fq.fp8_matmul(*a, *self.w_qkv, bias=self.b_qkv)
+        q, qs = fq.qkv_norm_rope_append(qkv, self.wq, self.wk, self.cos[pos], self.sin[pos], slots, *self.cache, Hq, self.Hk)
+        last = (starts[1:] - 1).long()
+        args = (q[last], qs[last], *self.cache, self.table, self.lens)
+        out, lse = fq.paged_attention(*args, window=self.window, sinks=self.sinks, want_lse=True)
+        m = self.quantise(out.view(B, Hq * D), self.w_mid)
+        stream = x[last]
+        y = fq.fp8_matmul(*m, *self.w_out, activation="silu", residual=stream)
+        n = self.quantise(y, self.w_last)
+        logits = fq.fp8_matmul(*n, *self.w_logits)
+        token, logprob = fq.sample(logits, self.u, temperature=self.heat, top_k=self.k, top_p=self.top_p, want_logprob=True)
+        if seen is not None:
+            seen.update(before=before, slots=slots, pos=pos, starts=starts, qkv=(qkv, a), attention=(args, out, lse), y=(y, m, stream), logits=logits,
+                        token=token, logprob=logprob)
+        return token
+
+    def check(self, s, max_tokens):
+        table, lens, ring, pool = (t.tolist() for t in s["before"])
+        w = ref.extend(table, lens, self.new.tolist(), ring, pool, self.page, max_tokens)
+        assert s["slots"].tolist() == w["slots"] and s["pos"].tolist() == w["positions"] and s["starts"].tolist() == w["starts"]
+        assert self.lens.tolist() == w["seq_lens"] and self.table.tolist() == w["table"] and self.ring.tolist() == w["ring"] and self.pool.tolist() == w["pool"]
+        qkv, a = s["qkv"]
+        ref.assert_epilogue(qkv, *a, *self.w_qkv, self.b_qkv, None, None)
+        args, out, lse = s["attention"]
+        serving_ref.assert_attention(out, lse, *ref.windowed(*args, self.window, self.sinks), self.D ** -0.5)
+        y, m, stream = s["y"]
+        ref.assert_epilogue(y, *m, *self.w_out, None, "silu", stream)
+        for b in range(self.B):
+            t, lp, margin = ref.sample(s["logits"][b].cpu().double(), self.u[b].double().item(), self.heat[b].double().item(), int(self.k[b]), self.top_p[b].double().item())
+            assert margin < 2.0 ** -38 or int(s["token"][b]) == t
+            assert margin < 2.0 ** -38 or abs(float(s["logprob"][b]) - lp) <= 2.0 ** -20 * abs(lp) + 2.0 ** -22
+
+
+def started(seed=90):
+    """A loop whose five prompts of 59 tokens in all are in the cache, and the tokens that follow them."""
+    s = Loop(seed=seed)
+    s.new.copy_(ints([7, 1, 18, 30, 3]))
+    ids = torch.randint(0, s.V, (64,), generator=gen(seed + 1)).cuda()
+    seen = {}
+    token = s.step(ids, 64, seen)
+    s.check(seen, 64)
+    s.new.fill_(1)
+    return s, token
+
+
+def test_serving_loop():
+    """Prompts, then steps of one token each: every operator against 64 bits on its own inputs, the requests' state too; a
+    sequence ends and another takes its place."""
+    s, token = started()
+    for step in range(8):
+        if step == 4:
+            s.new.copy_(ints([1, -1, 1, 1, 1]))
+            ids = torch.cat([token[[0, 2, 3, 4]], token[:1]])
+        else:
+            s.new.fill_(1)
+            ids = token
+        s.u.copy_(torch.rand(5, generator=gen(step)))
+        seen = {}
+        token = s.step(ids, 5, seen)
+        assert bool(((token >= 0) & (token < s.V)).all())
+        s.check(seen, 5)
+    assert s.lens.tolist() == [7 + 8, 3, 18 + 8, 30 + 8, 3 + 8]
+
+
+def test_serving_loop_captured():
+    """The step captured with its state updated in place, replayed with the tokens that it gave, equals the eager steps."""
+    a, token_a = started(91)
+    b, token = started(91)
+    assert torch.equal(token_a, token)
+    ids, side = token.clone(), torch.cuda.Stream()
+    keep = [t.clone() for t in (b.table, b.lens, b.ring, b.pool, *b.cache)]
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b.step(ids, 5)
+    torch.cuda.current_stream().wait_stream(side)
+    for t, k in zip((b.table, b.lens, b.ring, b.pool, *b.cache), keep):
+        t.copy_(k)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ids.copy_(b.step(ids, 5))
+    for step in range(6):
+        u = torch.rand(5, generator=gen(step)).cuda()
+        a.u.copy_(u)
+        b.u.copy_(u)
+        token_a = a.step(token_a, 5)
+        graph.replay()
+        assert torch.equal(token_a, ids)
+    for x, y in zip((a.table, a.lens, a.ring, a.pool, *a.cache), (b.table, b.lens, b.ring, b.pool, *b.cache)):
+        assert torch.equal(x, y)
+
+
+def test_serving_loops_on_two_streams():
+    """Two loops at once, each on its stream, as each alone."""
+    alone = []
+    for seed in (92, 93):
+        s, token = started(seed)
+        for _ in range(5):
+            token = s.step(token, 5)
+        alone.append((token, s.lens.clone()))
+    loops = [started(92), started(93)]
+    streams = [torch.cuda.Stream() for _ in loops]
+    torch.cuda.synchronize()
+    tokens = [t for _, t in loops]
+    for _ in range(5):
+        for i, (s, _) in enumerate(loops):
+            with torch.cuda.stream(streams[i]):
+                tokens[i] = s.step(tokens[i], 5)
+    torch.cuda.synchronize()
+    for (token, lens), got, (s, _) in zip(alone, tokens, loops):
+        assert torch.equal(token, got) and torch.equal(lens, s.lens)
