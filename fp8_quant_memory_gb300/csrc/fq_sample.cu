@@ -63,22 +63,20 @@ constexpr PowerTable make_powers() {
   return t;
 }
 
-__device__ const PowerTable kPowers = make_powers();  // each block copies it to shared memory
+__device__ const PowerTable kPowers = make_powers();
 
 // What a row's weights depend on: its largest value, and log2(e) / T / unit as two floats. Values are taken in halves
 // (unit 1/2) from a temperature of 1 on, so that the difference of any two is finite, and in smaller units at temperatures
 // whose reciprocal leaves fp32's normal range.
 struct Heat {
   float top, unit, hi, lo;
-  const PowerTable* powers;
 };
 
 // hi = L / t rounded, lo what it lacks: the remainder L - hi * t is exact.
-__device__ __forceinline__ Heat heat_of(float top, float temperature, const PowerTable* powers) {
+__device__ __forceinline__ Heat heat_of(float top, float temperature) {
   constexpr float kL = 1.44269502162933349609f, kLLo = 1.92596299112661746e-8f;  // log2(e)
   Heat h;
   h.top = top;
-  h.powers = powers;
   h.unit = temperature >= 1.8446744e19f ? 1.3552527e-20f : temperature >= 1.f ? 0.5f : 1.f;  // 2^64: 2^-66
   const float t = temperature * h.unit;
   if (t < INFINITY) {
@@ -101,7 +99,7 @@ __device__ __forceinline__ uint64_t falling(const Heat& h, float d, float err) {
   const float n = floorf(p), f = __fsub_rn(p, n);                     // exact
   const float j = rintf(f * 1024.f), r = fmaf(j, -0.0009765625f, f);  // exact, |r| <= 2^-11
   const int at = static_cast<int>(j);
-  const float th = h.powers->hi[at], tl = h.powers->lo[at];
+  const float th = __ldg(&kPowers.hi[at]), tl = __ldg(&kPowers.lo[at]);
   constexpr float kLn2 = 0.693147182464599609f, kLn2Lo = -1.90465429995776e-9f;
   const float z = __fmul_rn(r, -kLn2);
   const float zl = fmaf(r, -kLn2, -z) - fmaf(r, kLn2Lo, e * kLn2);
@@ -312,7 +310,6 @@ __device__ __forceinline__ N block_scan(N v, N* part, N* total) {
 
 struct Shared {
   uint32_t bin[kBins];
-  PowerTable powers;
   // of a group of 32 bins: tokens before it (x, by its number), and the number of the n-th that has any (y, by n)
   uint2 group[kGroups];
   u128 batch[kBatches];  // sums of 32 filled groups
@@ -330,8 +327,9 @@ struct Shared {
   };
   uint16_t ids[kFew];
   int32_t list_size, id_count;
-  // the border to find and what was found, by one thread for all
-  u128 border, kept;
+  // the border to find, the batch in which it lies and the sum before that, and what was found, by one thread for all
+  u128 border, kept, upto;
+  int32_t found;
   uint32_t key;
   int32_t nth;
   float logprob;
@@ -392,7 +390,7 @@ struct Round {
   int bins;
   int least;            // the lowest exponent in the table
   int32_t filled;       // groups with tokens
-  u128 before, mine[2];  // sum before the round, and of this lane's groups
+  u128 before, mine[2];  // sum before the round (in the first warp), and of this lane's groups
 
   __device__ __forceinline__ uint32_t group_key(uint32_t g) const { return first_key - 32 * g; }
   __device__ __forceinline__ bool even(const Cuts& c, uint32_t g) const {
@@ -458,7 +456,8 @@ struct Round {
     return total;
   }
 
-  // Adds the round's tokens, weights, and weights of at least min_weight to the three sums.
+  // Adds the round's tokens, weights, and weights of at least min_weight to the three sums, the latter two in the first warp
+  // alone: sums of 128 bits take it 60 instructions, and all warps 32 times that.
   __device__ __forceinline__ void add_up(Shared& sm, const Cuts& c, uint32_t& ranks, u128& total, u128& above) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, groups = (bins + 31) / 32;
     // tokens in the low half, filled groups in the high half
@@ -509,12 +508,12 @@ struct Round {
       if (lane == 0) sm.batch[batch] = sum;
     }
     __syncthreads();
-    total += warp_sum(sm.batch[lane]) + warp_sum(lane + kWarps < kBatches ? sm.batch[lane + kWarps] : 0);
+    if (warp == 0) total += warp_sum(sm.batch[lane] + (lane + kWarps < kBatches ? sm.batch[lane + kWarps] : 0));
     if (c.min_weight > 0) {
       own_above = warp_sum(own_above);
       if (lane == 0) sm.wide[warp] = own_above;
       __syncthreads();
-      above += warp_sum(sm.wide[lane]);
+      if (warp == 0) above += warp_sum(sm.wide[lane]);
     }
   }
 
@@ -523,23 +522,35 @@ struct Round {
   template <typename F>
   __device__ __forceinline__ bool find(Shared& sm, const Cuts& c, F found) const {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const u128 border = sm.border;
-    u128 upto = before;
-    int batch = -1;
+    if (warp == 0) {
+      const u128 border = sm.border;
+      u128 upto = before;
+      int batch = -1;
 #pragma unroll 1
-    for (int i = 0; i < 2 && batch < 0; ++i) {
-      const u128 s = lane + kWarps * i < kBatches ? sm.batch[lane + kWarps * i] : 0, incl = upto + warp_scan(s);
-      const uint32_t hit = __ballot_sync(0xffffffffu, incl > border);
-      if (hit != 0u) {
-        batch = __ffs(hit) - 1 + kWarps * i;
-        upto = broadcast(incl - s, __ffs(hit) - 1);
-      } else {
-        upto = broadcast(incl, 31);
+      for (int i = 0; i < 2 && batch < 0; ++i) {
+        const u128 s = lane + kWarps * i < kBatches ? sm.batch[lane + kWarps * i] : 0, incl = upto + warp_scan(s);
+        const uint32_t hit = __ballot_sync(0xffffffffu, incl > border);
+        if (hit != 0u) {
+          batch = __ffs(hit) - 1 + kWarps * i;
+          upto = broadcast(incl - s, __ffs(hit) - 1);
+        } else {
+          upto = broadcast(incl, 31);
+        }
+      }
+      if (lane == 0) {
+        sm.found = batch;
+        sm.upto = upto;
       }
     }
-    if (batch < 0) return false;
-    __syncthreads();  // every thread has read the border: found() may set the next one
+    __syncthreads();
+    const int batch = sm.found;
+    if (batch < 0) {
+      __syncthreads();  // read by all before the next round's search
+      return false;
+    }
     if (warp == (batch & (kWarps - 1))) {
+      const u128 border = sm.border;
+      u128 upto = sm.upto;
       const u128 s = batch < kWarps ? mine[0] : mine[1], incl = upto + warp_scan(s);
       const int who = __ffs(__ballot_sync(0xffffffffu, incl > border)) - 1;
       upto = broadcast(incl - s, who);
@@ -686,8 +697,6 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a,
   Shared& sm = *reinterpret_cast<Shared*>(smem_raw);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
-  for (int i = tid; i < static_cast<int>(sizeof(PowerTable) / 4); i += kThreads)
-    reinterpret_cast<float*>(&sm.powers)[i] = __ldg(reinterpret_cast<const float*>(&kPowers) + i);
   pdl_wait();
   int2 rows = make_int2(static_cast<int32_t>(blockIdx.x), static_cast<int64_t>(blockIdx.x) + ahead < a.B ? static_cast<int32_t>(blockIdx.x) + ahead : -1);
   if (ordered) rows = rows_of(a, sm, rows.x, rows.y);
@@ -738,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a,
   float logprob = 0.f;
   if (temperature >= 1.17549435e-38f && k != 1) {
     Cuts c;
-    c.heat = heat_of(value_of<T>(top), temperature, &sm.powers);
+    c.heat = heat_of(value_of<T>(top), temperature);
     c.top = top;
     c.top_k = k <= 0 ? 0xffffffffu : static_cast<uint32_t>(k);
     c.min_weight = min_p > 0.f ? static_cast<uint64_t>(share_of(fminf(min_p, 1.f), static_cast<u128>(1) << kOne, true)) : 0;
