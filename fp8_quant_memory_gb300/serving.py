@@ -9,7 +9,8 @@ share theirs. Codes are torch.uint8 or torch.float8_e4m3fn tensors of the same b
 
 Each call checks devices, dtypes and shapes on the host (ValueError), runs on the current stream of the
 tensors' device (which need not be the current device) and returns once its work is enqueued. The checks
-and the calls are compiled (csrc/fq_binding.cpp): a decoding step makes them with little work in each.
+and the calls are compiled (csrc/fq_binding.cpp): a decoding step makes them with little work in each. The tensors that
+paged_extend and sample return, where none are passed, are parts of one allocation.
 """
 from __future__ import annotations
 
