@@ -1,8 +1,4 @@
-// fq_attention_window.cu -- paged attention over the last `window` tokens of each sequence and its first `sinks`.
-#include "fq_attention.cuh"
-
-namespace fq {
-
-bool launch_attention_window(const PagedArgs& p, int dtype, cudaStream_t s) { return launch_split<true>(p, dtype, s); }
-
-}  // namespace fq
+// fq_attention_window.cu -- paged attention over the last `window` tokens of each sequence and its first `sinks`: the kernels
+// of fq_attention.cu, compiled with the window's tiles and masks.
+#define FQ_ATTENTION_WINDOW
+#include "fq_attention.cu"
