@@ -5,7 +5,8 @@
 // x = |y| / sqrt(2) on its falling side. In the product's epilogue they are bound by instructions and by the unit for
 // reciprocals and exponentials (8 clocks for a warp, an FMA 1): pairs take one instruction where there is one for two, and
 // share a reciprocal, that of the product of their denominators. Those are kept below 2^62 and above 0, so that the product
-// is inside fp32's range: a logistic function below 2^-62 is 2^-62, and one of a NaN is a number (y is the NaN).
+// is inside fp32's range: a logistic function below 2^-62 is 2^-62, and one of a NaN is a number (y is the NaN). y itself
+// is not taken below where that begins, so that what is left there is at most 1e-17 of size however large y is.
 #pragma once
 
 #include "fq.h"
@@ -26,10 +27,17 @@ __device__ __forceinline__ float2 reciprocals(float2 d) {
   return mul2(splat2(r), make_float2(d.y, d.x));
 }
 
-// y / (1 + 2^u)
-__device__ __forceinline__ float2 over_one_plus(float2 y, float2 u) {
+// The larger of the two, or NaN if y is.
+__device__ __forceinline__ float at_least(float y, float least) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(y), "f"(least));
+  return r;
+}
+
+// y / (1 + 2^u); u is above 62 below y = least
+__device__ __forceinline__ float2 over_one_plus(float2 y, float2 u, float least) {
   const float2 e = make_float2(exp2_approx(fminf(u.x, 62.f)), exp2_approx(fminf(u.y, 62.f)));
-  return mul2(y, reciprocals(add2(e, splat2(1.f))));
+  return mul2(make_float2(at_least(y.x, least), at_least(y.y, least)), reciprocals(add2(e, splat2(1.f))));
 }
 
 // y * erfc(-y / sqrt(2)) / 2. erfc(x) / 2 = t * 2^(q(t) - x^2 log2 e) with t = 1 / (1 + 0.4 x) and a polynomial q, fitted to
@@ -61,9 +69,9 @@ __device__ __forceinline__ float2 activate2(float2 y) {
   } else if constexpr (kAct == FQ_ACT_GELU_TANH) {
     // (1 + tanh(s)) / 2 is the logistic function of 2 s, s = sqrt(2 / pi) (y + 0.044715 y^3); in base 2
     const float2 f = fma2(mul2(y, y), splat2(-0.102943240f), splat2(-2.30220819f));
-    return over_one_plus(y, mul2(y, f));
+    return over_one_plus(y, mul2(y, f), -8.f);
   } else if constexpr (kAct == FQ_ACT_SILU) {
-    return over_one_plus(y, mul2(y, splat2(-1.44269504088896341f)));
+    return over_one_plus(y, mul2(y, splat2(-1.44269504088896341f)), -43.f);
   } else {
     return y;
   }

@@ -296,7 +296,8 @@ enum fq_activation {
 /*
  * fq_fp8_matmul with bias, activation and residual in its epilogue:
  *   out[i, j] = dtype( activation( P[i, j] + bias[j] ) + residual[i, j] )
- * where P is fq_fp8_matmul's fp32 product before its rounding; every step in fp32, one rounding to dtype. bias: [N] dtype
+ * where P is fq_fp8_matmul's fp32 product before its rounding; every step in fp32, one rounding to dtype. What the smooth
+ * activations leave of a value far below zero is off by up to 1e-17 (at -inf: at most that, or NaN with FQ_ACT_GELU). bias: [N] dtype
  * or null; residual: [M, N] dtype or null, rows residual_stride >= 0 elements apart (0: one row for all). The residual
  * may be the output itself (the same pointer and stride: out += activation(...)); otherwise they must not overlap.
  * activation: an fq_activation (else FQ_ERR_UNSUPPORTED). Without any of the three the result is fq_fp8_matmul's, bit for

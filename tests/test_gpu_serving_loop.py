@@ -343,6 +343,35 @@ def test_linear_ends_of_the_range(M, act):
     assert not bool(out[:, :8].isnan().any()) and not bool(out[:, 10:].isnan().any())
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,N,K", [(1, 264, 256), (100, 264, 256), (600, 264, 256), (20, 264, 250)])
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+def test_linear_far_below_zero(M, N, K, act, dt):
+    """What a smooth activation leaves far below zero: up to 1e-17 off, and the output's rounding, whatever the value is,
+    beside NaN and infinite neighbours, which share an instruction. Products are zero: the bias is what is activated."""
+    x, _, _ = linear_inputs(M, N, K, 6, "bf16", "")
+    x[0].zero_()
+    far = [-1e30, -3e38, -1e20, -65504.0, -1e4, -300.0, -90.0, -50.0, -44.0, -43.5, -43.0, -42.5, -42.0, -30.0, -20.0, -14.0, -10.0, -9.0, -8.5, -8.0, -7.5, -7.0]
+    far = torch.tensor(far, dtype=torch.float64).clamp(min=float(torch.finfo(DT[dt]).min)).repeat(3)
+    odd = torch.tensor([math.nan, math.inf, -math.inf], dtype=torch.float64).repeat_interleave(22)
+    bias = torch.zeros(N, dtype=torch.float64)
+    bias[0:132:2], bias[1:132:2] = far, odd
+    bias[132:264:2], bias[133:264:2] = odd, far
+    bias = bias.to(DT[dt])
+    out = fq.fp8_matmul(*x, out_dtype=DT[dt], bias=bias.cuda(), activation=act).cpu().double()
+    y = bias.double()
+    want = ref.ACTIVATIONS[act](y).expand(M, N)
+    finite = y.isfinite().expand(M, N)
+    # 2^-15: exponents of up to 2^6 (gelu: x^2 log2(e) of x = y / sqrt(2), rounded three times), 2^-24 of that each, times
+    # ln 2, and 2^-20 of the approximations; what is smaller than e^-43 is below 1e-17 itself
+    half = torch.finfo(DT[dt]).eps / 2
+    tol = (half + 2.0 ** -15) * want.abs() + 1e-17 + (2.0 ** -25 if dt == "fp16" else 0.0)
+    assert bool(((out - want).abs() <= tol)[finite].all())
+    assert bool(out[:, y.isnan()].isnan().all()) and bool((out[:, y == math.inf] == math.inf).all())
+    left = out[:, y == -math.inf]
+    assert bool(left.isnan().all()) if act == "gelu" else bool((left.abs() <= 1e-17).all())
+
+
 # ---------------------------------------------------------------------------------------- sampling
 def check_sample(x, u, heat=None, k=None, top_p=None, min_p=None, exact=True):
     """x: [B, V] on the GPU; lists of settings. Rows whose borders are met to 2^-38 may take a neighbour."""
