@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
     const bool fits = n >= 0 && then <= static_cast<int64_t>(a.width) * a.page_size && at <= a.tokens;
     taken[b] = fits ? pages_of(a, then) - held : kRefused;
     given[b] = n < 0 ? min(held, static_cast<uint32_t>(a.width)) : 0u;
+    if (n < 0) lens[b] = 0;  // from here on, the length without the step's tokens
     need[0] += taken[b] & ~kRefused;
     need[1] += given[b];
   }
@@ -246,9 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
   for (int32_t b = first; b <= a.B; b += step) {
     a.starts[b] = static_cast<int32_t>(tokens[b]);
     if (b == a.B) break;
-    // Tokens granted fit the step, so their sums are whole. One that ends gets 0: it holds returned pages, or had none.
-    const int32_t len = static_cast<int32_t>(lens[b]);
-    a.lens_out[b] = (taken[b] & kRefused) == 0u ? len + static_cast<int32_t>(tokens[b + 1] - tokens[b]) : __ldcg(a.added + b) < 0 ? 0 : len;
+    // Tokens granted fit the step, so their sums are whole.
+    a.lens_out[b] = static_cast<int32_t>(lens[b] + ((taken[b] & kRefused) == 0u ? tokens[b + 1] - tokens[b] : 0u));
   }
   if (first == 0) {
     a.pool_out[0] = static_cast<int32_t>(place(last) - a.ring);
