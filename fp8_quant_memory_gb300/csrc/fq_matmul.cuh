@@ -137,7 +137,8 @@ struct NarrowShared {
   uint32_t tmem;
 };
 
-// Residuals of rows col0 .. col0 + N - 1 of column `row`, two in a word.
+// Residuals of rows col0 .. col0 + N - 1 of column `row`, two in a word. Through L2, as in the wide kernel: they may be the
+// output, whose old values no line of L1 should hold when the next kernel starts beside this one.
 template <int N>
 __device__ __forceinline__ void narrow_residual(const MmArgs& p, int col0, int row, uint32_t (&r)[N / 2]) {
   const uint16_t* from = static_cast<const uint16_t*>(p.residual) + static_cast<int64_t>(col0) * p.residual_stride + row;
@@ -145,9 +146,9 @@ __device__ __forceinline__ void narrow_residual(const MmArgs& p, int col0, int r
 #pragma unroll
   for (int j = 0; j < N; j += 2) {
     uint32_t lo = 0, hi = 0;
-    if (j < n) lo = *from;
+    if (j < n) lo = __ldcg(from);
     from += p.residual_stride;
-    if (j + 1 < n) hi = *from;
+    if (j + 1 < n) hi = __ldcg(from);
     from += p.residual_stride;
     r[j / 2] = lo | (hi << 16);
   }
@@ -623,7 +624,7 @@ __device__ __forceinline__ void copy_residual(const MmArgs& p, unsigned char* st
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int x = lane + 32 * h;
-      if (col + x < p.N) *reinterpret_cast<uint16_t*>(stage + r * 128 + (((x >> 3) ^ (r & 7)) << 4) + 2 * (x & 7)) = *residual_at(p, row0 + r, col + x);
+      if (col + x < p.N) *reinterpret_cast<uint16_t*>(stage + r * 128 + (((x >> 3) ^ (r & 7)) << 4) + 2 * (x & 7)) = __ldcg(residual_at(p, row0 + r, col + x));
     }
 }
 
