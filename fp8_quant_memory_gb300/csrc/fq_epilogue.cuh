@@ -20,13 +20,6 @@ __device__ __forceinline__ float exp2_approx(float v) {
   return r;
 }
 
-// (1 / d.x, 1 / d.y) of two positive numbers whose product is inside fp32's range.
-__device__ __forceinline__ float2 reciprocals(float2 d) {
-  float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(d.x * d.y));
-  return mul2(splat2(r), make_float2(d.y, d.x));
-}
-
 // The larger of the two, or NaN if y is.
 __device__ __forceinline__ float at_least(float y, float least) {
   float r;
@@ -34,62 +27,99 @@ __device__ __forceinline__ float at_least(float y, float least) {
   return r;
 }
 
-// y / (1 + 2^u); u is above 62 below y = least
-__device__ __forceinline__ float2 over_one_plus(float2 y, float2 u, float least) {
-  const float2 e = make_float2(exp2_approx(fminf(u.x, 62.f)), exp2_approx(fminf(u.y, 62.f)));
-  return mul2(make_float2(at_least(y.x, least), at_least(y.y, least)), reciprocals(add2(e, splat2(1.f))));
+// d = (1 / d.x, 1 / d.y) of pairs of positive numbers whose product is inside fp32's range.
+template <int N>
+__device__ __forceinline__ void reciprocals(float2 (&d)[N]) {
+  float r[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm("rcp.approx.f32 %0, %1;" : "=f"(r[i]) : "f"(d[i].x * d[i].y));
+#pragma unroll
+  for (int i = 0; i < N; ++i) d[i] = mul2(splat2(r[i]), make_float2(d[i].y, d[i].x));
 }
 
-// y * erfc(-y / sqrt(2)) / 2. erfc(x) / 2 = t * 2^(q(t) - x^2 log2 e) with t = 1 / (1 + 0.4 x) and a polynomial q, fitted to
-// log2(erfc(x) exp(x^2) / (2 t)) on 0 <= x <= 12 by least squares whose weights follow the largest errors: 2^-23.4 of the
+// y = y / (1 + 2^u); u is above 62 below y = least
+template <int N>
+__device__ __forceinline__ void over_one_plus(float2 (&y)[N], float2 (&u)[N], float least) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) u[i] = make_float2(exp2_approx(fminf(u[i].x, 62.f)), exp2_approx(fminf(u[i].y, 62.f)));
+#pragma unroll
+  for (int i = 0; i < N; ++i) u[i] = add2(u[i], splat2(1.f));
+  reciprocals(u);
+#pragma unroll
+  for (int i = 0; i < N; ++i) y[i] = mul2(make_float2(at_least(y[i].x, least), at_least(y[i].y, least)), u[i]);
+}
+
+// y = y * erfc(-y / sqrt(2)) / 2. erfc(x) / 2 = t * 2^(q(t) - x^2 log2 e) with t = 1 / (1 + 0.4 x) and a polynomial q, fitted
+// to log2(erfc(x) exp(x^2) / (2 t)) on 0 <= x <= 12 by least squares whose weights follow the largest errors: 2^-23.4 of the
 // value, and in fp32 2^-20 up to x = 3 (the rounding of x^2; 2^-17 at x = 9).
-__device__ __forceinline__ float2 times_normal(float2 y) {
-  const float2 x = make_float2(fminf(fabsf(y.x) * 0.707106781186547524f, 16.f), fminf(fabsf(y.y) * 0.707106781186547524f, 16.f));
-  const float2 t = reciprocals(fma2(splat2(0.4f), x, splat2(1.f)));
-  float2 q = splat2(-0.30157715f);
-  q = fma2(q, t, splat2(1.3452829f));
-  q = fma2(q, t, splat2(-2.1683304f));
-  q = fma2(q, t, splat2(1.4709361f));
-  q = fma2(q, t, splat2(-0.66122967f));
-  q = fma2(q, t, splat2(0.4430461f));
-  q = fma2(q, t, splat2(0.5741099f));
-  q = fma2(q, t, splat2(1.4455438f));
-  q = fma2(q, t, splat2(-3.1477816f));
-  const float2 u = fma2(mul2(x, x), splat2(-1.44269504088896341f), q);
-  const float2 low = mul2(t, make_float2(exp2_approx(u.x), exp2_approx(u.y)));
-  return mul2(y, make_float2(y.x < 0.f ? low.x : 1.f - low.x, y.y < 0.f ? low.y : 1.f - low.y));
-}
-
-template <int kAct>
-__device__ __forceinline__ float2 activate2(float2 y) {
-  if constexpr (kAct == FQ_ACT_RELU) {
-    return make_float2(y.x <= 0.f ? 0.f : y.x, y.y <= 0.f ? 0.f : y.y);  // a NaN stays one
-  } else if constexpr (kAct == FQ_ACT_GELU) {
-    return times_normal(y);
-  } else if constexpr (kAct == FQ_ACT_GELU_TANH) {
-    // (1 + tanh(s)) / 2 is the logistic function of 2 s, s = sqrt(2 / pi) (y + 0.044715 y^3); in base 2
-    const float2 f = fma2(mul2(y, y), splat2(-0.102943240f), splat2(-2.30220819f));
-    return over_one_plus(y, mul2(y, f), -8.f);
-  } else if constexpr (kAct == FQ_ACT_SILU) {
-    return over_one_plus(y, mul2(y, splat2(-1.44269504088896341f)), -43.f);
-  } else {
-    return y;
+template <int N>
+__device__ __forceinline__ void times_normal(float2 (&y)[N]) {
+  constexpr float kQ[] = {1.3452829f, -2.1683304f, 1.4709361f, -0.66122967f, 0.4430461f, 0.5741099f, 1.4455438f, -3.1477816f};
+  float2 x[N], t[N], q[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = make_float2(fminf(fabsf(y[i].x) * 0.707106781186547524f, 16.f), fminf(fabsf(y[i].y) * 0.707106781186547524f, 16.f));
+    t[i] = fma2(splat2(0.4f), x[i], splat2(1.f));
+    q[i] = splat2(-0.30157715f);
+  }
+  reciprocals(t);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = fma2(q[i], t[i], splat2(kQ[k]));
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 u = fma2(mul2(x[i], x[i]), splat2(-1.44269504088896341f), q[i]);
+    q[i] = make_float2(exp2_approx(u.x), exp2_approx(u.y));
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 low = mul2(t[i], q[i]);
+    y[i] = mul2(y[i], make_float2(y[i].x < 0.f ? low.x : 1.f - low.x, y[i].y < 0.f ? low.y : 1.f - low.y));
   }
 }
 
+// Pairs side by side: each is a chain through two or three units, and the product has two warps to a scheduler (4096 x 8192 x
+// 4096 with gelu_tanh, 16 at a time: 138 us, one after another 146).
 template <int kAct, int N>
 __device__ __forceinline__ void activate_pairs(float2 (&y)[N]) {
+  if constexpr (kAct == FQ_ACT_RELU) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) y[i] = activate2<kAct>(y[i]);
+    for (int i = 0; i < N; ++i) y[i] = make_float2(y[i].x <= 0.f ? 0.f : y[i].x, y[i].y <= 0.f ? 0.f : y[i].y);  // a NaN stays one
+  } else if constexpr (kAct == FQ_ACT_GELU) {
+    times_normal(y);
+  } else if constexpr (kAct == FQ_ACT_GELU_TANH) {
+    // (1 + tanh(s)) / 2 is the logistic function of 2 s, s = sqrt(2 / pi) (y + 0.044715 y^3); in base 2
+    float2 u[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) u[i] = mul2(y[i], fma2(mul2(y[i], y[i]), splat2(-0.102943240f), splat2(-2.30220819f)));
+    over_one_plus(y, u, -8.f);
+  } else if constexpr (kAct == FQ_ACT_SILU) {
+    float2 u[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) u[i] = mul2(y[i], splat2(-1.44269504088896341f));
+    over_one_plus(y, u, -43.f);
+  }
+}
+
+// The same, pair by pair, of an activation known to the launch alone: less code, which short launches fetch anew.
+template <int kAct, int N>
+__device__ __forceinline__ void activate_each(float2 (&y)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float2 one[1] = {y[i]};
+    activate_pairs<kAct>(one);
+    y[i] = one[0];
+  }
 }
 
 template <int N>
-__device__ __forceinline__ void activate_pairs(int act, float2 (&y)[N]) {
+__device__ __forceinline__ void activate_each(int act, float2 (&y)[N]) {
   switch (act) {
-    case FQ_ACT_RELU: activate_pairs<FQ_ACT_RELU>(y); break;
-    case FQ_ACT_GELU: activate_pairs<FQ_ACT_GELU>(y); break;
-    case FQ_ACT_GELU_TANH: activate_pairs<FQ_ACT_GELU_TANH>(y); break;
-    case FQ_ACT_SILU: activate_pairs<FQ_ACT_SILU>(y); break;
+    case FQ_ACT_RELU: activate_each<FQ_ACT_RELU>(y); break;
+    case FQ_ACT_GELU: activate_each<FQ_ACT_GELU>(y); break;
+    case FQ_ACT_GELU_TANH: activate_each<FQ_ACT_GELU_TANH>(y); break;
+    case FQ_ACT_SILU: activate_each<FQ_ACT_SILU>(y); break;
     default: break;
   }
 }

@@ -23,6 +23,8 @@
 // others follow when their own waits run out, and tensor memory is freed either way.
 #pragma once
 
+#include <type_traits>
+
 #include "fq_device.cuh"
 #include "fq_epilogue.cuh"
 #include "fq_serving.h"
@@ -177,7 +179,7 @@ __device__ __forceinline__ void narrow_finish(const MmArgs& p, int col0, int row
       if (i & 1) v[i / 2].y = y;
       else v[i / 2].x = y;
     }
-    activate_pairs(p.activation, v);
+    activate_each(p.activation, v);
     if (p.residual != nullptr) {
 #pragma unroll
       for (int i = 0; i < kGroup / 2; ++i) v[i] = add2(v[i], unpack_in(p.dtype, words[j / 2 + i][t]));
@@ -476,7 +478,7 @@ constexpr int kPlain = -1;  // no fused epilogue
 constexpr int kTileM = 256, kTileN = 256;  // outputs of a CTA pair
 constexpr int kWideStageBytes = 256 * kBK; // one CTA's half of the pair's operands
 // With a fused epilogue a stage less, for staging rows of all a warp's columns: their residuals arrive there during the
-// products (half of them loaded at the end took 147 us where this takes 135: 4096 x 8192 x 4096 with bias and residual).
+// products (half of them loaded at the end took 12 us more: 4096 x 8192 x 4096 with bias and residual, 127 us).
 template <bool kFused>
 struct WideShared {
   static constexpr int kWideStages = kFused ? 5 : 6;
@@ -513,15 +515,14 @@ __device__ __forceinline__ Tile tile_at(const MmArgs& p, int t) {
 }
 
 // A warp's part of a piece: 32 rows x 32*kChunks columns over every block of k; `b` and `phase` are the next
-// accumulator buffer and its parity. False if a wait gave up.
+// accumulator buffer and its parity, a_next and b_next the first block's scales. False if a wait gave up.
 template <int kChunks, typename Sm>
-__device__ __forceinline__ bool wide_accumulate(const MmArgs& p, Sm& sm, const float* sa, const float* sb, uint32_t from,
-                                                uint32_t free0, uint32_t free1, int& b, uint32_t& phase,
-                                                float2 (&acc)[16 * kChunks]) {
+__device__ __forceinline__ bool wide_accumulate(const MmArgs& p, Sm& sm, const float* sa, const float* sb, float a_next,
+                                                float b_next, uint32_t from, uint32_t free0, uint32_t free1, int& b,
+                                                uint32_t& phase, float2 (&acc)[16 * kChunks]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int j = 0; j < 16 * kChunks; ++j) acc[j] = make_float2(0.f, 0.f);
-  float a_next = __ldg(sa), b_next = __ldg(sb);
   for (int kb = 0; kb < p.nkb; ++kb) {
     const float2 s2 = splat2(a_next * b_next);
     if (kb + 1 < p.nkb) {
@@ -629,16 +630,11 @@ __device__ __forceinline__ void copy_residual(const MmArgs& p, unsigned char* st
 }
 
 // What a piece's epilogue needs, on its way from the piece's start: the residuals, to the staging rows, and 4 columns'
-// biases of each lane (-0 where there are none: y + -0 is y).
+// biases of each lane (-0 where there are none: y + -0 is y), these before the residuals, behind which they would be waited
+// for (5 us of 4096 x 8192 x 4096).
 template <int kChunks>
 __device__ __forceinline__ uint2 wide_prepare(const MmArgs& p, unsigned char* stage, int row0, int col0) {
   const int lane = threadIdx.x & 31, col = col0 + 4 * lane;
-  if (p.residual != nullptr) {
-    if (lane == 0) bulk_wait_read();  // the last boxes have left the staging rows
-    __syncwarp();
-#pragma unroll
-    for (int c = 0; c < kChunks / 2; ++c) copy_residual(p, stage + 4096 * c, row0, col0 + 64 * c);
-  }
   uint2 b = make_uint2(0x80008000u, 0x80008000u);
   if (p.bias != nullptr && lane < 8 * kChunks) {
     const uint16_t* from = static_cast<const uint16_t*>(p.bias) + col;
@@ -651,6 +647,12 @@ __device__ __forceinline__ uint2 wide_prepare(const MmArgs& p, unsigned char* st
       b = make_uint2(v[0] | (v[1] << 16), v[2] | (v[3] << 16));
     }
   }
+  if (p.residual != nullptr) {
+    if (lane == 0) bulk_wait_read();  // the last boxes have left the staging rows
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < kChunks / 2; ++c) copy_residual(p, stage + 4096 * c, row0, col0 + 64 * c);
+  }
   return b;
 }
 
@@ -659,6 +661,7 @@ __device__ __forceinline__ uint2 wide_prepare(const MmArgs& p, unsigned char* st
 template <int kChunks, int kAct, typename T>
 __device__ __forceinline__ void wide_store_fused(const MmArgs& p, const CUtensorMap* omap, unsigned char* stage, int row0, int col0,
                                                  uint2 bias, const float2 (&acc)[16 * kChunks]) {
+  constexpr int kAtOnce = 4;  // pieces of 8 columns
   const int lane = threadIdx.x & 31;
   if (p.residual == nullptr) {
     if (lane == 0) bulk_wait_read();
@@ -669,31 +672,33 @@ __device__ __forceinline__ void wide_store_fused(const MmArgs& p, const CUtensor
 #pragma unroll
   for (int c = 0; c < kChunks / 2; ++c) {
 #pragma unroll
-    for (int e0 = 0; e0 < 8; e0 += 4) {
-      uint4 res[4];  // before the stores of these four, which the compiler cannot tell apart from them
+    for (int e0 = 0; e0 < 8; e0 += kAtOnce) {
+      uint4 res[kAtOnce];  // before the stores of these pieces, which the compiler cannot tell apart from them
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < kAtOnce; ++i)
         res[i] = p.residual != nullptr ? *reinterpret_cast<const uint4*>(stage + 4096 * c + lane * 128 + (((e0 + i) ^ (lane & 7)) << 4))
                                        : make_uint4(0u, 0u, 0u, 0u);
+      float2 y[4 * kAtOnce];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = e0 + i;
-        uint32_t packed[4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float2* v = &acc[32 * c + 4 * e + 2 * h];
-          const int owner = 16 * c + 2 * e + h;  // the lane with these four columns' biases
-          float2 y0 = activate2<kAct>(add2(v[0], Elem<T>::unpack(__shfl_sync(0xffffffffu, bias.x, owner))));
-          float2 y1 = activate2<kAct>(add2(v[1], Elem<T>::unpack(__shfl_sync(0xffffffffu, bias.y, owner))));
-          if (p.residual != nullptr) {
-            y0 = add2(y0, Elem<T>::unpack(h == 0 ? res[i].x : res[i].z));
-            y1 = add2(y1, Elem<T>::unpack(h == 0 ? res[i].y : res[i].w));
-          }
-          packed[2 * h] = Elem<T>::pack(y0);
-          packed[2 * h + 1] = Elem<T>::pack(y1);
-        }
-        *reinterpret_cast<uint4*>(stage + 4096 * c + lane * 128 + ((e ^ (lane & 7)) << 4)) = make_uint4(packed[0], packed[1], packed[2], packed[3]);
+      for (int i = 0; i < 2 * kAtOnce; ++i) {
+        const int owner = 16 * c + 2 * e0 + i;  // the lane with these four columns' biases
+        y[2 * i] = add2(acc[32 * c + 4 * e0 + 2 * i], Elem<T>::unpack(__shfl_sync(0xffffffffu, bias.x, owner)));
+        y[2 * i + 1] = add2(acc[32 * c + 4 * e0 + 2 * i + 1], Elem<T>::unpack(__shfl_sync(0xffffffffu, bias.y, owner)));
       }
+      activate_pairs<kAct>(y);
+      if (p.residual != nullptr) {
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          y[4 * i] = add2(y[4 * i], Elem<T>::unpack(res[i].x));
+          y[4 * i + 1] = add2(y[4 * i + 1], Elem<T>::unpack(res[i].y));
+          y[4 * i + 2] = add2(y[4 * i + 2], Elem<T>::unpack(res[i].z));
+          y[4 * i + 3] = add2(y[4 * i + 3], Elem<T>::unpack(res[i].w));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+        *reinterpret_cast<uint4*>(stage + 4096 * c + lane * 128 + (((e0 + i) ^ (lane & 7)) << 4)) =
+            make_uint4(Elem<T>::pack(y[4 * i]), Elem<T>::pack(y[4 * i + 1]), Elem<T>::pack(y[4 * i + 2]), Elem<T>::pack(y[4 * i + 3]));
     }
     send_staged(p, omap, stage + 4096 * c, row0, col0 + 64 * c);
   }
@@ -819,27 +824,20 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       const float* sa = p.sa + static_cast<int64_t>(min(row0 + lane, p.M - 1)) * p.sa_stride;
       // The columns start at a multiple of their number, so they lie in one scale block.
       const float* sb = p.sb + static_cast<int64_t>(min(col0, p.N - 1) / kScaleBlock) * p.sb_stride;
-      uint2 bias = make_uint2(0u, 0u);
-      if (both) {
-        if constexpr (kFused) bias = wide_prepare<4>(p, stage, row0, col0);
-        float2 acc[64];
-        ok = wide_accumulate<4>(p, sm, sa, sb, from, free0, free1, b, phase, acc);
-        if constexpr (kFused) {
-          if (ok) wide_store_fused<4, kAct, T>(p, &omap, stage, row0, col0, bias, acc);
-        } else {
-          if (ok) wide_store<4>(p, &omap, stage, row0, col0, acc);
-        }
-      } else {
-        // Of a piece of 64 columns the second half has none: it reads what is there and keeps the barriers going.
-        if (kFused && !none) bias = wide_prepare<2>(p, stage, row0, col0);
-        float2 acc[32];
-        ok = wide_accumulate<2>(p, sm, sa, sb, from, free0, free1, b, phase, acc);
-        if constexpr (kFused) {
-          if (ok && !none) wide_store_fused<2, kAct, T>(p, &omap, stage, row0, col0, bias, acc);
-        } else {
-          if (ok && !none) wide_store<2>(p, &omap, stage, row0, col0, acc);
-        }
-      }
+      // Of a piece of 64 columns the second half has none: it reads what is there and keeps the barriers going.
+      auto piece = [&](auto chunks) {
+        constexpr int kChunks = decltype(chunks)::value;
+        const float a0 = __ldg(sa), b0 = __ldg(sb);
+        uint2 bias = make_uint2(0u, 0u);
+        if (kFused && !none) bias = wide_prepare<kChunks>(p, stage, row0, col0);
+        float2 acc[16 * kChunks];
+        ok = wide_accumulate<kChunks>(p, sm, sa, sb, a0, b0, from, free0, free1, b, phase, acc);
+        if (!ok || none) return;
+        if constexpr (kFused) wide_store_fused<kChunks, kAct, T>(p, &omap, stage, row0, col0, bias, acc);
+        else wide_store<kChunks>(p, &omap, stage, row0, col0, acc);
+      };
+      if (both) piece(std::integral_constant<int, 4>());
+      else piece(std::integral_constant<int, 2>());
       if (!ok) flag_failure(p.status);
     }
     if (kFused) asm volatile("cp.async.wait_all;" ::: "memory");  // of a piece whose products never came

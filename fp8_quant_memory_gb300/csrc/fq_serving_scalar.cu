@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(kThreads) matmul_scalar_kernel(const MatmulArg
     }
     if (a.bias != nullptr) acc = __fadd_rn(acc, ld_any(dt, a.bias, j));
     float2 y[1] = {make_float2(acc, 0.f)};
-    activate_pairs(a.activation, y);
+    activate_each(a.activation, y);
     acc = y[0].x;
     if (a.residual != nullptr) acc = __fadd_rn(acc, ld_any(dt, a.residual, i * a.residual_stride + j));
     st_any(dt, a.out, i * a.out_stride + j, acc);
