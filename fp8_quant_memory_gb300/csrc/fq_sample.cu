@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a,
         });
       }
       __syncthreads();
-      if (rounds == 1 && first_key - kMinusZero < n) {  // in one round -0 is counted on its own
+      if (rounds == 1 && top >= kZero && first_key - kMinusZero < n) {  // in one round -0 is counted on its own
         if (tid == 0) {
           sm.bin[first_key - kZero] += sm.bin[first_key - kMinusZero];
           sm.bin[first_key - kMinusZero] = 0;

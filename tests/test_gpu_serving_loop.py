@@ -475,6 +475,19 @@ def test_sample_all_magnitudes(dt, heat):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("least", [0x8001, 0x8002, 0x801F, 0x8020, 0x8021])
+def test_sample_largest_next_to_zero(least, dt):
+    """The largest is a few steps below zero (there is no zero to count with it), or is zero, of either sign."""
+    raw = torch.randint(least, least + 400, (20, 5003), generator=gen(least), dtype=torch.int64)
+    raw[:, 17], raw[10:15, ::7], raw[15:, ::5] = least, 0x8000, 0
+    x = (raw - 65536 * (raw >= 32768).long()).to(torch.int16).view(DT[dt]).cuda()
+    s = settings(20, least)
+    s["k"] = [0, 2000, 3000, -1] * 5
+    s["heat"] = [1.0, 1e-5, 1e-6, 3e-39 if dt == "fp16" else 3e-38] * 5
+    check_sample(x, **s, exact=False)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
 @pytest.mark.parametrize("B", [1, 2, 18, 20, 39, 77])
 @pytest.mark.parametrize("V", [8191, 8193, 16385, 33000, 70001])
 def test_sample_rows_cut_among_blocks(B, V, dt):
