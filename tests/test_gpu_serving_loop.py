@@ -484,7 +484,39 @@ def test_sample_largest_next_to_zero(least, dt):
     s = settings(20, least)
     s["k"] = [0, 2000, 3000, -1] * 5
     s["heat"] = [1.0, 1e-5, 1e-6, 3e-39 if dt == "fp16" else 3e-38] * 5
-    check_sample(x, **s, exact=False)
+    check_sample(x, **s)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("V", [8193, 9001, 30000])
+def test_sample_largest_behind_the_first_thousands(V, dt):
+    """The first 8192 of a row, from whose largest the bins are laid out, are far below the rest, or nothing at all."""
+    B, n = 28, 8192
+    x = logits(B, V, dt, V)
+    top = float(torch.finfo(DT[dt]).max)
+    for b in range(B):
+        head, tail = x[b, :n], x[b, n:]
+        kind = b % 14
+        if kind == 0: head.fill_(-math.inf)
+        if kind == 1: head.fill_(math.nan)
+        if kind == 2: head[::2], head[1::2] = -math.inf, math.nan
+        if kind == 3: head.fill_(torch.finfo(DT[dt]).min)
+        if kind == 4: head.sub_(1000.0), tail.mul_(50.0)
+        if kind == 5: head.mul_(2.0 ** -20).abs_().neg_(), tail.abs_()
+        if kind == 6: head.mul_(2.0 ** -20), tail.mul_(100.0)
+        if kind == 7: head.zero_(), tail.fill_(-0.0)
+        if kind == 8: head.fill_(-0.0), tail.abs_().neg_()
+        if kind == 9: tail[-1] = math.inf
+        if kind == 10: tail[-1] = top
+        if kind == 11: tail.fill_(math.nan)
+        if kind == 12: head.fill_(-1e-30), tail.fill_(1e-30)
+        if kind == 13: tail[:] = -math.inf
+    s = settings(B, V)
+    s["heat"] = [r or 2.0 for r in s["heat"]]
+    s["k"], s["top_p"] = [0, 3000] * 14, [1.0, 0.9, 0.99, 0.5] * 7
+    check_sample(x, **s)
+    s["heat"] = [30000.0 if dt == "fp16" else 1e30] * B
+    check_sample(x, **s)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
