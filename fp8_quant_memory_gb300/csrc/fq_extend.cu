@@ -7,7 +7,8 @@
 //
 // What bounds it: one launch and two dependent rounds of loads (lengths; table and ring entries), not bytes: a step of 64
 // tokens moves 3.6 KB, one of 65536 1 MB. They take 3.6 and 8.0 us. Every CTA sums all lengths itself (a few per thread), then takes its share of the
-// tokens and pages, so that none waits for another; only where lengths or pool are updated in place, the CTAs are one
+// tokens and pages, so that none waits for another (returned pages that go to places which this step's pages leave, in a ring
+// smaller than the pages, are one CTA's, with all that is to be read there first); only where lengths or pool are updated in place, the CTAs are one
 // cluster and write them behind its barrier, after every CTA has read them.
 #include "fq_serving.h"
 #include "fq_sync.cuh"
@@ -147,7 +148,12 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
     const int32_t b = owner(taken, a.B + 1, ~kRefused, static_cast<uint32_t>(free_count));
     last = taken[b] & ~kRefused;  // the sequence whose pages would pass the border is refused
   }
-  const int64_t room = F - free_count, returned = min(all_given, room);
+  // Places for returned pages: those behind the last free page, then those that this step's pages leave.
+  const int64_t room = F - free_count, returned = min(all_given, room + last), refilled = max(returned - room, static_cast<int64_t>(0));
+  // The first places are then written over: what is to be read there, tokens' pages among it, is left to the CTA that does so,
+  // behind a barrier of its own.
+  const uint32_t apart = ctas > 1 ? static_cast<uint32_t>(refilled) : 0u;
+  const int passes = apart > 0u && rank == 0u ? 2 : 1;
 
   // This thread and how many there are for the tokens, the pages taken and those returned.
   constexpr uint32_t kPart = kThreads / 4;
@@ -157,56 +163,63 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
     const uint32_t step_t = kSmallStep ? 2 * kPart : step;
     const uint32_t live = static_cast<uint32_t>(min(all_tokens[0], static_cast<int64_t>(a.tokens)));
     const uint32_t lane = threadIdx.x & 31;
-    // A warp takes 32 * kRun tokens in a row: their first and last sequence, then each token's between those.
-    for (uint32_t base = (first - lane) * kRun; base < live; base += step_t * kRun) {
-      int32_t b_first, b_last;
-      if constexpr (kRun > 1) {
-        // one search by each half of the warp
-        const int32_t found = owner(tokens, a.B, ~0u, lane < 16 ? base : min(base + 32 * kRun, live) - 1);
-        b_first = __shfl_sync(0xffffffffu, found, 0);
-        b_last = __shfl_sync(0xffffffffu, found, 31);
-      } else {
-        b_first = 0;
-        b_last = a.B - 1;
-      }
-      int32_t b[kRun], end[kRun];
-#pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        b[i] = b_first;
-        end[i] = b_last + 1;
-      }
-      for (int32_t n = b_last - b_first; n > 0; n >>= 1) {  // owner(tokens, ..) of each, side by side
+#pragma unroll 1
+    for (int pass = 0; pass < passes; ++pass) {
+      const uint32_t from = pass == 0 ? first : threadIdx.x, by = pass == 0 ? step_t : kThreads;
+      // A warp takes 32 * kRun tokens in a row: their first and last sequence, then each token's between those.
+      for (uint32_t base = (from - lane) * kRun; base < live; base += by * kRun) {
+        int32_t b_first, b_last;
+        if constexpr (kRun > 1) {
+          // one search by each half of the warp
+          const int32_t found = owner(tokens, a.B, ~0u, lane < 16 ? base : min(base + 32 * kRun, live) - 1);
+          b_first = __shfl_sync(0xffffffffu, found, 0);
+          b_last = __shfl_sync(0xffffffffu, found, 31);
+        } else {
+          b_first = 0;
+          b_last = a.B - 1;
+        }
+        int32_t b[kRun], end[kRun];
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
-          const int32_t mid = (b[i] + end[i]) >> 1;
-          if (end[i] - b[i] > 1) {
-            if (tokens[mid] <= base + 32 * i + lane) b[i] = mid;
-            else end[i] = mid;
+          b[i] = b_first;
+          end[i] = b_last + 1;
+        }
+        for (int32_t n = b_last - b_first; n > 0; n >>= 1) {  // owner(tokens, ..) of each, side by side
+#pragma unroll
+          for (int i = 0; i < kRun; ++i) {
+            const int32_t mid = (b[i] + end[i]) >> 1;
+            if (end[i] - b[i] > 1) {
+              if (tokens[mid] <= base + 32 * i + lane) b[i] = mid;
+              else end[i] = mid;
+            }
           }
         }
-      }
-      int32_t pos[kRun], id[kRun];
-      uint32_t in_page[kRun];
+        int32_t pos[kRun], id[kRun];  // a negative position: not of this pass
+        uint32_t in_page[kRun];
 #pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        const uint32_t t = base + 32 * i + lane;
-        pos[i] = 0;
-        id[i] = -1;
-        in_page[i] = 0;
-        if (t >= live) continue;
-        const uint32_t len = lens[b[i]], own = taken[b[i]];
-        pos[i] = cut(static_cast<int64_t>(len) + (t - tokens[b[i]]));
-        if ((own & kRefused) != 0u) continue;
-        const uint32_t p = page_of(a, pos[i]), held = pages_of(a, len);
-        in_page[i] = pos[i] - p * a.page_size;
-        id[i] = __ldcg(p < held ? a.table + b[i] * a.table_stride + p : place(static_cast<int64_t>(own) + (p - held)));
-      }
+        for (int i = 0; i < kRun; ++i) {
+          const uint32_t t = base + 32 * i + lane;
+          pos[i] = -1;
+          id[i] = -1;
+          in_page[i] = 0;
+          if (t >= live) continue;
+          const uint32_t len = lens[b[i]], own = taken[b[i]], held = pages_of(a, len);
+          const int32_t at_t = cut(static_cast<int64_t>(len) + (t - tokens[b[i]]));
+          const uint32_t p = page_of(a, at_t), nth = own + (p - held);  // of the pages taken, if p is one
+          const bool granted = (own & kRefused) == 0u, late = granted && p >= held && nth < apart;
+          if (late != (pass == 1)) continue;
+          pos[i] = at_t;
+          if (!granted) continue;
+          in_page[i] = at_t - p * a.page_size;
+          id[i] = __ldcg(p < held ? a.table + b[i] * a.table_stride + p : place(nth));
+        }
 #pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        const uint32_t t = base + 32 * i + lane;
-        if (t >= live) continue;
-        a.slots[t] = id[i] >= 0 ? static_cast<int64_t>(id[i]) * a.page_size + in_page[i] : -1;
-        a.positions[t] = pos[i];
+        for (int i = 0; i < kRun; ++i) {
+          const uint32_t t = base + 32 * i + lane;
+          if (pos[i] < 0) continue;
+          a.slots[t] = id[i] >= 0 ? static_cast<int64_t>(id[i]) * a.page_size + in_page[i] : -1;
+          a.positions[t] = pos[i];
+        }
       }
     }
     for (uint32_t t = live + first; t < static_cast<uint32_t>(a.tokens); t += step_t) {
@@ -216,33 +229,41 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
   }
   if (!kSmallStep || warps_of == 2) {
     const uint32_t first_p = kSmallStep ? threadIdx.x - 2 * kPart : first, step_p = kSmallStep ? kPart : step;
-    for (int64_t j = first_p; j < last; j += step_p) {
+    auto take = [&](int64_t j) {
       const int32_t b = owner(taken, a.B, ~kRefused, static_cast<uint32_t>(j));
       const int64_t held = pages_of(a, lens[b]);
       a.table[b * a.table_stride + held + (j - (taken[b] & ~kRefused))] = __ldcg(place(j));
-    }
+    };
+    for (int64_t j = static_cast<int64_t>(apart) + first_p; j < last; j += step_p) take(j);
+    if (passes == 2)
+      for (int64_t j = threadIdx.x; j < apart; j += kThreads) take(j);
   }
   if (!kSmallStep || warps_of == 3) {
     const uint32_t first_p = kSmallStep ? threadIdx.x - 3 * kPart : first, step_p = kSmallStep ? kPart : step;
     constexpr int kAtOnce = 4;
-    for (int64_t j0 = first_p; j0 < returned; j0 += kAtOnce * static_cast<int64_t>(step_p)) {
+    for (int64_t j0 = first_p; j0 < returned - refilled; j0 += kAtOnce * static_cast<int64_t>(step_p)) {
       int32_t id[kAtOnce];
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
         const int64_t j = j0 + i * static_cast<int64_t>(step_p);
-        if (j >= returned) continue;
+        if (j >= returned - refilled) continue;
         const int32_t b = owner(given, a.B, ~0u, static_cast<uint32_t>(j));
         id[i] = __ldcg(a.table + b * a.table_stride + (j - given[b]));
       }
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
         const int64_t j = j0 + i * static_cast<int64_t>(step_p);
-        if (j < returned) *place(free_count + j) = id[i];
+        if (j < returned - refilled) *place(free_count + j) = id[i];
       }
     }
   }
-  // In place: every CTA has read the lengths and the pool.
   __syncthreads();
+  if (refilled > 0 && rank == 0u)  // all that lay there has been read, by this CTA
+    for (int64_t j = room + threadIdx.x; j < returned; j += kThreads) {
+      const int32_t b = owner(given, a.B, ~0u, static_cast<uint32_t>(j));
+      *place(j - room) = __ldcg(a.table + b * a.table_stride + (j - given[b]));
+    }
+  // In place: every CTA has read the lengths and the pool.
   if (a.in_place != 0 && ctas > 1) cluster_barrier();
   for (int32_t b = first; b <= a.B; b += step) {
     a.starts[b] = static_cast<int32_t>(tokens[b]);

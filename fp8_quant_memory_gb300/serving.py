@@ -108,7 +108,8 @@ def paged_extend(page_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: tor
 
     page_table: [B, max_pages], seq_lens and new_lens: [B], free_pages: [ring], a ring of the ids of free pages, pool:
     [3] = its front, how many are free, (not read); all int32. New pages come from the ring's front and enter page_table;
-    those of sequences that end go behind its last. Sequences whose tokens fit neither the table, nor max_tokens, nor the
+    those of sequences that end go behind its last (a ring of at least as many places as there are pages holds them
+    all; others are dropped). Sequences whose tokens fit neither the table, nor max_tokens, nor the
     free pages are left as they are (include/fq.h has the rule).
     Returns (slots int64 [max_tokens], positions int32 [max_tokens], starts int32 [B + 1], seq_lens_out, pool_out): what
     qkv_norm_rope_append and paged_attention take, slots of -1 behind the last token. pool_out[2] counts the pages that

@@ -416,8 +416,9 @@ int fq_paged_attention_window(const uint8_t* q, int64_t q_stride, const float* q
  *     page * page_size + position % page_size, or -1 where it is not granted or that page's id is negative.
  *   - Behind the last sequence's tokens, up to max_tokens: slot -1, position 0.
  * pool_out: {ring's new front, free pages, pages that sequences which were not granted theirs had asked for}.
- * pool[0] counts modulo `ring`, pool[1] within [0, ring]; pages returned to a full ring are dropped. pool[2] is not
- * read. seq_lens_out and pool_out may be seq_lens and pool (a graph that is replayed then advances); otherwise outputs
+ * pool[0] counts modulo `ring`, pool[1] within [0, ring]. Pages are taken from the ring before others are returned to it,
+ * so a ring of at least as many places as there are pages in all holds every one; what a smaller one has no place for,
+ * the places emptied by this step among them, is dropped, the last of the returned first. pool[2] is not read. seq_lens_out and pool_out may be seq_lens and pool (a graph that is replayed then advances); otherwise outputs
  * overlap nothing. slots: [max_tokens] int64; positions: [max_tokens] int32. table_stride >= max_pages.
  * B <= 12288 (else FQ_ERR_UNSUPPORTED), ring >= 1, page_size >= 1, max_pages * page_size < 2^31. B = 0 and
  * max_tokens = 0 are allowed.
