@@ -83,6 +83,7 @@ struct ExtendArgs {
   uint32_t page_magic;  // t / page_size = (t * page_magic) >> page_magic_shift for t < 2^31
   int32_t page_magic_shift;
   int32_t in_place;  // lens_out is lens, or pool_out pool
+  int32_t team, workers;  // CTAs that return pages (a cluster, the first), that take tokens (the last)
 };
 
 struct SampleArgs {

@@ -93,7 +93,8 @@ def paged_attention(q: torch.Tensor, q_scale: torch.Tensor, k_cache: torch.Tenso
     max_seq_len: an upper bound of the lengths known on the host (default: what the page table holds);
     longer sequences are cut to it. out: [B, Hq, D]; lse: fp32 [B, Hq]. A workspace that is passed
     (uint8) must not be in use by another call that may run at the same time.
-    window: only the last ``window`` tokens of a sequence take part, and the first ``sinks`` (None: all of them).
+    window: only the last ``window`` tokens of a sequence take part, and the first ``sinks`` (None: all of them). Whoever
+    returns a page that a window has passed writes a negative id in its place of page_table.
     """
     return (_native or _load()).paged_attention(q, q_scale, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens,
                                                 softmax_scale, out_dtype, max_seq_len, want_lse, out, lse, workspace, window,
@@ -108,8 +109,8 @@ def paged_extend(page_table: torch.Tensor, seq_lens: torch.Tensor, new_lens: tor
 
     page_table: [B, max_pages], seq_lens and new_lens: [B], free_pages: [ring], a ring of the ids of free pages, pool:
     [3] = its front, how many are free, (not read); all int32. New pages come from the ring's front and enter page_table;
-    those of sequences that end go behind its last (a ring of at least as many places as there are pages holds them
-    all; others are dropped). Sequences whose tokens fit neither the table, nor max_tokens, nor the
+    those of sequences that end, but for negative (absent) ids, go behind its last (a ring of at least as many places as
+    there are pages holds them all; others are dropped). Sequences whose tokens fit neither the table, nor max_tokens, nor the
     free pages are left as they are (include/fq.h has the rule).
     Returns (slots int64 [max_tokens], positions int32 [max_tokens], starts int32 [B + 1], seq_lens_out, pool_out): what
     qkv_norm_rope_append and paged_attention take, slots of -1 behind the last token. pool_out[2] counts the pages that

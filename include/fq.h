@@ -389,8 +389,9 @@ int fq_paged_attention(const uint8_t* q, int64_t q_stride, const float* q_scale,
  * fq_paged_attention of a sliding window with sinks: of a sequence of len_b tokens only those with
  *   j < sinks   or   j >= len_b - window
  * take part (window >= 1, sinks >= 0; a window of at least max_seq_len sees every token, and the call is then
- * fq_paged_attention's, bit for bit). Pages in between are not read; their table entries may be anything. Other
- * arguments, workspace and errors as fq_paged_attention.
+ * fq_paged_attention's, bit for bit). Pages in between are not read; their table entries may be anything to this call.
+ * fq_paged_extend returns what a row holds when its sequence ends: a caller that gives such a page back before, behind
+ * the free ring's last, writes a negative id in its place. Other arguments, workspace and errors as fq_paged_attention.
  */
 int fq_paged_attention_window(const uint8_t* q, int64_t q_stride, const float* q_scale, int64_t q_scale_stride,
                               const fq_paged_cache* cache, const int32_t* page_table, int64_t table_stride,
@@ -410,8 +411,9 @@ int fq_paged_attention_window(const uint8_t* q, int64_t q_stride, const float* q
  *     (starts[b+1] <= max_tokens), and the pages it needs are left: those that it and the sequences before it need
  *     (of the ones that fit) are pool[1] at most, or it needs none.
  *   - Granted: its new pages, next from the ring's front, enter its row of the table; seq_lens_out[b] = len + new.
- *     Not granted: row and length stay as they are. Ended: its pages (those below max_pages) go behind the ring's
- *     last, to be given out from the next step on, in order; seq_lens_out[b] = 0; its row stays as it is.
+ *     Not granted: row and length stay as they are. Ended: its pages (the ids of its row's entries below
+ *     ceil(len/page_size) and max_pages that are not negative) go behind the ring's last, to be given out from the next
+ *     step on, in order; seq_lens_out[b] = 0; its row stays as it is.
  *   - Token i of it is at position len + i: positions[starts[b] + i] (at most 2^31 - 1), slots[starts[b] + i] =
  *     page * page_size + position % page_size, or -1 where it is not granted or that page's id is negative.
  *   - Behind the last sequence's tokens, up to max_tokens: slot -1, position 0.

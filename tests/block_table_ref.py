@@ -1,5 +1,6 @@
 """A plain implementation of block tables and slot maps as include/fq.h states them, around a list of the free pages: pages are
-taken from its front, then those of sequences that end go behind its last, as far as the ring has places."""
+taken from its front, then those of sequences that end (absent ones, negative, aside) go behind its last, as far as the ring
+has places."""
 from __future__ import annotations
 
 MAX32 = 2 ** 31 - 1
@@ -22,7 +23,7 @@ def extend(table, lens, new, ring, pool, page, T):
         starts.append(start + max(m, 0))
         held = ceil(n, page)
         if m < 0:
-            ended += table[b][:min(held, W)]
+            ended += [id for id in table[b][:min(held, W)] if id >= 0]
             out.append(0)
             continue
         fits = ceil(n + m, page) <= W and starts[-1] <= T

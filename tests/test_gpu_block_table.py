@@ -1,5 +1,5 @@
 """GPU parity of paged_extend where its ring and its rows are not as a fresh server has them: rings with fewer places than there
-are pages."""
+are pages, rows whose pages were given back before their sequences end."""
 import random
 
 import pytest
@@ -61,3 +61,57 @@ def test_ring_smaller_than_the_pages(fill, B, T, in_place):
     taken = sum(x != y for old, row in zip(table, want["table"]) for x, y in zip(old, row))
     if fill == 1.0 and ended:  # every page that returned is in a place that the step has emptied
         assert 0 < want["pool"][1] - (F - taken) <= taken
+
+
+def absent(kind, ids, r):
+    """A row's ids with some of them absent."""
+    n = len(ids)
+    if kind == "some": return [-1 if r.random() < 0.3 else x for x in ids]
+    if kind == "one": return [-5 if i == n // 2 and r.random() < 0.2 else x for i, x in enumerate(ids)]
+    if kind == "window": return [x if i < 1 or i >= n - 3 else -1 for i, x in enumerate(ids)]
+    return [-2 ** 31] * n if kind == "all" or r.random() < 0.5 else ids
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("B,T,W", [(5, 40, 9), (64, 250, 40), (300, 900, 60), (400, 9000, 200), (900, 5000, 40), (3, 2000, 20000)])
+@pytest.mark.parametrize("kind", ["some", "one", "window", "all", "rows"])
+@pytest.mark.parametrize("small", [False, True])
+def test_absent_pages_do_not_return(small, kind, B, T, W, in_place):
+    """Rows of up to several thousand pages, of which some are absent; rings of enough places and of too few."""
+    r = random.Random(B + T + len(kind))
+    page = 4
+    lens = [r.randrange(W * page - 4 * page) for _ in range(B)]
+    new = [-1 if r.random() < 0.5 else r.choice([0, 1, 1, 5]) for _ in range(B)]
+    new[0], new[-1] = -1, 3
+    order = list(range(B * W + 200))
+    r.shuffle(order)
+    own = iter(order)
+    table = [absent(kind if m < 0 else "", ids, r) if m < 0 else ids for ids, m in
+             (([next(own) for _ in range(ref.ceil(n, page))], m) for n, m in zip(lens, new))]
+    returned = sum(x >= 0 for ids, m in zip(table, new) if m < 0 for x in ids)
+    table = [ids + [-1] * (W - len(ids)) for ids in table]
+    free = 100
+    F = max(free, free + returned // 2 if small else free + returned + 5)
+    ring = [next(own) if i < free else -1 for i in range(F)]
+    head = r.randrange(F)
+    ring = [ring[(i - head) % F] for i in range(F)]
+    want = check(table, lens, new, ring, [head, free, 0], page, T, in_place)
+    held = [want["ring"][(want["pool"][0] + i) % F] for i in range(want["pool"][1])]
+    assert min(held, default=0) >= 0 and len(set(held)) == len(held)
+
+
+def test_pages_given_back_before_the_end_are_granted_once():
+    """A window of one page over sequences of four: the two in between go back to the ring by hand, then the sequences end and
+    others take all the pages."""
+    page, B = 4, 6
+    table = [[4 * b + i for i in range(4)] for b in range(B)]
+    ring, pool = [-1] * 24, [20, 0, 0]
+    back = [id for row in table for id in row[1:3]]
+    for row in table:
+        row[1] = row[2] = -1
+    for j, id in enumerate(back):
+        ring[(pool[0] + j) % 24] = id
+    pool[1] = len(back)
+    w = check(table, [16] * B, [-1] * B, ring, pool, page, 1, False)
+    w = check([[-1] * 4] * B, [0] * B, [16] * B, w["ring"], w["pool"], page, 16 * B, True)
+    assert sorted(id for row in w["table"] for id in row) == list(range(24)) and min(w["slots"]) >= 0 and w["pool"][2] == 0
