@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     float* scale = a.scale + static_cast<int64_t>(t) * a.Hq + h;
     bool live = inside;
     if (!is_q) {
-      const int64_t slot = __ldg(p.slots + t);
+      const int64_t slot = p.slots[t];
       live = inside && slot >= 0 && slot < p.cache.pages * p.cache.page_size;
       int64_t page = 0, off = 0;
       if (live) locate(p.cache, slot, &page, &off);

@@ -133,7 +133,7 @@ struct Maps {
 };
 
 __device__ __forceinline__ int32_t length_of(const PagedArgs& p, int32_t b) {
-  return max(0, min(__ldg(p.lens + b), p.max_len));
+  return max(0, min(p.lens[b], p.max_len));
 }
 
 // The tokens of a sequence that take part, [0, sunk) and [start, len), and the tiles that hold them: the first `low`, then
@@ -354,7 +354,7 @@ __device__ __forceinline__ void produce_rows(const SplitArgs& a, Shared<DP, HG>&
   auto look_up = [&]() {
 #pragma unroll
     for (int q = 0; q < kQ; ++q)
-      page[q] = tok + 32 * q < at.len && lane + 32 * q < kTok && span.sees(tok + 32 * q) ? __ldg(table + page_index(tok + 32 * q)) : -1;
+      page[q] = tok + 32 * q < at.len && lane + 32 * q < kTok && span.sees(tok + 32 * q) ? table[page_index(tok + 32 * q)] : -1;
   };
   enter();
   look_up();
@@ -475,7 +475,7 @@ struct BoxFeed {
   __device__ __forceinline__ int32_t index_of(const SplitArgs& a, int32_t t) const {
     return static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(t)) * a.page_magic) >> a.page_magic_shift);
   }
-  __device__ __forceinline__ int32_t entry(int32_t i) const { return i < pages_here ? __ldg(table + i) : -1; }
+  __device__ __forceinline__ int32_t entry(int32_t i) const { return i < pages_here ? table[i] : -1; }
 
   // At unit `at`, whose first token is `base`.
   __device__ __forceinline__ void enter(const SplitArgs& a) {
@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int i = 0; i < DP / 64; ++i) {
         const int d = i < 2 * S::kA ? 128 * (i >> 1) + 16 * (2 * c + (i & 1)) : 128 * S::kA + 16 * c;
-        const uint4 v = h < rows && d < p.D ? __ldg(reinterpret_cast<const uint4*>(src + d)) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 v = h < rows && d < p.D ? *reinterpret_cast<const uint4*>(src + d) : make_uint4(0u, 0u, 0u, 0u);
         uint4 lo, hi;
         codes_f16(v.x, lo.x, lo.y);
         codes_f16(v.y, lo.z, lo.w);
@@ -781,7 +781,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int32_t he = kHeads * group + 2 * c + e;
-        qf[e] = he < rows ? __ldg(p.q_scale + static_cast<int64_t>(use.b) * p.q_scale_stride + head0 + he) * p.scale_log2 : 0.f;
+        qf[e] = he < rows ? p.q_scale[static_cast<int64_t>(use.b) * p.q_scale_stride + head0 + he] * p.scale_log2 : 0.f;
         m[e] = mo[e] = kLowest;
         l[e] = 0.f;
       }

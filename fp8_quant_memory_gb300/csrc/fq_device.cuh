@@ -158,9 +158,17 @@ __device__ __forceinline__ float2 round_trip(float2 v) {
 // ------------------------------------------------------------------------------------------------
 __device__ __forceinline__ uint4 ld_stream16(const void* p) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                : "l"(p));
+  return r;
+}
+
+// A load that stays where it is written among the waits and other such loads (a plain one moves, which cost the matrix
+// product's blocks of k 0.5 us of 66).
+__device__ __forceinline__ float ld_f32(const float* p) {
+  float r;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(r) : "l"(p));
   return r;
 }
 

@@ -103,8 +103,8 @@ __device__ __forceinline__ void owners(const uint32_t* first, int32_t n, uint32_
   }
 }
 
-// Lengths, pool, table and ring are read through L2: this call writes them, and a kernel that starts on the same SM
-// before this one ends must not find their old lines in L1.
+// Lengths, pool, table and ring are read through L2: other CTAs of this call write them, and no line of L1 is left with what
+// they held before.
 
 // Page of position t < 2^31; pages of n < 2^31 tokens.
 __device__ __forceinline__ uint32_t page_of(const ExtendArgs& a, uint32_t t) {

@@ -291,11 +291,11 @@ __global__ void __launch_bounds__(kNarrowThreads<G>, 1)
     constexpr int kL = (NT + 31) / 32;  // scales of a that a lane brings per block
     float next[kL];
     auto fetch = [&](int k) {
-      const float b = __ldg(sb + k);
+      const float b = sb[k];
 #pragma unroll
       for (int i = 0; i < kL; ++i) {
         const int j = lane + 32 * i;
-        next[i] = j < NT && t0 + j < p.M ? __ldg(p.sa + static_cast<int64_t>(t0 + j) * p.sa_stride + k) * b : 0.f;
+        next[i] = j < NT && t0 + j < p.M ? p.sa[static_cast<int64_t>(t0 + j) * p.sa_stride + k] * b : 0.f;
       }
     };
     // The residuals of the outputs that this thread will finish are on their way during the products, as far as there
@@ -526,8 +526,8 @@ __device__ __forceinline__ bool wide_accumulate(const MmArgs& p, Sm& sm, const f
   for (int kb = 0; kb < p.nkb; ++kb) {
     const float2 s2 = splat2(a_next * b_next);
     if (kb + 1 < p.nkb) {
-      a_next = __ldg(sa + kb + 1);
-      b_next = __ldg(sb + kb + 1);
+      a_next = ld_f32(sa + kb + 1);
+      b_next = ld_f32(sb + kb + 1);
     }
     // one verdict for the whole warp: the loads below are collective
     if (!__all_sync(0xffffffffu, mbar_wait(kWaitLimitNs, &sm.done[b], phase))) return false;
@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // Of a piece of 64 columns the second half has none: it reads what is there and keeps the barriers going.
       auto piece = [&](auto chunks) {
         constexpr int kChunks = decltype(chunks)::value;
-        const float a0 = __ldg(sa), b0 = __ldg(sb);
+        const float a0 = ld_f32(sa), b0 = ld_f32(sb);
         uint2 bias = make_uint2(0u, 0u);
         if (kFused && !none) bias = wide_prepare<kChunks>(p, stage, row0, col0);
         float2 acc[16 * kChunks];

@@ -239,7 +239,7 @@ struct Row {
     last = max(first, static_cast<int32_t>((static_cast<int64_t>(V) + skip) / 8));
   }
   __device__ __forceinline__ uint4 whole(int32_t v) const {
-    return __ldg(reinterpret_cast<const uint4*>(x + (8 * static_cast<int64_t>(v) - skip)));
+    return ld_stream16(x + (8 * static_cast<int64_t>(v) - skip));
   }
   __device__ __forceinline__ uint4 part(int32_t v) const {
     uint32_t w[4] = {~0u, ~0u, ~0u, ~0u};
@@ -680,8 +680,8 @@ struct Setting {
   float temperature, top_p, min_p;
   int32_t k;
   __device__ __forceinline__ Setting(const SampleArgs& a, int32_t b)
-      : temperature(a.temperature == nullptr ? 1.f : __ldg(a.temperature + b)), top_p(a.top_p == nullptr ? 1.f : __ldg(a.top_p + b)),
-        min_p(a.min_p == nullptr ? 0.f : __ldg(a.min_p + b)), k(a.top_k == nullptr ? 0 : __ldg(a.top_k + b)) {}
+      : temperature(a.temperature == nullptr ? 1.f : a.temperature[b]), top_p(a.top_p == nullptr ? 1.f : a.top_p[b]),
+        min_p(a.min_p == nullptr ? 0.f : a.min_p[b]), k(a.top_k == nullptr ? 0 : a.top_k[b]) {}
   // Whether the largest alone is asked for.
   __device__ __forceinline__ bool greedy() const { return !(temperature >= 1.17549435e-38f) || k == 1; }
   // Whether every token counts (no top-k that a list holds, nor a min-p alone): such a row takes longer than others. The list
