@@ -825,6 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleArgs a,
     c.heat = heat_of(value_of<T>(top), set.temperature);
     c.top = top;
     c.top_k = set.k <= 0 ? 0xffffffffu : static_cast<uint32_t>(set.k);
+    // (above 1 as 1: the largest and its equals)
     c.min_weight = min_p > 0.f ? static_cast<uint64_t>(share_of(fminf(min_p, 1.f), static_cast<u128>(1) << kOne, true)) : 0;
     // Which keys count at all. Those below min_p matter to the sum that top_p is a part of, but without top_p to nothing.
     float reach = 45.f;

@@ -127,7 +127,7 @@ def sample(logits: torch.Tensor, u: torch.Tensor, temperature: torch.Tensor | No
 
     temperature, top_p, min_p: fp32 [B], top_k: int32 [B], each row its own; None leaves a step out. The cuts apply in the
     order top-k, top-p, min-p to the tokens by falling logit (equal ones by rising index); u picks along that order.
-    temperature 0 takes the largest. Returns (token int64 [B], logprob fp32 [B] of the token among those kept, or None);
+    temperature 0 takes the largest; a min_p above 1 counts as 1 (the largest and its equals stay). Returns (token int64 [B], logprob fp32 [B] of the token among those kept, or None);
     -1 for a row whose mask (-inf) leaves nothing.
     """
     return (_native or _load()).sample(logits, u, temperature, top_k, top_p, min_p, want_logprob, token, logprob)

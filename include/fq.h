@@ -436,7 +436,7 @@ int fq_paged_extend(int32_t* page_table, int64_t table_stride, const int32_t* se
  *   top-k: the first top_k tokens of the order stay (top_k <= 0 or >= V: all);
  *   top-p: of these, those before which the sum of w is below top_p times the sum over them all, and the first
  *          (top_p >= 1: all);
- *   min-p: of these, those with w >= min_p (and the first);
+ *   min-p: of these, those with w >= min_p, which counts as 1 where it is above 1 (the largest and those equal to it);
  *   token: the first of these in the order up to and with which the sum of w exceeds u times the sum over these;
  *   logprob = log(w of the token / that sum).
  * A temperature that is not at least 2^-126 gives the first token of the order, logprob 0. u is cut to [0, 1 - 2^-24].
