@@ -7,7 +7,8 @@
 // search for the bin in which a running sum passes a border. The token is then the n-th of the row with that value.
 //
 // Borders are met by random numbers, and results have to be those of exact arithmetic: weights are computed in two fp32
-// words each (2^-41 of themselves), held as integers in units of 2^-62 of the largest, and summed in 128 bits. fp64
+// words each (2^-41 of themselves), held as integers in units of 2^-62 of the largest, and summed in 128 bits. (A bin's, which is
+// the product of two such, is right to 2^-40 or four units: one for each factor's rounding, two for the product's.) fp64
 // instructions would cost more than everything else here (2 a clock and SM: a division by every thread was 6 us).
 //
 // A block takes a row in three ways. A row's largest alone (temperature 0, top-k 1): one pass. Few tokens (a top-k, a min-p
@@ -377,7 +378,7 @@ struct Sum {
   __device__ __forceinline__ u128 whole() const { return (static_cast<u128>(hi) << 31) + lo; }
 };
 
-// a * b / 2^62 of numbers up to 2^62, rounded down but for 1; the low limbs' product is below that.
+// a * b / 2^62 of numbers up to 2^62, less 2 at most: the low limbs' product, below 1, is left out, and the rest rounded down.
 __device__ __forceinline__ uint64_t product62(uint64_t a, uint64_t b) {
   const uint32_t a0 = static_cast<uint32_t>(a) & 0x7fffffffu, a1 = static_cast<uint32_t>(a >> 31);
   const uint32_t b0 = static_cast<uint32_t>(b) & 0x7fffffffu, b1 = static_cast<uint32_t>(b >> 31);
@@ -400,8 +401,8 @@ __device__ __forceinline__ uint32_t among_first(uint32_t count, uint32_t rank, u
 // up counts times steps, two instructions a bin, and multiplies by the group's first weight once. (A weight for each bin by
 // itself took 90 instructions of each lane, 20 of the 29 thousand clocks of a row of 151936 fp16 logits.) Bins are taken
 // one by one where that does not do: in the first group, whose first values may be above the largest of the row, in one that
-// top-k or min-p cuts, and at exponents 2^-32 of the largest. A group's sum and the sum over its bins may differ in the last
-// of 62 bits of each.
+// top-k or min-p cuts, and at exponents 2^-32 of the largest. A group's sum, rounded down twice, and the sum over its bins may
+// differ by a unit or two a token.
 template <typename T>
 struct Round {
   uint32_t first_key;

@@ -442,8 +442,9 @@ int fq_paged_extend(int32_t* page_table, int64_t table_stride, const int32_t* se
  * A temperature that is not at least 2^-126 gives the first token of the order, logprob 0. u is cut to [0, 1 - 2^-24].
  * A NaN counts as -inf. -inf takes no part; a row of nothing else gives token -1 and logprob -inf. Where +inf
  * occurs, it alone counts. A NaN among the parameters switches its step off (temperature: as 0; u: as 0).
- * Sums are exact sums of weights that are right to 2^-40 of themselves or 2^-62 of the largest, and the borders exact
- * products of them, so that a result is that of 64-bit arithmetic but for borders met to about 2^-40 of the sum.
+ * Weights are whole numbers in units of 2^-62 of the largest, right to 2^-40 of themselves or four units; sums of them are
+ * exact, but for two units a run of 32 neighbouring 16-bit values, and so are the borders' products. So a result is that of
+ * 64-bit arithmetic but for borders met to about 2^-40 of the sum, or V units where that is more.
  * logits: [B, V] dtype, rows `stride` >= 0 elements apart; u, temperature, top_p, min_p: [B] fp32, top_k: [B] int32; each
  * of the last four may be null (T = 1, no cut). token: [B] int64; logprob: [B] fp32 or null. B >= 0 (0: no-op),
  * 1 <= V < 2^31 - 1024. Any alignment and stride; the same call gives the same tokens on every GPU and run.
