@@ -94,12 +94,6 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 }
 
 // --------------------------------------------------------------------------------- clusters
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t n;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
-  return n;
-}
-
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
