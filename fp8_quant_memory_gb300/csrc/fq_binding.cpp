@@ -81,12 +81,23 @@ double real(PyObject* o) {
 
 cudaStream_t stream_of(Tensor t) { return c10::cuda::getCurrentCUDAStream(t.device().index()).stream(); }
 
+// The interpreter lock, given up for a scope: taken again however that is left, since what catches a C++ exception (a tensor
+// without memory of its own has thrown) sets a Python error.
+struct Unlocked {
+  PyThreadState* const state = PyEval_SaveThread();
+  Unlocked() = default;
+  Unlocked(const Unlocked&) = delete;
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // Runs an entry point without the interpreter lock (strict mode waits in it) and raises FqError on failure.
 template <typename F>
 void launch(const char* fn, F f) {
   int rc;
-  Py_BEGIN_ALLOW_THREADS rc = f();
-  Py_END_ALLOW_THREADS
+  {
+    const Unlocked scope;
+    rc = f();
+  }
   if (rc == FQ_OK) return;
   PyObject* e = PyObject_CallFunction(g_fq_error, "sis", fn, rc, fq_last_error());
   if (e != nullptr) {
