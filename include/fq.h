@@ -389,7 +389,9 @@ int fq_paged_attention(const uint8_t* q, int64_t q_stride, const float* q_scale,
  * fq_paged_attention of a sliding window with sinks: of a sequence of len_b tokens only those with
  *   j < sinks   or   j >= len_b - window
  * take part (window >= 1, sinks >= 0; a window of at least max_seq_len sees every token, and the call is then
- * fq_paged_attention's, bit for bit). Pages in between are not read; their table entries may be anything to this call.
+ * fq_paged_attention's, bit for bit). The arithmetic is the same: fp32, but for the probabilities times V scales, which are
+ * rounded once to fp16 (the largest part of the error with fp16 outputs: 2.6e-4 of the result's norm against the 2.1e-4 that
+ * the output's own rounding leaves; bf16 outputs round eight times coarser). Pages in between are not read; their table entries may be anything to this call.
  * fq_paged_extend returns what a row holds when its sequence ends: a caller that gives such a page back before, behind
  * the free ring's last, writes a negative id in its place. Other arguments, workspace and errors as fq_paged_attention.
  */
