@@ -115,3 +115,63 @@ def test_pages_given_back_before_the_end_are_granted_once():
     w = check(table, [16] * B, [-1] * B, ring, pool, page, 1, False)
     w = check([[-1] * 4] * B, [0] * B, [16] * B, w["ring"], w["pool"], page, 16 * B, True)
     assert sorted(id for row in w["table"] for id in row) == list(range(24)) and min(w["slots"]) >= 0 and w["pool"][2] == 0
+
+
+def state(B, W, page, seed):
+    """A state with pages to spare, some sequences of which end."""
+    r = random.Random(seed)
+    lens = [r.randrange(W * page // 2) for _ in range(B)]
+    new = [-1 if r.random() < 0.2 else r.choice([0, 1, 1, 9]) for _ in range(B)]
+    own = iter(r.sample(range(2 * B * W), 2 * B * W))
+    table = [[next(own) if i < ref.ceil(n, page) else -1 for i in range(W)] for n in lens]
+    return table, lens, new, [next(own) for _ in range(B * W)], [r.randrange(B * W), B * W // 2, 0]
+
+
+@pytest.mark.parametrize("which", ["seq_lens_out", "pool_out"])
+@pytest.mark.parametrize("B,T", [(20, 100), (300, 1000), (500, 5000), (600, 12000)])
+def test_lengths_or_pool_alone_in_place(B, T, which):
+    table, lens, new, ring, pool = state(B, 12, 4, B)
+    want = ref.extend(table, lens, new, ring, pool, 4, T)
+    t, ln, nw, rg, pl = (ints(x) for x in (table, lens, new, ring, pool))
+    out = fq.paged_extend(t, ln, nw, rg, pl, 4, T, **{which: ln if which == "seq_lens_out" else pl})
+    for k, v in zip(("slots", "positions", "starts", "seq_lens", "pool"), out):
+        assert v.tolist() == want[k], k
+    assert t.tolist() == want["table"] and rg.tolist() == want["ring"]
+    assert (pl if which == "seq_lens_out" else ln).tolist() == (pool if which == "seq_lens_out" else lens)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("B,T", [(300, 700), (500, 5000), (600, 12000)])
+def test_steps_of_many_blocks_captured(B, T, in_place):
+    """Replayed with other lengths to add: as the same steps one by one."""
+    page = 4
+    table, lens, new, ring, pool = state(B, 12, page, B)
+    t, ln, nw, rg, pl = (ints(x) for x in (table, lens, new, ring, pool))
+    given = dict(seq_lens_out=ln, pool_out=pl) if in_place else {}
+    call = lambda: fq.paged_extend(t, ln, nw, rg, pl, page, T, **given)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    for x, y in ((t, table), (ln, lens), (rg, ring), (pl, pool)):
+        x.copy_(ints(y))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    r = random.Random(T)
+    for _ in range(3):
+        graph.replay()
+        want = ref.extend(table, lens, new, ring, pool, page, T)
+        for k, v in zip(("slots", "positions", "starts", "seq_lens", "pool"), out):
+            assert v.tolist() == want[k], k
+        assert t.tolist() == want["table"] and rg.tolist() == want["ring"]
+        table, ring = want["table"], want["ring"]
+        if in_place:
+            lens, pool = want["seq_lens"], want["pool"]
+        else:
+            ln.copy_(ints(want["seq_lens"]))
+            pl.copy_(ints(want["pool"]))
+            lens, pool = want["seq_lens"], want["pool"]
+        new = [-1 if r.random() < 0.2 else r.choice([0, 1, 5]) for _ in range(B)]
+        nw.copy_(ints(new))
