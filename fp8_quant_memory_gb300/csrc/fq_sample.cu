@@ -17,11 +17,12 @@
 // over the keys from the largest down to where weights are 0, filled while the largest is still being looked for: that of the
 // first 8192 tells where the bins have to lie, but for rows whose largest is far above it, which take a second pass.
 //
-// What bounds it. 256 x 151936 bf16, a third of the rows whole: 43 us, the bytes 11.5. A whole row takes an SM 22 us, 28 with
+// What bounds it. 256 x 151936 bf16, a third of the rows whole: 41 us, the bytes 11.5. A whole row takes an SM 22 us, 28 with
 // all SMs reading (its bytes at an SM's share of the memory: 6.7): 12 us the bins (22 thousand clocks for 4.8 thousand
 // warp-wide additions: banks that 32 lanes meet at random, 3.7 clocks each by the conflict counter, a plain store is no
-// faster), 5 us sums and searches, 3 us the token's place. Other rows take 8 to 12 us. 1 x 32000, top-k 50 and top-p: 6.7 us,
-// 2.5 of them launch and first loads.
+// faster), 5 us sums and searches, 3 us the token's place: phases that hand over at the block's barriers, where warps wait most
+// of all (8.6 to an issue slot, 2.4 for shared memory; 31% of the slots issue). Other rows take 8 to 12 us, of the memory's
+// latency and barriers. 1 x 32000, top-k 50 and top-p: 6.7 us, 2.5 of them launch and first loads.
 //
 // Tried and left: the largest first, then the bins (256 x 151936 whole: 70 us against 59; rows of few tokens 0.5 us less, whose
 // loads need not wait for the row's settings); the largest of 32768 instead of 8192, kept in registers (63 us); a cluster of
