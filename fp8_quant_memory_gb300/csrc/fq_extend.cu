@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
       for (int i = 0; i < kOwn; ++i) count += __popc(__ballot_sync(0xffffffffu, id[i] >= 0));
     }
     if (lane == 0) present[warp] = count;
+    __syncwarp();
     if constexpr (kSmallStep) asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
     else __syncthreads();
     const uint32_t its = lane < kWarps ? present[lane] : 0u;
@@ -302,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
       cluster_wait();
       if (warp == 0 && lane < team)
         asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(in_cta(&present_in[rank], lane)), "r"(total) : "memory");
+      __syncwarp();
       cluster_barrier();  // in place, too: every CTA has read the lengths and the pool
       const uint32_t of = lane < team ? present_in[lane] : 0u;
       spot += __reduce_add_sync(0xffffffffu, lane < rank ? of : 0u);
@@ -319,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_kernel(const ExtendArgs a)
       }
     }
   } else if (!kSmallStep && team > 1 && returns) {
+    __syncwarp();  // whole warps, which the loops above have split
     cluster_wait();
     if (a.in_place != 0) cluster_barrier();
   }
@@ -366,7 +369,7 @@ bool launch_extend(const ExtendArgs& given, cudaStream_t s) {
   } else {
     a.team = kTeam;
     const int64_t most = sm_count() / kTeam * kTeam - kTeam, whole = (want + kTeam - 1) / kTeam * kTeam;
-    a.workers = static_cast<int32_t>(whole < kTeam ? kTeam : whole < most ? whole : most);
+    a.workers = static_cast<int32_t>(whole < kTeam || most < kTeam ? kTeam : whole < most ? whole : most);
   }
   const int64_t ctas = a.in_place != 0 ? a.team : a.team + a.workers;
   return want > a.workers ? launch<1024, 8, false>(a, ctas, s) : launch<1024, 1, false>(a, ctas, s);
